@@ -1,0 +1,115 @@
+"""Binding of libarcserve.so (include/serve/): loading, error codes, structs.
+
+The operators of a decode step before the sampler live in kv_cache.py and
+w4.py; every step of them runs in the library's CUDA kernels.  There is no
+fallback: if the library is not built, `load()` raises.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+from . import sampler
+from .workloads import DTYPE_BF16, DTYPE_F16, DTYPE_F32
+
+LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libarcserve.so")
+
+P, I32, I64, SIZE = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+
+
+class KvCache(ctypes.Structure):
+    """arc_kv_cache, 64 bytes."""
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("page_stride", I64), ("head_stride", I64),
+                ("pages", I32), ("heads", I32), ("page_size", I32), ("head_dim", I32)]
+
+
+class KvStep(ctypes.Structure):
+    """arc_kv_step, 56 bytes."""
+    _fields_ = [("page_table", P), ("table_stride", I64), ("positions", P), ("row_offsets", P), ("B", I64), ("T", I64),
+                ("max_pages", I32), ("reserved", I32)]
+
+
+class RopeArgs(ctypes.Structure):
+    """arc_rope, 24 bytes."""
+    _fields_ = [("turns", P), ("amplitude", ctypes.c_float), ("rot_dim", I32), ("layout", I32), ("reserved", I32)]
+
+
+class KvRows(ctypes.Structure):
+    """arc_kv_rows, 104 bytes."""
+    _fields_ = [("q", P), ("k", P), ("v", P), ("q_out", P), ("q_token_stride", I64), ("q_head_stride", I64),
+                ("k_token_stride", I64), ("k_head_stride", I64), ("v_token_stride", I64), ("v_head_stride", I64),
+                ("out_token_stride", I64), ("out_head_stride", I64), ("q_heads", I32), ("dtype", I32)]
+
+
+class KvQuery(ctypes.Structure):
+    """arc_kv_query, 64 bytes."""
+    _fields_ = [("q", P), ("out", P), ("q_token_stride", I64), ("q_head_stride", I64), ("out_token_stride", I64),
+                ("out_head_stride", I64), ("q_heads", I32), ("dtype", I32), ("scale", ctypes.c_float), ("window", I32)]
+
+
+class W4Weight(ctypes.Structure):
+    """arc_w4_weight, 48 bytes."""
+    _fields_ = [("q", P), ("scales", P), ("zeros", P), ("row_bytes", I64), ("outs", I64), ("ins", I32), ("group", I32)]
+
+
+# exported symbol -> (restype, argtypes)
+SIGNATURES = {
+    "arc_kv_append": (ctypes.c_int, [P, P, P, P, P, P]),
+    "arc_kv_attend": (ctypes.c_int, [P, P, P, P, P, SIZE, P]),
+    "arc_kv_attend_workspace_bytes": (SIZE, [P]),
+    "arc_w4_matvec": (ctypes.c_int, [P, P, I64, I64, I32, P, I64, I32, P, SIZE, P]),
+    "arc_w4_workspace_bytes": (SIZE, [P, I64]),
+    "arc_serve_strerror": (ctypes.c_char_p, [ctypes.c_int]),
+    "arc_serve_abi_version": (ctypes.c_int, []),
+}
+
+_lib = None
+
+
+def load():
+    """Load libarcserve.so (raises if it has not been built)."""
+    global _lib
+    if _lib is None:
+        if not os.path.exists(LIB_PATH):
+            raise RuntimeError(
+                f"{LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'` "
+                "(there is no CPU fallback)")
+        lib = ctypes.CDLL(LIB_PATH)
+        for name, (res, args) in SIGNATURES.items():
+            fn = getattr(lib, name)
+            fn.restype = res
+            fn.argtypes = args
+        _lib = lib
+    return _lib
+
+
+class ServeError(sampler.ArcError):
+    """A call of libarcserve refused its arguments or could not launch."""
+
+    def __init__(self, rc: int):
+        RuntimeError.__init__(self, f"arc_serve error {rc}: {load().arc_serve_strerror(rc).decode()}")
+        self.rc = rc
+
+
+def dtype_code(t, f32: bool = False) -> int:
+    """ARC_* code of a tensor's type: bfloat16 or float16 (or float32 where allowed)."""
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float16:
+        return DTYPE_F16
+    if f32 and t.dtype == torch.float32:
+        return DTYPE_F32
+    raise TypeError(f"must be bfloat16 or float16{' or float32' if f32 else ''}, not {t.dtype}")
+
+
+def want(ok: bool, text: str) -> None:
+    if not ok:
+        raise ValueError(text)
+
+
+def finish(rc: int, check: bool) -> int:
+    if check and rc != sampler.ARC_OK:
+        raise ServeError(rc)
+    return rc
