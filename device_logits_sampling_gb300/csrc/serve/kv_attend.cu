@@ -1,118 +1,794 @@
 // arc_kv_attend: attention of a step's new tokens over the paged 8-bit cache.
+//
+// Work.  An item is (sequence, tile of up to R query rows, cached head); the
+// rows of an item are the new tokens' query heads that share the cached head.
+// An item is a run of steps of 16 cached tokens.  All items' steps lie one
+// after another on a line (their counts come from the lengths in device
+// memory), the line is cut into equal pieces, one for each warp of the grid,
+// so that ragged lengths, one long sequence and many short ones all fill the
+// GPU alike.  A piece that begins or ends inside an item leaves a partial
+// (maximum, sum, output); the block joins its warps' partials in shared memory
+// and, where an item spans blocks, the last block to arrive joins the blocks'
+// in the order of the line, so results do not depend on timing.
+//
+// A step.  Each warp streams its steps through its own ring of shared-memory
+// stages with asynchronous 16-byte copies; no block barrier is met on the way.
+// S^T = K Q^T and O^T = V^T P^T run on fp16 matrix instructions: 16 tokens (or
+// 16 values of the head) are the long side of a tile and the R = 8 or 16 query
+// rows the short one, so that one token's grouped heads waste little.  The
+// order of head values inside the products is free: a lane takes the bytes
+// that one 16-byte shared load gives it, and the query is laid out to match;
+// e4m3 codes become fp16 pairs by one conversion each, and the two scales
+// enter outside the products.
+//
+// Softmax.  Value scales differ from page to page.  With the value scale
+// 2^ev * vm, the running maximum is that of s + ev (log2 units): weights
+// p' = 2^(s + ev - m) are at most 1 and small only where their product with
+// the values is, so their fp16 form loses nothing that counts; the sum of the
+// true weights is sum p' 2^-ev, in the same reference.
+#include <atomic>
+
 #include "kv_host.cuh"
+#include "launch_util.cuh"
 #include "serve_util.cuh"
 
 namespace {
 
 using namespace arcs;
 
-constexpr int kThreads = 256;
+constexpr int kMaxBlocks = 256;  // blocks of a launch: at most one for each SM
+constexpr int kItemCost = 1;     // an item's fixed cost in steps (query load, output store), for the cut
+constexpr int kStatusBytes = kMaxBlocks * 4;
 
 struct AttendArgs {
     arc_kv_cache c;
     arc_kv_step s;
     arc_kv_query q;
     uint32_t* err;
+    uint32_t* arrived;  // one counter a block, 0 between calls
+    float* partial;     // two slots a block
+    int32_t group;      // query heads for each cached one
+    int32_t bf16;
+    int32_t vec;        // bit 0: q, 1: out allow 16-byte accesses
 };
 
-// One warp for each (token, query head): the running maximum, sum and output
-// of its softmax over the tokens in turn, head_dim / 32 values a lane.
-template <int DT, int D>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
-    constexpr int V = D / 32;
-    using T = typename Half<DT>::T;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    if (w >= a.s.T * a.q.q_heads) return;
-    const int hq = static_cast<int>(w % a.q.q_heads);
-    const int64_t t = w / a.q.q_heads;
-    const int h = hq / (a.q.q_heads / a.c.heads);
-    int64_t b = t, first = t;
-    bool bad = false;
-    if (a.s.row_offsets != nullptr) {
-        int64_t lo = 0, hi = a.s.B - 1;
-        while (lo < hi) {
-            const int64_t m = (lo + hi + 1) >> 1;
-            if (__ldg(a.s.row_offsets + m) <= t)
-                lo = m;
-            else
-                hi = m - 1;
-        }
-        b = lo;
-        first = __ldg(a.s.row_offsets + b);
-        const int64_t end = __ldg(a.s.row_offsets + b + 1);
-        if (first < 0 || first > t || end <= t || end > a.s.T || (b > 0 && __ldg(a.s.row_offsets + b - 1) > first)) {
-            if (a.err && lane == 0) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
-            return;
-        }
-    }
-    const int64_t held = __ldg(a.s.positions + b);
-    const int64_t pos = held + (t - first);
-    T* out = static_cast<T*>(a.q.out) + t * a.q.out_token_stride + hq * a.q.out_head_stride + lane * V;
-    float o[V], q[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    if (held >= 0) {
-        const T* qp = static_cast<const T*>(a.q.q) + t * a.q.q_token_stride + hq * a.q.q_head_stride + lane * V;
-#pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = Half<DT>::to_float(qp[i]) * (a.q.scale * 1.4426950408889634f);
-        const int64_t from = a.q.window > 0 && pos + 1 > a.q.window ? pos + 1 - a.q.window : 0;
-        if (pos >= int64_t{a.s.max_pages} * a.c.page_size) {
-            bad = true;
-            if (a.err && lane == 0) atomicOr(a.err, ARC_KV_ERR_POSITION);
-        }
-        for (int64_t j = from; j <= pos && !bad; ++j) {
-            const int64_t pi = j / a.c.page_size;
-            const int page = __ldg(a.s.page_table + b * a.s.table_stride + pi);
-            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.c.pages)) {
-                bad = true;
-                if (a.err && lane == 0) atomicOr(a.err, ARC_KV_ERR_PAGE);
-                break;
-            }
-            const int64_t at = page * a.c.page_stride + h * a.c.head_stride + (j - pi * a.c.page_size) * D + lane * V;
-            const uint8_t* kp = static_cast<const uint8_t*>(a.c.k) + at;
-            const uint8_t* vp = static_cast<const uint8_t*>(a.c.v) + at;
-            const int64_t si = static_cast<int64_t>(page) * a.c.heads + h;
-            float s = 0.0f, v[V];
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-                const uint32_t kw = e4m3x2_to_half2(kp[i] | (kp[i + 1] << 8));
-                const uint32_t vw = e4m3x2_to_half2(vp[i] | (vp[i + 1] << 8));
-                const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kw));
-                const float2 vf = __half22float2(*reinterpret_cast<const __half2*>(&vw));
-                s = fmaf(q[i], kf.x, fmaf(q[i + 1], kf.y, s));
-                v[i] = vf.x;
-                v[i + 1] = vf.y;
-            }
-            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-            s *= a.c.k_scale[si];
-            const float vs = a.c.v_scale[si];
-            const float mn = fmaxf(m, s);
-            const float keep = m == -INFINITY ? 0.0f : exp2f(m - mn), p = exp2f(s - mn);
-            l = l * keep + p;
-#pragma unroll
-            for (int i = 0; i < V; ++i) o[i] = fmaf(o[i], keep, p * vs * v[i]);
-            m = mn;
-        }
-    }
-    const float inv = bad ? __int_as_float(0x7FC00000) : (l > 0.0f || l != l ? 1.0f / l : 0.0f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = Half<DT>::from_float(o[i] * inv);
+// Warps of a block and stages of a warp's ring, for one block an SM.
+template <int D, int NT>
+struct Shape;
+template <>
+struct Shape<64, 1> {
+    static constexpr int kWarps = 16, kStages = 4;
+};
+template <>
+struct Shape<64, 2> {
+    static constexpr int kWarps = 16, kStages = 4;
+};
+template <>
+struct Shape<128, 1> {
+    static constexpr int kWarps = 12, kStages = 3;
+};
+template <>
+struct Shape<128, 2> {
+    static constexpr int kWarps = 10, kStages = 3;
+};
+template <>
+struct Shape<256, 1> {
+    static constexpr int kWarps = 6, kStages = 3;
+};
+
+struct Part {        // a partial's item
+    int64_t from, to;  // the item's units on the line
+    int64_t first;     // its sequence's first row
+    int32_t rows;      // query rows of its sequence and head (tokens * group)
+    int32_t row0;      // first row of its tile
+    int32_t head;
+};
+
+template <int D, int NT>
+struct Smem {
+    static constexpr int kW = Shape<D, NT>::kWarps, kS = Shape<D, NT>::kStages, kR = 8 * NT;
+    static constexpr int kStage = 32 * D;  // 16 keys and 16 values
+    static constexpr int kRing = kS * kStage, kHead = kR * D * 4;
+    static constexpr int kPerWarp = kRing + kHead;
+    static constexpr int kThreads = kW * 32;
+    static_assert(kRing >= kHead, "the last partial goes where the ring was");
+    float scales[kW][kS][2];
+    float m[2 * kW][kR], l[2 * kW][kR];
+    Part part[2 * kW];
+    int64_t before[kThreads + 1];
+    int64_t wsum[kW];
+    uint32_t last;
+    static constexpr int kBytes = kW * kPerWarp;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t p) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
+    return v;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int DT>
-int launch(const AttendArgs& a, cudaStream_t st) {
-    const int64_t warps = a.s.T * a.q.q_heads;
-    const int64_t grid = (warps * 32 + kThreads - 1) / kThreads;
-    if (grid > INT_MAX) return ARC_E_SHAPE;
-    const unsigned g = static_cast<unsigned>(grid);
-    if (a.c.head_dim == 64)
-        attend_kernel<DT, 64><<<g, kThreads, 0, st>>>(a);
-    else if (a.c.head_dim == 128)
-        attend_kernel<DT, 128><<<g, kThreads, 0, st>>>(a);
+// Byte offset of 16-byte chunk `c` of token row `r` in a stage's half: the
+// chunks of each 128-byte line are permuted so that the lanes of a fragment
+// load, which read one chunk of 2 to 8 rows, meet in no bank.
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+    const int lin = r * (D / 16) + c, line = lin >> 3;
+    int f;
+    if constexpr (D == 64)
+        f = 2 * (line & 3);
+    else if constexpr (D == 128)
+        f = line & 7;
     else
-        attend_kernel<DT, 256><<<g, kThreads, 0, st>>>(a);
+        f = (line & 3) ^ ((line >> 2) & 1) ^ (((line >> 3) & 1) << 2);
+    return (line * 8 + ((lin & 7) ^ f)) * 16;
+}
+
+// A sequence of the step: its rows, and its steps on the line.
+struct Seq {
+    int64_t first;   // first row
+    int32_t pos, n;  // tokens held before, new tokens
+    int32_t step0;   // first step that any row sees
+    int32_t cost;    // units of an item: steps + kItemCost; 0: nothing to do
+    int32_t tiles;   // of R rows
+    bool bad, late;  // offsets are wrong; past the page table
+};
+
+template <int R>
+__device__ __forceinline__ Seq load_seq(const AttendArgs& a, int64_t b) {
+    Seq q;
+    q.bad = q.late = false;
+    q.cost = 0;
+    q.tiles = 0;
+    q.step0 = 0;
+    q.pos = __ldg(a.s.positions + b);
+    int64_t n = 1;
+    q.first = b;
+    if (a.s.row_offsets != nullptr) {
+        const int64_t lo = __ldg(a.s.row_offsets + b), hi = __ldg(a.s.row_offsets + b + 1);
+        q.first = lo;
+        n = hi - lo;
+        if (lo < 0 || hi < lo || hi > a.s.T || (b == 0 && lo != 0) || (b == a.s.B - 1 && hi != a.s.T)) {
+            q.bad = true;
+            n = 0;
+        }
+    }
+    q.n = static_cast<int32_t>(n);
+    if (n == 0 || q.pos < 0) return q;
+    if (q.pos + n > int64_t{a.s.max_pages} * a.c.page_size) {
+        q.late = true;
+        return q;
+    }
+    const int end = q.pos + q.n;
+    q.step0 = a.q.window > 0 && q.pos + 1 > a.q.window ? (q.pos + 1 - a.q.window) >> 4 : 0;
+    q.cost = ((end + 15) >> 4) - q.step0 + kItemCost;
+    q.tiles = static_cast<int32_t>((n * a.group + R - 1) / R);
+    return q;
+}
+
+__device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Seq& q) {
+    return int64_t{q.tiles} * a.c.heads * q.cost;
+}
+
+// A place on the line: an item, and a unit of it.
+template <int R>
+struct Cursor {
+    Seq q;
+    int64_t b;
+    int64_t left;  // units of the warp's piece from here on
+    int32_t tile, head, unit;
+
+    // The line promises one while `left` is positive; should the lengths change
+    // under the call, the piece ends at the last sequence.
+    __device__ __forceinline__ void next_item(const AttendArgs& a) {
+        unit = 0;
+        if (++head < a.c.heads) return;
+        head = 0;
+        if (++tile < q.tiles) return;
+        tile = 0;
+        do {
+            if (++b >= a.s.B) {
+                left = 0;
+                return;
+            }
+            q = load_seq<R>(a, b);
+        } while (q.cost == 0);
+    }
+    // to the next unit that is a step; false at the end of the piece
+    __device__ __forceinline__ bool to_step(const AttendArgs& a) {
+        while (left > 0) {
+            if (unit == q.cost) {
+                next_item(a);
+            } else if (unit < kItemCost) {
+                ++unit;
+                --left;
+            } else {
+                return true;
+            }
+        }
+        return false;
+    }
+    __device__ __forceinline__ int step() const { return q.step0 + unit - kItemCost; }
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
+    using S = Smem<D, NT>;
+    constexpr int R = S::kR, W = S::kW, ST = S::kS, kThreads = S::kThreads;
+    constexpr int KS = D / 16;   // 16-value slices of a head
+    constexpr int KC = D / 64;   // 16-byte chunks of a key that a lane takes
+    constexpr int LB = D / 8;    // values of a head that a lane holds of the output
+    extern __shared__ __align__(128) uint8_t dyn[];
+    __shared__ S sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    // ---- the line: units before each thread's run of sequences
+    const int64_t run = (a.s.B + kThreads - 1) / kThreads;
+    int64_t mine = 0;
+    uint32_t seen = 0;
+    for (int64_t b = run * tid; b < run * (tid + 1) && b < a.s.B; ++b) {
+        const Seq q = load_seq<R>(a, b);
+        mine += units_of(a, q);
+        if (q.bad) seen |= ARC_KV_ERR_OFFSETS;
+        if (q.late) seen |= ARC_KV_ERR_POSITION;
+    }
+    if (seen && a.err && blockIdx.x == 0) atomicOr(a.err, seen);
+    int64_t incl = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+        if (lane >= m) incl += o;
+    }
+    if (lane == 31) sm.wsum[warp] = incl;
+    if (tid < 2 * W) sm.part[tid].from = -1;
+    __syncthreads();
+    int64_t off = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const int64_t s = sm.wsum[w];
+        if (w < warp) off += s;
+        total += s;
+    }
+    sm.before[tid] = off + incl - mine;
+    if (tid == 0) sm.before[kThreads] = total;
+
+    // rows without work: parked sequences give 0, those past their page table NaN
+    for (int64_t b = blockIdx.x; b < a.s.B; b += gridDim.x) {
+        const Seq q = load_seq<R>(a, b);
+        if (q.cost != 0 || q.n == 0) continue;
+        const uint32_t fill = q.late ? (a.bf16 ? 0x7FC0u : 0x7E00u) : 0u;
+        const int64_t vals = int64_t{q.n} * a.q.q_heads * D;
+        for (int64_t i = tid; i < vals; i += kThreads) {
+            const int64_t th = i / D;
+            static_cast<uint16_t*>(a.q.out)[(q.first + th / a.q.q_heads) * a.q.out_token_stride +
+                                            (th % a.q.q_heads) * a.q.out_head_stride + i % D] = static_cast<uint16_t>(fill);
+        }
+    }
+    __syncthreads();
+    if (total == 0) return;
+
+    // ---- this block's and this warp's piece; short lines take fewer blocks
+    const int64_t want = (total + W - 1) / W;
+    const int64_t blocks = want < gridDim.x ? want : gridDim.x;
+    if (blockIdx.x >= blocks) return;
+    const int64_t pieces = blocks * W, piece = static_cast<int64_t>(blockIdx.x) * W + warp;
+    // floor(total * i / of), without the product
+    auto cut = [total](int64_t i, int64_t of) { return total / of * i + total % of * i / of; };
+    const int64_t from = cut(piece, pieces), to = cut(piece + 1, pieces);
+    const int64_t block_from = cut(blockIdx.x, blocks), block_to = cut(blockIdx.x + 1, blocks);
+
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * S::kPerWarp;
+    float* const head_store = reinterpret_cast<float*>(dyn + warp * S::kPerWarp + S::kRing);
+    float* const tail_store = reinterpret_cast<float*>(dyn + warp * S::kPerWarp);
+
+    if (from < to) {
+        Cursor<R> at;  // of the arithmetic; `ahead` of the copies
+        {
+            int lo = 0, hi = kThreads;  // the run of sequences that holds `from`
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sm.before[mid] <= from)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            int64_t rest = from - sm.before[lo];
+            at.b = run * lo;
+            at.q = load_seq<R>(a, at.b);
+            while (rest >= units_of(a, at.q) && at.b + 1 < a.s.B) {
+                rest -= units_of(a, at.q);
+                at.q = load_seq<R>(a, ++at.b);
+            }
+            const int64_t item = at.q.cost > 0 ? rest / at.q.cost : 0;
+            at.unit = static_cast<int32_t>(rest - item * at.q.cost);
+            at.tile = static_cast<int32_t>(item / a.c.heads);
+            at.head = static_cast<int32_t>(item - int64_t{at.tile} * a.c.heads);
+            at.left = at.q.cost > 0 ? to - from : 0;
+        }
+        Cursor<R> ahead = at;
+
+        // ---- copies
+        const int ps_shift = 31 - __clz(a.c.page_size);
+        int issued = 0;           // stage of the next copy
+        int page = -1, page_of = -1, page_next = -1;  // current page id, its index, the id after it
+        int64_t page_seq = -1;
+        auto issue = [&]() {
+            if (ahead.to_step(a)) {
+                const int tok0 = ahead.step() << 4, pi = tok0 >> ps_shift;
+                const int32_t* table = a.s.page_table + ahead.b * a.s.table_stride;
+                if (ahead.b != page_seq || pi != page_of) {
+                    page = ahead.b == page_seq && pi == page_of + 1 ? page_next : __ldg(table + pi);
+                    page_seq = ahead.b;
+                    page_of = pi;
+                    const int more = pi + 1 < a.s.max_pages ? pi + 1 : pi;
+                    page_next = __ldg(table + more);
+                }
+                const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+                const int id = ok ? page : 0;
+                // tokens that no row of the tile sees are filled with zeros
+                const int row0 = ahead.tile * R, rows = ahead.q.n * a.group;
+                const int last = ahead.q.pos + ((row0 + R < rows ? row0 + R : rows) - 1) / a.group;
+                const int first = a.q.window > 0 ? ahead.q.pos + row0 / a.group - a.q.window + 1 : 0;
+                const int64_t base = id * a.c.page_stride + ahead.head * a.c.head_stride +
+                                     int64_t{tok0 - (pi << ps_shift)} * D;
+                const uint32_t dst = ring + issued * S::kStage;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int c = lane + 32 * i, r = c / (D / 16), cc = c % (D / 16);
+                    const bool on = ok && tok0 + r <= last && tok0 + r >= first;
+                    copy16(dst + chunk_at<D>(r, cc), static_cast<const char*>(a.c.k) + base + c * 16, on);
+                    copy16(dst + 16 * D + chunk_at<D>(r, cc), static_cast<const char*>(a.c.v) + base + c * 16, on);
+                }
+                const int64_t si = static_cast<int64_t>(id) * a.c.heads + ahead.head;
+                if (ok) {
+                    if (lane < 2)
+                        copy4(static_cast<uint32_t>(__cvta_generic_to_shared(&sm.scales[warp][issued][lane])),
+                              (lane ? a.c.v_scale : a.c.k_scale) + si);
+                } else {
+                    if (lane < 2) sm.scales[warp][issued][lane] = __int_as_float(0x7FC00000);
+                    if (lane == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
+                }
+                ++ahead.unit;
+                --ahead.left;
+            }
+            copies_end();
+            issued = issued + 1 == ST ? 0 : issued + 1;
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) issue();
+
+        // ---- the piece, item by item
+        int stage = 0;
+        int64_t here = from;  // unit of the line
+        while (at.left > 0) {
+            if (at.unit == at.q.cost) at.next_item(a);
+            if (at.left <= 0) break;
+            const int64_t item_from = here - at.unit;
+            const int32_t unit0 = at.unit;
+            const int32_t unit1 = at.q.cost - unit0 < at.left ? at.q.cost : unit0 + static_cast<int32_t>(at.left);
+            const int row0 = at.tile * R, rows = at.q.n * a.group;
+
+            // queries: fp16, each row scaled by a power of two to [2^14, 2^15)
+            uint32_t qf[NT][KS][2];
+            float rf[NT][2];
+            int hi[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float x[D / 4];
+                const int r = row0 + 8 * nt + g;
+                const int tok = (r < rows ? r : rows - 1) / a.group;
+                if (r < rows) {
+                    const char* p = static_cast<const char*>(a.q.q) +
+                                    ((at.q.first + tok) * a.q.q_token_stride +
+                                     (at.head * a.group + r - tok * a.group) * a.q.q_head_stride + t * (D / 4)) * 2;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        float e[8];
+                        if (a.bf16)
+                            load8<ARC_BF16>(p + 16 * i, a.vec & 1, e);
+                        else
+                            load8<ARC_F16>(p + 16 * i, a.vec & 1, e);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[8 * i + k] = e[k];
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 4; ++k) x[k] = 0.0f;
+                }
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < D / 4; ++k) top = fmaxf(top, fabsf(x[k]));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                // 2^(14 - exponent), kept inside fp32's normal range
+                const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+                const int up = top == 0.0f ? 0 : (14 - ex > 126 ? 126 : (14 - ex < -113 ? -113 : 14 - ex));
+                const float f = exp2i(up);
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                    qf[nt][j][0] = pack_f16(x[4 * j] * f, x[4 * j + 1] * f);
+                    qf[nt][j][1] = pack_f16(x[4 * j + 2] * f, x[4 * j + 3] * f);
+                }
+                const float back = exp2i(-up) * (a.q.scale * 1.4426950408889634f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    rf[nt][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + e) * 4);
+                    const int rr = row0 + 8 * nt + 2 * t + e;
+                    hi[nt][e] = at.q.pos + (rr < rows ? rr : rows - 1) / a.group;
+                }
+            }
+            const int hi_first = at.q.pos + row0 / a.group;
+            const int hi_last = at.q.pos + ((row0 + R < rows ? row0 + R : rows) - 1) / a.group;
+
+            float o[NT][KS][4], m[NT][2], l[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int i = 0; i < KS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
+                m[nt][0] = m[nt][1] = -INFINITY;
+                l[nt][0] = l[nt][1] = 0.0f;
+            }
+
+            for (int u = unit0 < kItemCost ? kItemCost : unit0; u < unit1; ++u) {
+                copies_wait<ST - 2>();
+                __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
+                issue();
+                const uint32_t kst = ring + stage * S::kStage, vst = kst + 16 * D;
+                const float ks = sm.scales[warp][stage][0];
+                const uint32_t vb = __float_as_uint(sm.scales[warp][stage][1]);
+                stage = stage + 1 == ST ? 0 : stage + 1;
+                const int tok0 = (at.q.step0 + u - kItemCost) << 4;
+
+                float s[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < KC; ++i) {
+                    const uint4 k0 = lds16(kst + chunk_at<D>(g, KC * t + i));
+                    const uint4 k1 = lds16(kst + chunk_at<D>(g + 8, KC * t + i));
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t a0 = e4m3x2_to_half2(w0[w]), a2 = e4m3x2_to_half2(w0[w] >> 16);
+                        const uint32_t a1 = e4m3x2_to_half2(w1[w]), a3 = e4m3x2_to_half2(w1[w] >> 16);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
+                    }
+                }
+                const float ev = static_cast<float>(static_cast<int>((vb >> 23) & 0xFF) - 127);
+                const float vm = __uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u);
+                const float vi = __uint_as_float((254u - ((vb >> 23) & 0xFF)) << 23);
+                const bool edge = tok0 + 15 > hi_first || (a.q.window > 0 && tok0 <= hi_last - a.q.window);
+                float top[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[nt][e] = fmaf(s[nt][e], ks * rf[nt][e & 1], ev);
+                        if (edge) {
+                            const int tok = tok0 + g + (e >> 1) * 8, h = hi[nt][e & 1];
+                            if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) s[nt][e] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(s[nt][e], s[nt][e + 2]);
+                }
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[nt][e], x));
+                bool up = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) up = up || top[nt][e] > m[nt][e];
+                if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float mn = fmaxf(m[nt][e], top[nt][e]);
+                            f[e] = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - mn);
+                            m[nt][e] = mn;
+                            l[nt][e] *= f[e];
+                        }
+#pragma unroll
+                        for (int i = 0; i < KS; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[nt][i][e] *= f[e & 1];
+                    }
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
+                        p[e] = ex2(s[nt][e] - ref);
+                        l[nt][e & 1] = fmaf(p[e], vi, l[nt][e & 1]);
+                    }
+                    // token-major to row-major: what the products take
+                    pf[nt][0] = transpose8x8(pack_f16(p[0] * vm, p[1] * vm));
+                    pf[nt][1] = transpose8x8(pack_f16(p[2] * vm, p[3] * vm));
+                }
+
+                // values: tokens 2t, 2t+1, 2t+8, 2t+9, D / 8 bytes from g * D / 8
+                uint32_t v[4][LB / 4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+                    if constexpr (D == 64) {
+                        const uint2 x = lds8(vst + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
+                        v[i][0] = x.x;
+                        v[i][1] = x.y;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < D / 128; ++c) {
+                            const uint4 x = lds16(vst + chunk_at<D>(r, (D / 128) * g + c));
+                            v[i][4 * c] = x.x;
+                            v[i][4 * c + 1] = x.y;
+                            v[i][4 * c + 2] = x.z;
+                            v[i][4 * c + 3] = x.w;
+                        }
+                    }
+                }
+                if (edge && hi_first != hi_last) {
+                    // a token that some rows see and others do not: its NaN values must not
+                    // reach the others through 0 * NaN
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int w = 0; w < LB / 4; ++w) any |= ((v[i][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    if (__any_sync(0xFFFFFFFFu, any != 0)) {
+                        for (int r = 0; r < R; ++r) {
+                            const int rr = row0 + r, h = at.q.pos + (rr < rows ? rr : rows - 1) / a.group;
+                            uint32_t hit = 0;  // values of this lane's that are NaN in a token row r sees
+                            for (int i = 0; i < 4; ++i) {
+                                const int tok = tok0 + 2 * t + (i & 1) + (i >> 1) * 8;
+                                if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) continue;
+#pragma unroll
+                                for (int k = 0; k < LB; ++k)
+                                    if (((v[i][k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) hit |= 1u << k;
+                            }
+                            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
+                            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (8 * nt + 2 * t + e == r)
+#pragma unroll
+                                        for (int k = 0; k < LB; ++k)
+                                            if ((hit >> k) & 1) o[nt][k >> 1][2 * (k & 1) + e] = __int_as_float(0x7FC00000);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int w = 0; w < LB / 4; ++w) {
+                                const uint32_t bad = ((v[i][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                v[i][w] &= ~((bad >> 7) * 0xFFu);
+                            }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    const int w = i >> 1;
+                    const uint32_t x = __byte_perm(v[0][w], v[1][w], (i & 1) ? 0x7362 : 0x5140);
+                    const uint32_t y = __byte_perm(v[2][w], v[3][w], (i & 1) ? 0x7362 : 0x5140);
+                    const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
+                    const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                }
+            }
+
+            // ---- the part is done: lanes' sums, then the output or a partial
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) l[nt][e] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][e], x);
+            const int32_t units = unit1 - unit0;
+            at.unit = unit1;
+            at.left -= units;
+            here += units;
+            if (units == at.q.cost) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int rr = row0 + 8 * nt + 2 * t + e;
+                        if (rr >= rows) continue;
+                        const int tok = rr / a.group;
+                        const float inv = 1.0f / l[nt][e];
+                        char* p = static_cast<char*>(a.q.out) +
+                                  ((at.q.first + tok) * a.q.out_token_stride +
+                                   (at.head * a.group + rr - tok * a.group) * a.q.out_head_stride + g * LB) * 2;
+#pragma unroll
+                        for (int c = 0; c < LB / 8; ++c) {
+                            float x[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[k] = o[nt][4 * c + (k >> 1)][2 * (k & 1) + e] * inv;
+                            if (a.bf16)
+                                store8<ARC_BF16>(p + 16 * c, a.vec & 2, x);
+                            else
+                                store8<ARC_F16>(p + 16 * c, a.vec & 2, x);
+                        }
+                    }
+            } else {
+                // the piece's first item goes to its own store (the ring is in use), the last one over the ring
+                const bool tail = at.left == 0;
+                const int slot = 2 * warp + (tail ? 1 : 0);
+                float* store = tail ? tail_store : head_store;
+                if (tail) {
+                    copies_wait<0>();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * nt + 2 * t + e;
+                        float* p = store + r * D + g * LB;
+#pragma unroll
+                        for (int c = 0; c < LB / 4; ++c)
+                            *reinterpret_cast<float4*>(p + 4 * c) =
+                                make_float4(o[nt][2 * c][e], o[nt][2 * c][2 + e], o[nt][2 * c + 1][e], o[nt][2 * c + 1][2 + e]);
+                        if (g == 0) {
+                            sm.m[slot][r] = m[nt][e];
+                            sm.l[slot][r] = l[nt][e];
+                        }
+                    }
+                if (lane == 0)
+                    sm.part[slot] = Part{item_from, item_from + at.q.cost, at.q.first, rows, row0, at.head};
+            }
+        }
+        copies_wait<0>();
+    }
+    __syncthreads();
+
+    // ---- join the block's partials: neighbours on the line that belong to one item
+    auto write_row = [&](const Part& p, int r, int d, float x0, float x1) {
+        const int rr = p.row0 + r;
+        if (rr >= p.rows) return;
+        const int tok = rr / a.group;
+        const int64_t at = (p.first + tok) * a.q.out_token_stride +
+                           (p.head * a.group + rr - tok * a.group) * a.q.out_head_stride + d;
+        uint16_t* out = static_cast<uint16_t*>(a.q.out) + at;
+        const uint32_t w = a.bf16 ? Half<ARC_BF16>::pack(x0, x1) : Half<ARC_F16>::pack(x0, x1);
+        out[0] = static_cast<uint16_t>(w);
+        out[1] = static_cast<uint16_t>(w >> 16);
+    };
+    auto store_of = [&](int slot) {
+        return reinterpret_cast<const float*>(dyn + (slot >> 1) * S::kPerWarp + ((slot & 1) ? 0 : S::kRing));
+    };
+    constexpr int kSlot = R * D + 2 * R;  // floats of a block's partial: output, maxima, sums
+    int e0 = 0;
+    while (e0 < 2 * W) {
+        const Part p = sm.part[e0];
+        if (p.from < 0) {
+            ++e0;
+            continue;
+        }
+        int e1 = e0 + 1;
+        while (e1 < 2 * W && (sm.part[e1].from == p.from || sm.part[e1].from < 0)) ++e1;
+        const bool whole = p.from >= block_from && p.to <= block_to;
+        float* slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (p.from >= block_from ? 1 : 0)) * kSlot;
+        for (int i = tid; i < R * D / 2; i += kThreads) {
+            const int r = i / (D / 2), d = (i % (D / 2)) * 2;
+            float mm = -INFINITY;
+            for (int e = e0; e < e1; ++e)
+                if (sm.part[e].from >= 0) mm = fmaxf(mm, sm.m[e][r]);
+            float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
+            for (int e = e0; e < e1; ++e) {
+                if (sm.part[e].from < 0) continue;
+                const float f = sm.m[e][r] == -INFINITY ? (sm.l[e][r] != sm.l[e][r] ? 1.0f : 0.0f) : ex2(sm.m[e][r] - mm);
+                const float2 v = *reinterpret_cast<const float2*>(store_of(e) + r * D + d);
+                l = fmaf(sm.l[e][r], f, l);
+                x0 = fmaf(v.x, f, x0);
+                x1 = fmaf(v.y, f, x1);
+            }
+            if (whole) {
+                write_row(p, r, d, x0 / l, x1 / l);
+            } else {
+                __stcg(reinterpret_cast<float2*>(slot + r * D + d), make_float2(x0, x1));
+                if (d == 0) {
+                    __stcg(slot + R * D + r, mm);
+                    __stcg(slot + R * D + R + r, l);
+                }
+            }
+        }
+        e0 = e1;
+        if (whole) continue;
+        // ---- an item over several blocks: the last of them to arrive joins all, in order
+        auto block_of = [&](int64_t f) { return ((f + 1) * blocks - 1) / total; };
+        const int64_t c0 = block_of(p.from), c1 = block_of(p.to - 1);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) sm.last = atomicInc(a.arrived + c0, static_cast<uint32_t>(c1 - c0)) == static_cast<uint32_t>(c1 - c0);
+        __syncthreads();
+        if (sm.last) {
+            __threadfence();
+            for (int i = tid; i < R * D / 2; i += kThreads) {
+                const int r = i / (D / 2), d = (i % (D / 2)) * 2;
+                if (p.row0 + r >= p.rows) continue;
+                float mm = -INFINITY;
+                for (int64_t c = c0; c <= c1; ++c)
+                    mm = fmaxf(mm, __ldcg(a.partial + (c * 2 + (c == c0)) * kSlot + R * D + r));
+                float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
+                for (int64_t c = c0; c <= c1; ++c) {
+                    const float* q = a.partial + (c * 2 + (c == c0)) * kSlot;
+                    const float mc = __ldcg(q + R * D + r), lc = __ldcg(q + R * D + R + r);
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(q + r * D + d));
+                    const float f = mc == -INFINITY ? (lc != lc ? 1.0f : 0.0f) : ex2(mc - mm);
+                    l = fmaf(lc, f, l);
+                    x0 = fmaf(v.x, f, x0);
+                    x1 = fmaf(v.y, f, x1);
+                }
+                write_row(p, r, d, x0 / l, x1 / l);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NT>
+int launch(const AttendArgs& a, int dev, int sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    using S = Smem<D, NT>;
+    static_assert(S::kBytes + sizeof(S) <= arc::kSmemPerBlock, "shared memory");
+    if (arc::prepare(attend_kernel<D, NT>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
+    const int grid = sms < kMaxBlocks ? sms : kMaxBlocks;
+    attend_kernel<D, NT><<<grid, S::kThreads, S::kBytes, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
 }
 
@@ -120,7 +796,11 @@ int launch(const AttendArgs& a, cudaStream_t st) {
 
 extern "C" {
 
-size_t arc_kv_attend_workspace_bytes(const arc_kv_cache* cache) { return check_cache(cache) == ARC_OK ? 16 : 0; }
+size_t arc_kv_attend_workspace_bytes(const arc_kv_cache* cache) {
+    if (check_cache(cache) != ARC_OK) return 0;
+    const size_t rows = cache->head_dim == 256 ? 8 : 16;
+    return kStatusBytes + size_t{kMaxBlocks} * 2 * (rows * cache->head_dim + 2 * rows) * 4;
+}
 
 int arc_kv_attend(const arc_kv_cache* cache, const arc_kv_step* step, const arc_kv_query* query, uint32_t* err_word,
                   void* workspace, size_t workspace_bytes, void* stream) {
@@ -134,9 +814,29 @@ int arc_kv_attend(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
     if (!aligned(query->q, 2) || !aligned(query->out, 2) || !aligned(err_word, 4)) return ARC_E_ALIGN;
     if (workspace == nullptr || workspace_bytes < arc_kv_attend_workspace_bytes(cache)) return ARC_E_WORKSPACE;
     if (!aligned(workspace, 16)) return ARC_E_ALIGN;
-    AttendArgs a{*cache, *step, *query, err_word};
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    AttendArgs a;
+    a.c = *cache;
+    a.s = *step;
+    a.q = *query;
+    a.err = err_word;
+    a.arrived = static_cast<uint32_t*>(workspace);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+    a.group = query->q_heads / cache->heads;
+    a.bf16 = query->dtype == ARC_BF16;
+    a.vec = (vectors(query->q, query->q_token_stride, query->q_head_stride) ? 1 : 0) |
+            (vectors(query->out, query->out_token_stride, query->out_head_stride) ? 2 : 0);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return query->dtype == ARC_BF16 ? launch<ARC_BF16>(a, st) : launch<ARC_F16>(a, st);
+    // rows of a (sequence, cached head) on average: more than 8 take tiles of 16, which read the cache half as often
+    const int64_t rows = (step->T + step->B - 1) / step->B * a.group;
+    if (cache->head_dim == 64) return rows <= 8 ? launch<64, 1>(a, dev, sms, st) : launch<64, 2>(a, dev, sms, st);
+    if (cache->head_dim == 128) return rows <= 8 ? launch<128, 1>(a, dev, sms, st) : launch<128, 2>(a, dev, sms, st);
+    return launch<256, 1>(a, dev, sms, st);
 }
 
 }  // extern "C"
