@@ -1,7 +1,10 @@
 // arc_w4_matvec: a few rows times a matrix of 4-bit weights with group scales.
+#include <atomic>
 #include <climits>
 #include <cstdint>
+#include <cstring>
 
+#include "launch_util.cuh"
 #include "serve/arc_w4.h"
 #include "serve_util.cuh"
 
@@ -18,6 +21,7 @@ struct W4Args {
     int64_t x_stride, y_stride;
     int32_t rows;
     int32_t y_f32;
+    int32_t x_bf16;
 };
 
 // One warp for each output column, the rows in turn: a lane takes eight
@@ -55,6 +59,433 @@ __global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4
     }
 }
 
+// ------------------------------------------------------------------ few rows
+// 1 .. 16 rows of x: fp16 matrix instructions with 16 weight rows on the long
+// side and the rows of x on the short one.
+//
+// Mathematics.  A row of x is scaled by a power of two to [2^14, 2^15) and
+// taken as fp16: exact for values above 2^-25 of its largest.  A 4-bit code q,
+// masked out of its word, IS the fp16 subnormal q * 2^-24 (or, one nibble up,
+// 16 q * 2^-24, with x divided by 16 beforehand), so a word of eight weights
+// becomes four operand registers with one shift and four ANDs and no
+// conversion.  The zero point and the scale of a group act on its fp32 sum:
+//     y += s (sum q x - z sum x),
+// with the group's sum of x computed once a block.
+//
+// Layout.  A block's 16 warps are `parts` slices of the inner dimension (at
+// most 512 values each) times 16 / parts groups of 16 weight rows; blocks walk
+// over tiles of the outer dimension.  Each warp streams its own slice of its
+// own rows through a private ring of stages with 16-byte asynchronous copies;
+// the only barrier is the one that joins the slices' sums.  Weights are read
+// once, in their natural layout: the order of the inner dimension inside a
+// product is free, x is laid out to match what one shared load of a lane
+// gives.  Inner dimensions over one block's reach are split over a cluster,
+// whose first block adds the others' sums.
+constexpr int kFewThreads = 512;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kPart = 512;              // inner values of a warp's stage
+constexpr int kTileCost = 4;
+
+struct FewArgs {
+    W4Args a;
+    int32_t slice;    // inner values of a block, a multiple of 128
+    int32_t part;     // inner values of a warp, a multiple of 128, at most kPart
+    int32_t pitch;    // bytes of a weight row in a stage: 128 or 256
+    int32_t parts;    // 1, 2, 4, 8 or 16
+    int32_t stages;   // 2, 3 or 4
+    int32_t cluster;  // blocks that share a tile
+    int32_t tiles;
+    int32_t x_vec;
+    // shared-memory layout, bytes
+    int32_t x_off, xs_off, scale_off, red_off, join_off, up_off;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16-byte chunk c (0 .. 15) of weight row r (0 .. 15) in a stage: the chunks
+// of a 128-byte line are permuted by the row's bit-reversed low bits, so that
+// lanes reading 4, 8 or 16 bytes of one chunk in 8, 4 or 2 rows meet in no bank.
+__device__ __forceinline__ int weight_at(int pitch, int r, int c) {
+    const int f = ((r & 1) << 2) | (r & 2) | ((r >> 2) & 1);
+    return r * pitch + ((c & 8) | ((c & 7) ^ f)) * 16;
+}
+
+// x of the block's slice to shared memory: fp16, scaled row by row, in the
+// order of the products, and the sums of each group.
+template <int DT, int G, int NT>
+__device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, int ks) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rows = f.a.rows;
+    float* up = reinterpret_cast<float*>(dyn + f.up_off);
+    for (int m = warp; m < 8 * NT; m += kFewWarps) {
+        float top = 0.0f;
+        if (m < rows) {
+            const char* x = static_cast<const char*>(f.a.x) + (m * f.a.x_stride + k0) * 2;
+            for (int k = lane * 8; k < ks; k += 256) {
+                float v[8];
+                load8<DT>(x + k * 2, f.x_vec, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float z = fabsf(v[i]);
+                    if (z <= 3.4028235e38f) top = fmaxf(top, z);  // the largest finite one
+                }
+            }
+        }
+        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+        if (lane == 0) {
+            const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            const int e = top == 0.0f ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
+            up[m] = exp2i(e);
+        }
+    }
+    __syncthreads();
+    const int units = ks >> 3, groups = ks / G;
+    float* xs = reinterpret_cast<float*>(dyn + f.xs_off);
+    for (int i = tid; i < groups * 8 * NT; i += kFewThreads)
+        if (i % (8 * NT) >= rows) xs[i] = 0.0f;
+    for (int base = 0; base < units * rows; base += kFewThreads) {  // the same trips in every lane
+        // units of a group are neighbouring lanes: units is a multiple of G / 8
+        const int i = base + tid;
+        const bool on = i < units * rows;
+        const int m = on ? i / units : 0, u = i - m * units, k = on ? u * 8 : 0;
+        float v[8];
+        load8<DT>(static_cast<const char*>(f.a.x) + (m * f.a.x_stride + k0 + k) * 2, f.x_vec, v);
+        const float s = up[m];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v[j] *= s;
+            sum += v[j];
+        }
+        const int gi = k / G, in = k % G, t = in / (G / 4), w = (in % (G / 4)) >> 3;
+        const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
+                              __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f),
+                              __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f)};
+        if (on)
+            *reinterpret_cast<uint4*>(dyn + f.x_off + (((gi * (G / 32) + w) * rows + m) * 4 + t) * 16) =
+                *reinterpret_cast<const uint4*>(h);
+#pragma unroll
+        for (int x = 1; x < G / 8; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        if (on && (u & (G / 8 - 1)) == 0) xs[gi * 8 * NT + m] = sum;
+    }
+}
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewArgs f) {
+    extern __shared__ __align__(128) uint8_t dyn[];
+    const W4Args& a = f.a;
+    constexpr int WG = G / 32;            // weight words of a group that a lane takes
+    constexpr int SC = 16 * (kPart / G) / 32;  // scales of a part that a lane loads, at most
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int part = warp % f.parts, sub = warp / f.parts;  // slice of the inner dimension, group of 16 rows
+    const int per_tile = kFewWarps / f.parts * 16;
+    const int rank = f.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int first_tile = static_cast<int>(blockIdx.x) / f.cluster, tile_step = static_cast<int>(gridDim.x) / f.cluster;
+    const int k0 = rank * f.slice;                                              // the block's slice
+    const int ks = a.w.ins - k0 < f.slice ? a.w.ins - k0 : f.slice;
+    const int p0 = part * f.part;                                               // the warp's, within it
+    const int pk = ks - p0 < f.part ? (ks - p0 > 0 ? ks - p0 : 0) : f.part;
+    const int pg = pk / G;                                                      // its groups
+    const int groups = a.w.ins / G;
+
+    const int stage_bytes = 16 * f.pitch;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * f.stages * stage_bytes;
+    // [group][row]: the scale's bits, and above them the zero point's, which are those of the
+    // fp16 subnormal z * 2^-24
+    uint32_t* scales = reinterpret_cast<uint32_t*>(dyn + f.scale_off) + warp * (16 * (f.part / G));
+    const float* xs = reinterpret_cast<const float*>(dyn + f.xs_off) + (p0 / G) * 8 * NT;
+    const uint8_t* xf = dyn + f.x_off + static_cast<size_t>(p0 / 32) * a.rows * 64;
+
+    auto issue = [&](int tile, int stage) {
+        if (tile < f.tiles) {
+            const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;
+            const int c = lane & 15;
+            const char* q = static_cast<const char*>(a.w.q) + (k0 + p0) / 2 + c * 16;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                const bool on = n0 + r < a.w.outs && c * 32 < pk;
+                if (c * 16 < f.pitch) copy16(ring + stage * stage_bytes + weight_at(f.pitch, r, c), on ? q + (n0 + r) * a.w.row_bytes : a.w.q, on);
+            }
+        }
+        copies_end();
+    };
+    // scales and zero points of a tile: loaded a tile ahead, as they lie
+    uint16_t sv[SC];
+    uint8_t zv[SC];
+    auto fetch = [&](int tile) {
+        const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const int e = lane + 32 * i, r = e & 15, gi = e >> 4;
+            sv[i] = 0;
+            zv[i] = 8;
+            if (tile < f.tiles && n0 + r < a.w.outs && gi < pg) {
+                const int64_t at = (n0 + r) * groups + (k0 + p0) / G + gi;
+                sv[i] = __ldg(static_cast<const uint16_t*>(a.w.scales) + at);
+                if (a.w.zeros) zv[i] = __ldg(a.w.zeros + at);
+            }
+        }
+    };
+    int next = first_tile, fill = 0;
+    for (int i = 0; i < f.stages - 1; ++i) {
+        issue(next, fill++);
+        next += tile_step;
+    }
+    fetch(first_tile);
+
+    if (a.x_bf16)
+        stage_x<ARC_BF16, G, NT>(f, dyn, k0, ks);
+    else
+        stage_x<ARC_F16, G, NT>(f, dyn, k0, ks);
+    __syncthreads();
+    if (f.cluster > 1) cluster_sync_all();  // every block runs before its memory is written to
+
+    int stage = 0, turn = 0;
+    for (int tile = first_tile; tile < f.tiles; tile += tile_step) {
+        if (f.stages == 2)
+            copies_wait<0>();
+        else if (f.stages == 3)
+            copies_wait<1>();
+        else
+            copies_wait<2>();
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const int e = lane + 32 * i;
+            if ((e >> 4) < pg) scales[e] = sv[i] | (static_cast<uint32_t>(zv[i]) << 16);
+        }
+        __syncwarp();  // every lane's copies and scales are in; the stage before is free
+        issue(next, fill);
+        next += tile_step;
+        fill = fill + 1 == f.stages ? 0 : fill + 1;
+        fetch(tile + tile_step);
+
+        float y[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[nt][e] = 0.0f;
+        const uint32_t st = ring + stage * stage_bytes;
+        stage = stage + 1 == f.stages ? 0 : stage + 1;
+#pragma unroll 2
+        for (int gi = 0; gi < pg; ++gi) {
+            uint32_t w0[WG], w1[WG];
+            if constexpr (G == 128) {
+                const int c = gi * 4 + t;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(st + weight_at(f.pitch, g, c)));
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(st + weight_at(f.pitch, g + 8, c)));
+            } else if constexpr (G == 64) {
+                const int c = gi * 2 + (t >> 1), o = (t & 1) * 8;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(st + weight_at(f.pitch, g, c) + o));
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(st + weight_at(f.pitch, g + 8, c) + o));
+            } else {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0[0]) : "r"(st + weight_at(f.pitch, g, gi) + t * 4));
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1[0]) : "r"(st + weight_at(f.pitch, g + 8, gi) + t * 4));
+            }
+            float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WG; ++w) {
+                constexpr uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
+                const uint32_t u0 = w0[w] >> 8, u1 = w1[w] >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    if (8 * nt + g < a.rows)
+                        x = *reinterpret_cast<const uint4*>(xf + (((gi * WG + w) * a.rows + 8 * nt + g) * 4 + t) * 16);
+                    mma16816(acc[nt], w0[w] & lo, w1[w] & lo, u0 & lo, u1 & lo, x.x, x.y);
+                    mma16816(acc[nt], w0[w] & hi, w1[w] & hi, u0 & hi, u1 & hi, x.z, x.w);
+                }
+            }
+            const uint32_t b0 = scales[gi * 16 + g], b1 = scales[gi * 16 + g + 8];
+            auto scale_of = [&](uint32_t b) {
+                return make_float2(a.x_bf16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half(b & 0xFFFF)),
+                                   __half2float(__ushort_as_half(b >> 16)));
+            };
+            const float2 s0 = scale_of(b0), s1 = scale_of(b1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 sx = *reinterpret_cast<const float2*>(xs + gi * 8 * NT + 8 * nt + 2 * t);
+                y[nt][0] = fmaf(s0.x, fmaf(-s0.y, sx.x, acc[nt][0]), y[nt][0]);
+                y[nt][1] = fmaf(s0.x, fmaf(-s0.y, sx.y, acc[nt][1]), y[nt][1]);
+                y[nt][2] = fmaf(s1.x, fmaf(-s1.y, sx.x, acc[nt][2]), y[nt][2]);
+                y[nt][3] = fmaf(s1.x, fmaf(-s1.y, sx.y, acc[nt][3]), y[nt][3]);
+            }
+        }
+
+        // join the parts (and the cluster's slices); a value for each (weight row, row of x).
+        // Two buffers in turn: one barrier a tile.
+        constexpr int kVals = 16 * 8 * NT;
+        float* red = reinterpret_cast<float*>(dyn + f.red_off) + turn * kFewWarps * kVals;
+        float* mine = red + warp * kVals;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            // [row of x][weight row]
+            mine[(8 * nt + 2 * t) * 16 + g] = y[nt][0];
+            mine[(8 * nt + 2 * t + 1) * 16 + g] = y[nt][1];
+            mine[(8 * nt + 2 * t) * 16 + g + 8] = y[nt][2];
+            mine[(8 * nt + 2 * t + 1) * 16 + g + 8] = y[nt][3];
+        }
+        if (f.parts == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(f.parts * 32) : "memory");
+        const float* group = red + sub * f.parts * kVals;
+        const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;
+        const float* up = reinterpret_cast<const float*>(dyn + f.up_off);
+        auto finish = [&](int i, float v) {
+            const int m = i >> 4, r = i & 15;
+            if (n0 + r >= a.w.outs) return;
+            v = v * 0x1p24f;
+            const int64_t at = m * a.y_stride + n0 + r;
+            if (a.y_f32)
+                static_cast<float*>(a.y)[at] = v;
+            else if (a.x_bf16)
+                static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+            else
+                static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+        };
+        for (int i = part * 32 + lane; i < a.rows * 16; i += f.parts * 32) {
+            float v = 0.0f;
+            for (int p = 0; p < f.parts; ++p) v += group[p * kVals + i];
+            v = v / up[i >> 4];  // a power of two
+            if (f.cluster == 1) {
+                finish(i, v);
+            } else {
+                // into the first block's memory, a place for each rank
+                const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(
+                    dyn + f.join_off + (((turn * 8 + rank) * (kFewWarps / f.parts) + sub) * kVals + i) * 4));
+                uint32_t remote;
+                asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(local));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+            }
+        }
+        if (f.cluster > 1) {
+            __syncwarp();
+            cluster_sync_all();
+            if (rank == 0)
+                for (int i = part * 32 + lane; i < a.rows * 16; i += f.parts * 32) {
+                    float v = 0.0f;
+                    for (int c = 0; c < f.cluster; ++c)
+                        v += reinterpret_cast<const float*>(dyn + f.join_off)[((turn * 8 + c) * (kFewWarps / f.parts) + sub) * kVals + i];
+                    finish(i, v);
+                }
+        }
+        turn ^= 1;
+    }
+    copies_wait<0>();
+}
+
+template <int G, int NT>
+int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    if (arc::prepare(few_kernel<G, NT>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
+    FewArgs f;
+    f.a = a;
+    // a block's x stays within 64 KB: 4,096 inner values of 8 rows, 2,048 of 16
+    const int reach = NT == 1 ? 4096 : 2048;
+    int c = 1;
+    while (c * reach < a.w.ins) c *= 2;
+    f.cluster = c;
+    f.slice = ((a.w.ins + c - 1) / c + 127) / 128 * 128;
+    while (f.cluster > 1 && (f.cluster - 1) * f.slice >= a.w.ins) --f.cluster;  // no empty slice
+    int parts = 1;
+    while (parts * kPart < f.slice) parts *= 2;
+    // More parts of the inner dimension make smaller tiles: the parts whose rounds over the blocks cost least,
+    // counted in weight rows, with kTileCost for a tile's join
+    auto tiles_of = [&](int p) { return (a.w.outs + kFewWarps / p * 16 - 1) / (kFewWarps / p * 16); };
+    auto cost_of = [&](int p) {
+        const int64_t at_once = sms / f.cluster;
+        return (tiles_of(p) + at_once - 1) / at_once * (kFewWarps / p * 16 + kTileCost);
+    };
+    const int groups = f.slice / G;
+    // shared memory of `p` parts and `n` stages
+    auto layout = [&](int p, int n) {
+        f.parts = p;
+        f.part = ((f.slice + p - 1) / p + 127) / 128 * 128;
+        f.pitch = f.part > 256 ? 256 : 128;
+        f.stages = n;
+        int off = n * kFewWarps * 16 * f.pitch;
+        auto take = [&](int bytes) {
+            const int at = off;
+            off += (bytes + 127) / 128 * 128;
+            return at;
+        };
+        f.x_off = take(a.rows * f.slice * 2);
+        f.xs_off = take(groups * 8 * NT * 4);
+        f.scale_off = take(kFewWarps * 16 * (f.part / G) * 4);
+        f.red_off = take(2 * kFewWarps * 16 * 8 * NT * 4);
+        f.join_off = take(f.cluster > 1 ? 2 * 8 * (kFewWarps / p) * 16 * 8 * NT * 4 : 0);
+        f.up_off = take(8 * NT * 4);
+        return off;
+    };
+    int best = 0;
+    for (int p = parts; p <= kFewWarps && (p == parts || f.slice / p >= 128); p *= 2)
+        if (layout(p, 2) <= arc::kSmemPerBlock && (best == 0 || cost_of(p) < cost_of(best))) best = p;
+    if (best == 0) return ARC_E_UNSUPPORTED;
+    int stages = 4;
+    while (stages > 2 && layout(best, stages) > arc::kSmemPerBlock) --stages;
+    const int off = layout(best, stages);
+    parts = best;
+    f.tiles = static_cast<int32_t>(tiles_of(parts));
+    f.x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
+    int64_t grid = sms / f.cluster;
+    if (grid > f.tiles) grid = f.tiles;
+    grid *= f.cluster;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(off);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(f.cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = f.cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, few_kernel<G, NT>, f) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    return ARC_OK;
+}
+
+template <int NT>
+int launch_few_group(const W4Args& a, int dev, int sms, cudaStream_t st) {
+    if (a.w.group == 128) return launch_few<128, NT>(a, dev, sms, st);
+    if (a.w.group == 64) return launch_few<64, NT>(a, dev, sms, st);
+    return launch_few<32, NT>(a, dev, sms, st);
+}
+
 int check_weight(const arc_w4_weight* w) {
     if (w == nullptr || w->q == nullptr || w->scales == nullptr) return ARC_E_NULL;
     if (w->group != 32 && w->group != 64 && w->group != 128) return ARC_E_UNSUPPORTED;
@@ -83,7 +514,27 @@ int arc_w4_matvec(const arc_w4_weight* weight, const void* x, int64_t rows, int6
     if (rows <= 0 || rows > ARC_W4_MAX_ROWS || x_stride < weight->ins || y_stride < weight->outs) return ARC_E_SHAPE;
     if (reinterpret_cast<uintptr_t>(x) % 2 != 0 || reinterpret_cast<uintptr_t>(y) % (y_dtype == ARC_F32 ? 4 : 2) != 0)
         return ARC_E_ALIGN;
-    W4Args a{*weight, x, y, x_stride, y_stride, static_cast<int32_t>(rows), y_dtype == ARC_F32};
+    W4Args a{*weight, x, y, x_stride, y_stride, static_cast<int32_t>(rows), y_dtype == ARC_F32,
+             x_dtype == ARC_BF16};
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    if (rows <= 16) {
+        cudaStream_t few = static_cast<cudaStream_t>(stream);
+        if (rows <= 8) return launch_few_group<1>(a, dev, sms, few);
+        // 16 rows reach 16,384 inner values in a cluster of 8 blocks
+        if (weight->ins <= 16384) return launch_few_group<2>(a, dev, sms, few);
+        W4Args first = a, second = a;
+        first.rows = 8;
+        second.rows = a.rows - 8;
+        second.x = static_cast<const char*>(x) + 8 * x_stride * 2;
+        second.y = static_cast<char*>(y) + 8 * y_stride * (a.y_f32 ? 4 : 2);
+        const int one = launch_few_group<1>(first, dev, sms, few);
+        return one != ARC_OK ? one : launch_few_group<1>(second, dev, sms, few);
+    }
     const unsigned grid = static_cast<unsigned>((weight->outs * 32 + kThreads - 1) / kThreads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (x_dtype == ARC_BF16)
