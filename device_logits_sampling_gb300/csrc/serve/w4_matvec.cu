@@ -90,7 +90,6 @@ struct FewArgs {
     W4Args a;
     int32_t slice;    // inner values of a block, a multiple of 128
     int32_t part;     // inner values of a warp, a multiple of 128, at most kPart
-    int32_t pitch;    // bytes of a weight row in a stage: 128 or 256
     int32_t parts;    // 1, 2, 4, 8 or 16
     int32_t stages;   // 2, 3 or 4
     int32_t cluster;  // blocks that share a tile
@@ -124,17 +123,18 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 16-byte chunk c (0 .. 15) of weight row r (0 .. 15) in a stage: the chunks
-// of a 128-byte line are permuted by the row's bit-reversed low bits, so that
-// lanes reading 4, 8 or 16 bytes of one chunk in 8, 4 or 2 rows meet in no bank.
-__device__ __forceinline__ int weight_at(int pitch, int r, int c) {
-    const int f = ((r & 1) << 2) | (r & 2) | ((r >> 2) & 1);
-    return r * pitch + ((c & 8) | ((c & 7) ^ f)) * 16;
+// 16-byte chunk c of weight row r (0 .. 15) in a stage: the chunks of a
+// 128-byte line are permuted by the row's bit-reversed low bits, so that lanes
+// reading 4, 8 or 16 bytes of one chunk in 8, 4 or 2 rows meet in no bank.
+__device__ __forceinline__ constexpr int row_bits(int r) { return ((r & 1) << 2) | (r & 2) | ((r >> 2) & 1); }
+template <int PITCH>
+__device__ __forceinline__ int weight_at(int r, int c) {
+    return r * PITCH + ((c & 8) | ((c & 7) ^ row_bits(r))) * 16;
 }
 
 // x of the block's slice to shared memory: fp16, scaled row by row, in the
 // order of the products, and the sums of each group.
-template <int DT, int G, int NT>
+template <int DT, int G, int NT, bool Z>
 __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, int ks) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rows = f.a.rows;
@@ -188,16 +188,38 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
                 *reinterpret_cast<const uint4*>(h);
 #pragma unroll
         for (int x = 1; x < G / 8; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        if (on && (u & (G / 8 - 1)) == 0) xs[gi * 8 * NT + m] = sum;
+        // without zero points the sum comes times the common one, 8 * 2^-24
+        if (on && (u & (G / 8 - 1)) == 0) xs[gi * 8 * NT + m] = Z ? sum : sum * 0x1p-21f;
     }
 }
 
-template <int G, int NT>
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+__device__ __forceinline__ void load_words(uint32_t p, Words<4>& x) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]) : "r"(p));
+}
+__device__ __forceinline__ void load_words(uint32_t p, Words<2>& x) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.w[0]), "=r"(x.w[1]) : "r"(p));
+}
+__device__ __forceinline__ void load_words(uint32_t p, Words<1>& x) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.w[0]) : "r"(p));
+}
+
+// G: group. NT: tiles of 8 rows of x. P: inner values of a part at most (512 or
+// 256). Z: zero points are given.
+template <int G, int NT, int P, bool Z>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewArgs f) {
-    extern __shared__ __align__(128) uint8_t dyn[];
+    extern __shared__ __align__(1024) uint8_t dyn[];
     const W4Args& a = f.a;
     constexpr int WG = G / 32;            // weight words of a group that a lane takes
-    constexpr int SC = 16 * (kPart / G) / 32;  // scales of a part that a lane loads, at most
+    constexpr int PG = P / G;             // groups of a full part
+    constexpr int PITCH = P / 2;          // bytes of a weight row in a stage
+    constexpr int STAGE = 16 * PITCH;
+    constexpr int SC = 16 * PG / 32;      // scales of a part that a lane loads
+    constexpr int CPY = PITCH / 32;       // 16-byte copies of a lane a stage
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int part = warp % f.parts, sub = warp / f.parts;  // slice of the inner dimension, group of 16 rows
     const int per_tile = kFewWarps / f.parts * 16;
@@ -210,43 +232,55 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     const int pg = pk / G;                                                      // its groups
     const int groups = a.w.ins / G;
 
-    const int stage_bytes = 16 * f.pitch;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * f.stages * stage_bytes;
-    // [group][row]: the scale's bits, and above them the zero point's, which are those of the
-    // fp16 subnormal z * 2^-24
-    uint32_t* scales = reinterpret_cast<uint32_t*>(dyn + f.scale_off) + warp * (16 * (f.part / G));
-    const float* xs = reinterpret_cast<const float*>(dyn + f.xs_off) + (p0 / G) * 8 * NT;
-    const uint8_t* xf = dyn + f.x_off + static_cast<size_t>(p0 / 32) * a.rows * 64;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * f.stages * STAGE;
+    // [group][row]: the scale, and with Z the zero point times 2^-24
+    constexpr int SW = Z ? 2 : 1;
+    float* scales = reinterpret_cast<float*>(dyn + f.scale_off) + warp * (16 * PG * SW);
+    const float* xs = reinterpret_cast<const float*>(dyn + f.xs_off) + (p0 / G) * 8 * NT + 2 * t;
+    const uint8_t* xf = dyn + f.x_off + (static_cast<size_t>(p0 / 32) * a.rows * 4 + g * 4 + t) * 16;
 
+    // A lane copies chunk cc of the rows ch, ch + step, ...; the rows' permutation (weight_at) is an
+    // exclusive or with a constant of the unrolled copy.
+    constexpr int kRowsAtOnce = P == 512 ? 2 : 4;
+    const int cc = lane % (32 / kRowsAtOnce), ch = lane / (32 / kRowsAtOnce);
+    const uint32_t copy_to = ring + weight_at<PITCH>(ch, cc);
+    const bool whole_part = pk == P;
+    const char* const q_from = static_cast<const char*>(a.w.q) + (k0 + p0) / 2 + cc * 16;
     auto issue = [&](int tile, int stage) {
         if (tile < f.tiles) {
-            const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;
-            const int c = lane & 15;
-            const char* q = static_cast<const char*>(a.w.q) + (k0 + p0) / 2 + c * 16;
+            const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16 + ch;
+            const char* q = q_from + n0 * a.w.row_bytes;
+            const uint32_t dst = copy_to + stage * STAGE;
+            const bool full = whole_part && n0 - ch + 16 <= a.w.outs;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 2 * i + (lane >> 4);
-                const bool on = n0 + r < a.w.outs && c * 32 < pk;
-                if (c * 16 < f.pitch) copy16(ring + stage * stage_bytes + weight_at(f.pitch, r, c), on ? q + (n0 + r) * a.w.row_bytes : a.w.q, on);
+            for (int i = 0; i < CPY; ++i) {
+                const int r = kRowsAtOnce * i;
+                const uint32_t to = (dst ^ (row_bits(r) * 16)) + r * PITCH;
+                if (full) {
+                    copy16(to, q, true);
+                } else {
+                    const bool on = n0 + r < a.w.outs && cc * 32 < pk;
+                    copy16(to, on ? q : a.w.q, on);
+                }
+                q += kRowsAtOnce * a.w.row_bytes;
             }
         }
         copies_end();
     };
-    // scales and zero points of a tile: loaded a tile ahead, as they lie
+    // scales and zero points of a tile, loaded a tile ahead: row lane % 16, every other group
     uint16_t sv[SC];
     uint8_t zv[SC];
+    const int64_t s_from = (k0 + p0) / G + (lane >> 4);
     auto fetch = [&](int tile) {
-        const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;
+        const int64_t n = static_cast<int64_t>(tile) * per_tile + sub * 16 + (lane & 15);
+        const bool row = tile < f.tiles && n < a.w.outs;
+        const uint16_t* s = static_cast<const uint16_t*>(a.w.scales) + n * groups + s_from;
+        const uint8_t* z = a.w.zeros + n * groups + s_from;
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
-            const int e = lane + 32 * i, r = e & 15, gi = e >> 4;
-            sv[i] = 0;
-            zv[i] = 8;
-            if (tile < f.tiles && n0 + r < a.w.outs && gi < pg) {
-                const int64_t at = (n0 + r) * groups + (k0 + p0) / G + gi;
-                sv[i] = __ldg(static_cast<const uint16_t*>(a.w.scales) + at);
-                if (a.w.zeros) zv[i] = __ldg(a.w.zeros + at);
-            }
+            const bool on = row && 2 * i + (lane >> 4) < pg;
+            sv[i] = on ? __ldg(s + 2 * i) : 0;
+            if (Z) zv[i] = on ? __ldg(z + 2 * i) : 0;
         }
     };
     int next = first_tile, fill = 0;
@@ -257,12 +291,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     fetch(first_tile);
 
     if (a.x_bf16)
-        stage_x<ARC_BF16, G, NT>(f, dyn, k0, ks);
+        stage_x<ARC_BF16, G, NT, Z>(f, dyn, k0, ks);
     else
-        stage_x<ARC_F16, G, NT>(f, dyn, k0, ks);
+        stage_x<ARC_F16, G, NT, Z>(f, dyn, k0, ks);
     __syncthreads();
     if (f.cluster > 1) cluster_sync_all();  // every block runs before its memory is written to
 
+    const uint32_t read_at = g * PITCH;
+    const uint32_t gbits = row_bits(g) * 16;  // those of row g + 8 too
     int stage = 0, turn = 0;
     for (int tile = first_tile; tile < f.tiles; tile += tile_step) {
         if (f.stages == 2)
@@ -273,8 +309,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             copies_wait<2>();
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
-            const int e = lane + 32 * i;
-            if ((e >> 4) < pg) scales[e] = sv[i] | (static_cast<uint32_t>(zv[i]) << 16);
+            const int e = (lane + 32 * i) * SW;
+            scales[e] = a.x_bf16 ? __uint_as_float(static_cast<uint32_t>(sv[i]) << 16) : __half2float(__ushort_as_half(sv[i]));
+            if (Z) scales[e + 1] = __half2float(__ushort_as_half(zv[i]));  // the code's bits as fp16: z * 2^-24
         }
         __syncwarp();  // every lane's copies and scales are in; the stage before is free
         issue(next, fill);
@@ -287,25 +324,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[nt][e] = 0.0f;
-        const uint32_t st = ring + stage * stage_bytes;
+        const uint32_t st = ring + stage * STAGE + read_at;
         stage = stage + 1 == f.stages ? 0 : stage + 1;
-#pragma unroll 2
-        for (int gi = 0; gi < pg; ++gi) {
-            uint32_t w0[WG], w1[WG];
-            if constexpr (G == 128) {
-                const int c = gi * 4 + t;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w0[0]), "=r"(w0[1]), "=r"(w0[2]), "=r"(w0[3]) : "r"(st + weight_at(f.pitch, g, c)));
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(w1[0]), "=r"(w1[1]), "=r"(w1[2]), "=r"(w1[3]) : "r"(st + weight_at(f.pitch, g + 8, c)));
-            } else if constexpr (G == 64) {
-                const int c = gi * 2 + (t >> 1), o = (t & 1) * 8;
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0[0]), "=r"(w0[1]) : "r"(st + weight_at(f.pitch, g, c) + o));
-                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w1[0]), "=r"(w1[1]) : "r"(st + weight_at(f.pitch, g + 8, c) + o));
-            } else {
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0[0]) : "r"(st + weight_at(f.pitch, g, gi) + t * 4));
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1[0]) : "r"(st + weight_at(f.pitch, g + 8, gi) + t * 4));
-            }
+        auto one_group = [&](int gi) {
+            Words<WG> w0, w1;
+            // chunk of the lane's words and the byte within it
+            const int c = WG == 4 ? gi * 4 + t : WG == 2 ? gi * 2 + (t >> 1) : gi;
+            const int o = WG == 4 ? 0 : WG == 2 ? (t & 1) * 8 : t * 4;
+            const uint32_t at = st + ((c * 16) ^ gbits) + o;
+            load_words(at, w0);
+            load_words(at + 8 * PITCH, w1);
             float acc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -314,30 +342,39 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
             for (int w = 0; w < WG; ++w) {
                 constexpr uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
-                const uint32_t u0 = w0[w] >> 8, u1 = w1[w] >> 8;
+                const uint32_t u0 = w0.w[w] >> 8, u1 = w1.w[w] >> 8;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
                     if (8 * nt + g < a.rows)
-                        x = *reinterpret_cast<const uint4*>(xf + (((gi * WG + w) * a.rows + 8 * nt + g) * 4 + t) * 16);
-                    mma16816(acc[nt], w0[w] & lo, w1[w] & lo, u0 & lo, u1 & lo, x.x, x.y);
-                    mma16816(acc[nt], w0[w] & hi, w1[w] & hi, u0 & hi, u1 & hi, x.z, x.w);
+                        x = *reinterpret_cast<const uint4*>(xf + ((gi * WG + w) * a.rows + 8 * nt) * 64);
+                    mma16816(acc[nt], w0.w[w] & lo, w1.w[w] & lo, u0 & lo, u1 & lo, x.x, x.y);
+                    mma16816(acc[nt], w0.w[w] & hi, w1.w[w] & hi, u0 & hi, u1 & hi, x.z, x.w);
                 }
             }
-            const uint32_t b0 = scales[gi * 16 + g], b1 = scales[gi * 16 + g + 8];
-            auto scale_of = [&](uint32_t b) {
-                return make_float2(a.x_bf16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half(b & 0xFFFF)),
-                                   __half2float(__ushort_as_half(b >> 16)));
-            };
-            const float2 s0 = scale_of(b0), s1 = scale_of(b1);
+            float s0, s1, z0 = 1.0f, z1 = 1.0f;
+            if constexpr (Z) {
+                const float2 b0 = *reinterpret_cast<const float2*>(scales + (gi * 16 + g) * 2);
+                const float2 b1 = *reinterpret_cast<const float2*>(scales + (gi * 16 + g + 8) * 2);
+                s0 = b0.x, z0 = b0.y, s1 = b1.x, z1 = b1.y;
+            } else {
+                s0 = scales[gi * 16 + g];
+                s1 = scales[gi * 16 + g + 8];
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float2 sx = *reinterpret_cast<const float2*>(xs + gi * 8 * NT + 8 * nt + 2 * t);
-                y[nt][0] = fmaf(s0.x, fmaf(-s0.y, sx.x, acc[nt][0]), y[nt][0]);
-                y[nt][1] = fmaf(s0.x, fmaf(-s0.y, sx.y, acc[nt][1]), y[nt][1]);
-                y[nt][2] = fmaf(s1.x, fmaf(-s1.y, sx.x, acc[nt][2]), y[nt][2]);
-                y[nt][3] = fmaf(s1.x, fmaf(-s1.y, sx.y, acc[nt][3]), y[nt][3]);
+                const float2 sx = *reinterpret_cast<const float2*>(xs + gi * 8 * NT + 8 * nt);
+                y[nt][0] = fmaf(s0, fmaf(-z0, sx.x, acc[nt][0]), y[nt][0]);
+                y[nt][1] = fmaf(s0, fmaf(-z0, sx.y, acc[nt][1]), y[nt][1]);
+                y[nt][2] = fmaf(s1, fmaf(-z1, sx.x, acc[nt][2]), y[nt][2]);
+                y[nt][3] = fmaf(s1, fmaf(-z1, sx.y, acc[nt][3]), y[nt][3]);
             }
+        };
+        if (whole_part) {
+#pragma unroll
+            for (int gi = 0; gi < PG; ++gi) one_group(gi);
+        } else {
+            for (int gi = 0; gi < pg; ++gi) one_group(gi);
         }
 
         // join the parts (and the cluster's slices); a value for each (weight row, row of x).
@@ -348,10 +385,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             // [row of x][weight row]
-            mine[(8 * nt + 2 * t) * 16 + g] = y[nt][0];
-            mine[(8 * nt + 2 * t + 1) * 16 + g] = y[nt][1];
-            mine[(8 * nt + 2 * t) * 16 + g + 8] = y[nt][2];
-            mine[(8 * nt + 2 * t + 1) * 16 + g + 8] = y[nt][3];
+            if (8 * nt + 2 * t < a.rows) {
+                mine[(8 * nt + 2 * t) * 16 + g] = y[nt][0];
+                mine[(8 * nt + 2 * t) * 16 + g + 8] = y[nt][2];
+                mine[(8 * nt + 2 * t + 1) * 16 + g] = y[nt][1];
+                mine[(8 * nt + 2 * t + 1) * 16 + g + 8] = y[nt][3];
+            }
         }
         if (f.parts == 1)
             __syncwarp();
@@ -403,10 +442,32 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     copies_wait<0>();
 }
 
+template <int G, int NT, int P, bool Z>
+int start_few(const FewArgs& f, int64_t grid, int smem, int dev, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    if (arc::prepare(few_kernel<G, NT, P, Z>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(f.cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = f.cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, few_kernel<G, NT, P, Z>, f) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    return ARC_OK;
+}
+
 template <int G, int NT>
 int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
-    static std::atomic<uint64_t> done{0};
-    if (arc::prepare(few_kernel<G, NT>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
     FewArgs f;
     f.a = a;
     // a block's x stays within 64 KB: 4,096 inner values of 8 rows, 2,048 of 16
@@ -430,9 +491,9 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
     auto layout = [&](int p, int n) {
         f.parts = p;
         f.part = ((f.slice + p - 1) / p + 127) / 128 * 128;
-        f.pitch = f.part > 256 ? 256 : 128;
+        const int most = f.part > 256 ? 512 : 256;  // the kernel's P
         f.stages = n;
-        int off = n * kFewWarps * 16 * f.pitch;
+        int off = n * kFewWarps * 16 * most / 2;
         auto take = [&](int bytes) {
             const int at = off;
             off += (bytes + 127) / 128 * 128;
@@ -440,7 +501,7 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
         };
         f.x_off = take(a.rows * f.slice * 2);
         f.xs_off = take(groups * 8 * NT * 4);
-        f.scale_off = take(kFewWarps * 16 * (f.part / G) * 4);
+        f.scale_off = take(kFewWarps * 16 * (most / G) * (a.w.zeros ? 8 : 4));
         f.red_off = take(2 * kFewWarps * 16 * 8 * NT * 4);
         f.join_off = take(f.cluster > 1 ? 2 * 8 * (kFewWarps / p) * 16 * 8 * NT * 4 : 0);
         f.up_off = take(8 * NT * 4);
@@ -459,24 +520,9 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
     int64_t grid = sms / f.cluster;
     if (grid > f.tiles) grid = f.tiles;
     grid *= f.cluster;
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kFewThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(off);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(f.cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = f.cluster > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, few_kernel<G, NT>, f) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return ARC_E_CUDA;
-    }
-    return ARC_OK;
+    if (f.part > 256)
+        return a.w.zeros ? start_few<G, NT, 512, true>(f, grid, off, dev, st) : start_few<G, NT, 512, false>(f, grid, off, dev, st);
+    return a.w.zeros ? start_few<G, NT, 256, true>(f, grid, off, dev, st) : start_few<G, NT, 256, false>(f, grid, off, dev, st);
 }
 
 template <int NT>

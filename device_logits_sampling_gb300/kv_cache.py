@@ -182,7 +182,7 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
         want(rope.turns.device == cache.device, "every tensor must be on the cache's device")
     step = _step(cache, T, positions, page_table, row_offsets)
     rc = serve.load().arc_kv_append(cache._ref, ctypes.addressof(step), ctypes.addressof(rows),
-                                    None if rope is None else rope._ref, sampler._ptr(err_word), sampler._stream(stream))
+                                    None if rope is None else rope._ref, sampler._ptr(err_word), serve.stream_of(stream, cache.device))
     serve.finish(rc, check)
     return q_out
 
@@ -209,6 +209,6 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
                           q.shape[1], serve.dtype_code(q), cache.head_dim ** -0.5 if scale is None else scale, int(window))
     step = _step(cache, T, positions, page_table, row_offsets)
     rc = serve.load().arc_kv_attend(cache._ref, ctypes.addressof(step), ctypes.addressof(query), sampler._ptr(err_word),
-                                    workspace.data_ptr(), workspace.numel(), sampler._stream(stream))
+                                    workspace.data_ptr(), workspace.numel(), serve.stream_of(stream, cache.device))
     serve.finish(rc, check)
     return out

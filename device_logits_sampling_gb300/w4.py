@@ -52,6 +52,6 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     rc = lib.arc_w4_matvec(ref, x.data_ptr(), rows, x.stride(0) if rows > 1 else ins, serve.dtype_code(x), out.data_ptr(),
                            out.stride(0) if rows > 1 else outs, serve.dtype_code(out, f32=True),
-                           sampler._ptr(workspace), 0 if workspace is None else workspace.numel(), sampler._stream(stream))
+                           sampler._ptr(workspace), 0 if workspace is None else workspace.numel(), serve.stream_of(stream, x.device))
     serve.finish(rc, check)
     return out
