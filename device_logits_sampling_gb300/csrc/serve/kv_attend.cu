@@ -112,20 +112,11 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t p) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t p) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p));
-    return v;
-}
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint2 lds8(const uint8_t* p) { return *reinterpret_cast<const uint2*>(p); }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -472,7 +463,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 copies_wait<ST - 2>();
                 __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
                 issue();
-                const uint32_t kst = ring + stage * S::kStage, vst = kst + 16 * D;
+                const uint8_t *kst = dyn + warp * S::kPerWarp + stage * S::kStage, *vst = kst + 16 * D;
                 const float ks = sm.scales[warp][stage][0];
                 const uint32_t vb = __float_as_uint(sm.scales[warp][stage][1]);
                 stage = stage + 1 == ST ? 0 : stage + 1;

@@ -1,0 +1,622 @@
+// 9 .. 256 rows of x times 4-bit weights, on the 5th-generation tensor cores.
+//
+// Mathematics.  128 weight rows are the long side of a product (operand A), up
+// to 128 rows of x the other (B, in shared memory).  A code masked out of its
+// word is the fp16 subnormal q * 2^-24 (one nibble up: 16 q * 2^-24, with x
+// divided by 16 beforehand); the zero point is subtracted in the same form,
+// exactly, and x is fp16 after a power-of-two scaling of each row.  Group
+// scales stay out of the products: each group's fp32 sum is read back and
+// multiplied by its scale in fp32.
+//
+// Where things lie.  A never touches shared memory: a thread owns one weight
+// row, unpacks 128 values of it into 64 registers and stores them to tensor
+// memory, which is where the product reads A.  The order of the inner
+// dimension inside a product is free, so the unpacked pairs stay as the masks
+// give them and x is laid out to match, once a call, by a small kernel that
+// also swizzles it: a stage of x is one contiguous bulk copy.  A group's sums
+// lie in tensor memory with the weight row as the lane, so its scale is one
+// number a thread and the running sums are the thread's registers.
+//
+// Roles of a block: warps 0-3 add up groups (and store the output), warps 4-7
+// copy and unpack weights, warp 8 issues the products, warp 9 copies x.  They
+// meet at barriers in shared memory: rings of unpacked A, of x and of group
+// sums, so that copying, unpacking, multiplying and adding up overlap across
+// groups and tiles.  Few tiles: the inner dimension is split over a cluster
+// whose blocks add each other's sums through distributed shared memory.
+//
+// Every wait has a limit; a block whose wait runs out writes NaN.
+#include <atomic>
+#include <climits>
+#include <cstdint>
+#include <cstring>
+
+#include "launch_util.cuh"
+#include "serve_util.cuh"
+#include "w4_many.cuh"
+
+namespace arcs {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kInner = 128;    // inner values of a block of A and x
+constexpr int kRawStage = 32 * 128;  // bytes of a warp's raw stage: 32 rows of 256 codes
+constexpr int kWaits = 1 << 24;
+
+template <int N>
+struct Many {
+    static constexpr int kSums = N == 128 ? 3 : 4;       // ring of group sums, N columns each
+    static constexpr int kA = 2;                         // ring of unpacked A, 64 columns each
+    static constexpr int kX = N == 128 ? 3 : 4;          // ring of x
+    static constexpr int kRaw = N == 128 ? 6 : 8;        // a warp's ring of raw weights
+    static constexpr int kColumns = N >= 64 ? 512 : 256; // tensor memory taken
+    static constexpr int kXBytes = N * kInner * 2;
+    static constexpr int kRawBytes = 4 * kRaw * kRawStage;
+    static constexpr int kJoin = N * 128 * 4;            // over the rings, at the end
+    static constexpr int kRings = kX * kXBytes + kRawBytes;
+    static constexpr int kSmem = (kRings > kJoin ? kRings : kJoin) + 1024;
+};
+
+struct Bars {
+    uint64_t a_full[2], a_empty[2];
+    uint64_t x_full[4], x_empty[4];
+    uint64_t s_full[4], s_empty[4];
+    uint32_t tmem;
+    uint32_t failed;
+};
+
+__device__ __forceinline__ uint32_t shared_of(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_of(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_of(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_of(b)), "r"(bytes) : "memory");
+}
+// Waits for the phase; gives up after kWaits tries, or when another role has.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, uint32_t* failed) {
+    const uint32_t p = shared_of(b);
+    for (int i = 0; i < kWaits; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(p), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 1023) == 1023 && *static_cast<volatile uint32_t*>(failed)) return false;
+    }
+    *static_cast<volatile uint32_t*>(failed) = 1;
+    return false;
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void commit_to(uint64_t* b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_of(b)) : "memory");
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+#define ARC_REGS8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&x)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        ARC_REGS8(x, 0), ARC_REGS8(x, 8), ARC_REGS8(x, 16), ARC_REGS8(x, 24)
+        : "memory");
+}
+#undef ARC_REGS8
+#define ARC_OUT8(x, o) "=r"(x[o]), "=r"(x[o + 1]), "=r"(x[o + 2]), "=r"(x[o + 3]), "=r"(x[o + 4]), "=r"(x[o + 5]), "=r"(x[o + 6]), "=r"(x[o + 7])
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : ARC_OUT8(x, 0), ARC_OUT8(x, 8)
+        : "r"(at)
+        : "memory");
+}
+#undef ARC_OUT8
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int C>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C) : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// K-major operand in shared memory, rows of 128 bytes in swizzled groups of
+// eight: start address, 1,024 bytes from group to group, 128-byte swizzle.
+__device__ __forceinline__ uint64_t operand_at(uint32_t shared) {
+    return static_cast<uint64_t>((shared & 0x3FFFFu) >> 4) | (uint64_t{1} << 16) | (uint64_t{1024 >> 4} << 32) |
+           (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// ------------------------------------------------------------------ x
+// One block for each row (and each row of padding): fp16, scaled by a power of
+// two to [2^14, 2^15), in the order of the unpacked pairs: a word of eight
+// codes k0 .. k7 gives (k0, k4), (k2, k6) and, times 16, (k1, k5), (k3, k7).
+template <int DT>
+__global__ void __launch_bounds__(256) many_x_kernel(const __grid_constant__ ManyArgs a) {
+    __shared__ uint32_t red[8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int row = blockIdx.x, tid = threadIdx.x;
+    const int block_rows = a.columns, half = row / block_rows, in = row % block_rows;
+    const bool real = row < a.rows;
+    const char* x = static_cast<const char*>(a.x) + row * a.x_stride * 2;
+    const int units = a.ins / 8, all = a.blocks * (kInner / 8);
+    float top = 0.0f;
+    if (real)
+        for (int u = tid; u < units; u += 256) {
+            float v[8];
+            load8<DT>(x + u * 16, a.x_vec, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float z = fabsf(v[i]);
+                if (z <= 3.4028235e38f) top = fmaxf(top, z);  // the largest finite one
+            }
+        }
+    const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+    if ((tid & 31) == 0) red[tid >> 5] = w;
+    __syncthreads();
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+    const int ex = static_cast<int>(m >> 23) - 127;
+    const int e = m == 0 ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
+    const float up = exp2i(e);
+    if (tid == 0) a.x_back[row] = exp2i(-e);
+    uint8_t* const out = static_cast<uint8_t*>(a.x_ready) + static_cast<size_t>(half) * a.blocks * block_rows * (kInner * 2);
+    for (int u = tid; u < all; u += 256) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        if (real && u < units) load8<DT>(x + u * 16, a.x_vec, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= up;
+        const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
+                              __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f),
+                              __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f)};
+        // 64 values of all rows, 128 bytes a row, its 16-byte chunks swizzled by the row
+        const size_t at = (static_cast<size_t>(u >> 3) * block_rows + in) * 128 + (((u & 7) ^ (in & 7)) * 16);
+        *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(h);
+    }
+}
+
+// ------------------------------------------------------------------ products
+template <int N>
+__global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ ManyArgs a) {
+    using M = Many<N>;
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ Bars bars;
+    uint8_t* const dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(blockIdx.x) % a.cluster;
+    const int first = static_cast<int>(blockIdx.x) / a.cluster, step = static_cast<int>(gridDim.x) / a.cluster;
+    const int items = a.tiles * a.halves;
+    // blocks of the inner dimension that this block takes
+    const int b0 = static_cast<int>(static_cast<int64_t>(a.blocks) * rank / a.cluster);
+    const int nb = static_cast<int>(static_cast<int64_t>(a.blocks) * (rank + 1) / a.cluster) - b0;
+    const int per = kInner / a.group;  // groups of a block
+    uint8_t* const x_ring = dyn;
+    uint8_t* const raw_ring = dyn + M::kX * M::kXBytes;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&bars.a_full[i], 4);
+            bar_init(&bars.a_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            bar_init(&bars.x_full[i], 1);
+            bar_init(&bars.x_empty[i], 1);
+            bar_init(&bars.s_full[i], 1);
+            bar_init(&bars.s_empty[i], 4);
+        }
+        bars.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_of(&bars.tmem)),
+                     "n"(M::kColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bars.tmem, tmem_a = tmem + M::kSums * N;
+
+    if (warp >= 4 && warp < 8) {
+        // ---- unpack: a thread for each weight row
+        const int w = warp - 4;
+        const uint32_t ring = shared_of(raw_ring) + w * M::kRaw * kRawStage;
+        const uint8_t* const ring_p = raw_ring + w * M::kRaw * kRawStage;
+        const int pairs = (nb + 1) / 2;  // raw stages of an item: two blocks each
+        int c_item = first, c_pair = 0, c_stage = 0;
+        auto issue = [&]() {
+            if (c_item < items) {
+                const int64_t n0 = static_cast<int64_t>(c_item / a.halves) * 128 + w * 32;
+                const int k = (b0 + 2 * c_pair) * kInner;         // first inner value
+                const int end = (b0 + nb) * kInner < a.ins ? (b0 + nb) * kInner : a.ins;
+                const int c = lane & 7;
+                const bool inner = k + c * 32 < end;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    const bool on = inner && n0 + r < a.outs;
+                    const char* src = static_cast<const char*>(a.q) + (on ? (n0 + r) * a.row_bytes + k / 2 + c * 16 : 0);
+                    copy16(ring + c_stage * kRawStage + r * 128 + ((c ^ (r & 7)) * 16), src, on);
+                }
+                if (++c_pair == pairs) {
+                    c_pair = 0;
+                    c_item += step;
+                }
+            }
+            copies_end();
+            c_stage = c_stage + 1 == M::kRaw ? 0 : c_stage + 1;
+        };
+        for (int i = 0; i < M::kRaw - 1; ++i) issue();
+        int stage = 0;
+        uint32_t used = 0;  // blocks of A so far
+        bool ok = true;
+        for (int item = first; ok && item < items; item += step) {
+            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + w * 32 + lane;
+            const uint8_t* zero_at = a.zeros && n < a.outs ? a.zeros + n * a.groups : nullptr;
+            int gi = b0 * per;
+            // eight zero points ahead in a register pair
+            auto zeros_of = [&](int g) {
+                uint2 z = make_uint2(0x08080808u, 0x08080808u);
+                if (zero_at && g < a.groups) {
+                    if (a.z_vec) {
+                        z = __ldg(reinterpret_cast<const uint2*>(zero_at + g));
+                    } else {
+                        uint32_t b[2] = {0, 0};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (g + i < a.groups) b[i >> 2] |= static_cast<uint32_t>(__ldg(zero_at + g + i)) << (8 * (i & 3));
+                        z = make_uint2(b[0], b[1]);
+                    }
+                }
+                return z;
+            };
+            uint2 z_now = zeros_of(gi & ~7), z_next = zeros_of((gi & ~7) + 8);
+            for (int i = 0; i < (gi & 7); ++i) {
+                z_now.x = __funnelshift_r(z_now.x, z_now.y, 8);
+                z_now.y >>= 8;
+            }
+            uint32_t z_lo = 0, z_hi = 0;
+            for (int pair = 0; ok && pair < pairs; ++pair) {
+                copies_wait<M::kRaw - 2>();
+                __syncwarp();
+                issue();
+                const uint8_t* row = ring_p + stage * kRawStage + lane * 128;
+                stage = stage + 1 == M::kRaw ? 0 : stage + 1;
+                for (int h = 0; h < 2 && 2 * pair + h < nb; ++h) {
+                    const int buf = used & 1;
+                    ok = bar_wait(&bars.a_empty[buf], ((used >> 1) & 1) ^ 1, &bars.failed);
+                    if (!__all_sync(0xFFFFFFFFu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_after();
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int ci = 2 * s + c;  // chunk of 32 values within the block
+                            if ((ci * 32 & (a.group - 1)) == 0) {
+                                const uint32_t z = z_now.x & 0xFFu;
+                                z_lo = z | (z << 16);
+                                z_hi = z_lo << 4;
+                                z_now.x = __funnelshift_r(z_now.x, z_now.y, 8);
+                                z_now.y >>= 8;
+                                if ((++gi & 7) == 0) {
+                                    z_now = z_next;
+                                    z_next = zeros_of(gi + 8);
+                                }
+                            }
+                            const uint4 q = *reinterpret_cast<const uint4*>(row + (((4 * h + ci) ^ (lane & 7)) * 16));
+                            const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t u = ws[i] >> 8;
+                                v[16 * c + 4 * i] = sub2(ws[i] & 0x000F000Fu, z_lo);
+                                v[16 * c + 4 * i + 1] = sub2(u & 0x000F000Fu, z_lo);
+                                v[16 * c + 4 * i + 2] = sub2(ws[i] & 0x00F000F0u, z_hi);
+                                v[16 * c + 4 * i + 3] = sub2(u & 0x00F000F0u, z_hi);
+                            }
+                        }
+                        tmem_store32(tmem_a + (static_cast<uint32_t>(w * 32) << 16) + buf * 64 + s * 32, v);
+                    }
+                    tmem_wait_store();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&bars.a_full[buf]);
+                    ++used;
+                }
+            }
+        }
+        copies_wait<0>();
+    } else if (warp == 8) {
+        // ---- products
+        if (lane == 0) {
+            constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
+            uint32_t used = 0, sums = 0;
+            bool ok = true;
+            for (int item = first; ok && item < items; item += step)
+                for (int b = 0; ok && b < nb; ++b, ++used) {
+                    const int buf = used & 1, xs = used % M::kX;
+                    ok = bar_wait(&bars.a_full[buf], (used >> 1) & 1, &bars.failed) &&
+                         bar_wait(&bars.x_full[xs], (used / M::kX) & 1, &bars.failed);
+                    if (!ok) break;
+                    const uint32_t x_at = shared_of(x_ring) + xs * M::kXBytes;
+                    for (int g = 0; g < per; ++g, ++sums) {
+                        const int slot = sums % M::kSums;
+                        ok = bar_wait(&bars.s_empty[slot], ((sums / M::kSums) & 1) ^ 1, &bars.failed);
+                        if (!ok) break;
+                        fence_after();
+                        const int steps = a.group / 16;
+                        for (int k = 0; k < steps; ++k) {
+                            const int kk = g * steps + k;  // of the block's eight
+                            mma_f16(tmem + slot * N, tmem_a + buf * 64 + kk * 8,
+                                    operand_at(x_at + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc, k != 0);
+                        }
+                        commit_to(&bars.s_full[slot]);
+                    }
+                    if (!ok) break;
+                    commit_to(&bars.a_empty[buf]);
+                    commit_to(&bars.x_empty[xs]);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- x
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            uint32_t used = 0;
+            bool ok = true;
+            for (int item = first; ok && item < items; item += step) {
+                const uint8_t* src = static_cast<const uint8_t*>(a.x_ready) +
+                                     (static_cast<size_t>(item % a.halves) * a.blocks + b0) * M::kXBytes;
+                for (int b = 0; b < nb; ++b, ++used) {
+                    const int xs = used % M::kX;
+                    ok = bar_wait(&bars.x_empty[xs], ((used / M::kX) & 1) ^ 1, &bars.failed);
+                    if (!ok) break;
+                    bar_expect(&bars.x_full[xs], M::kXBytes);
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            shared_of(x_ring) + xs * M::kXBytes),
+                        "l"(src + static_cast<size_t>(b) * M::kXBytes), "r"(M::kXBytes), "r"(shared_of(&bars.x_full[xs]))
+                        : "memory");
+                }
+            }
+            // a failed block still waits for its copies in flight before its memory goes away
+            if (!ok)
+                for (int i = 0; i < M::kX && used > 0; ++i) {
+                    const uint32_t u = used - 1 - i;
+                    if (u >= used) break;
+                    uint32_t quiet = 0;
+                    bar_wait(&bars.x_full[u % M::kX], (u / M::kX) & 1, &quiet);
+                }
+        }
+        __syncwarp();
+    } else {
+        // ---- group sums: a thread for each weight row
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        uint32_t sums = 0;
+        bool ok = true;
+        for (int item = first; item < items; item += step) {
+            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + tid;
+            const uint16_t* scale_at = static_cast<const uint16_t*>(a.scales) + (n < a.outs ? n : 0) * a.groups;
+            auto scales_of = [&](int g) {  // eight of them ahead
+                uint4 s = make_uint4(0u, 0u, 0u, 0u);
+                if (g < a.groups) {
+                    if (a.s_vec) {
+                        s = __ldg(reinterpret_cast<const uint4*>(scale_at + g));
+                    } else {
+                        uint32_t b[4] = {0, 0, 0, 0};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (g + i < a.groups) b[i >> 1] |= static_cast<uint32_t>(__ldg(scale_at + g + i)) << (16 * (i & 1));
+                        s = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                }
+                return s;
+            };
+            float2 y[N / 2];
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) y[i] = make_float2(0.0f, 0.0f);
+            int gi = b0 * per;
+            uint4 now = scales_of(gi & ~7), next = scales_of((gi & ~7) + 8);
+            auto shift = [&]() {
+                now.x = __funnelshift_r(now.x, now.y, 16);
+                now.y = __funnelshift_r(now.y, now.z, 16);
+                now.z = __funnelshift_r(now.z, now.w, 16);
+                now.w >>= 16;
+            };
+            for (int i = 0; i < (gi & 7); ++i) shift();
+            const int end = gi + nb * per;
+            for (; ok && gi < end; ++sums) {
+                const uint32_t bits = now.x & 0xFFFFu;
+                const float s = a.x_bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(bits));
+                shift();
+                if ((++gi & 7) == 0) {
+                    now = next;
+                    next = scales_of(gi + 8);
+                }
+                const int slot = sums % M::kSums;
+                ok = bar_wait(&bars.s_full[slot], (sums / M::kSums) & 1, &bars.failed);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                fence_after();
+                // past the last group the weights are copied as zeros and x is zero, whatever the scale
+                const float ss = gi - 1 < a.groups ? s : 0.0f;
+                const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + slot * N;
+#pragma unroll
+                for (int c = 0; c < N; c += 16) {
+                    uint32_t d[16];
+                    tmem_load16(at + c, d);
+                    tmem_wait_load();
+                    if (c + 16 == N) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&bars.s_empty[slot]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float2& acc = y[c / 2 + i];
+                        acc.x = fmaf(ss, __uint_as_float(d[2 * i]), acc.x);
+                        acc.y = fmaf(ss, __uint_as_float(d[2 * i + 1]), acc.y);
+                    }
+                }
+            }
+            if (!ok) {
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) y[i] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+            }
+            const int m0 = (item % a.halves) * N;
+            if (a.cluster == 1) {
+                if (n < a.outs) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int m = m0 + i;
+                        if (m < a.rows) {
+                            const float v = ((i & 1) ? y[i / 2].y : y[i / 2].x) * 0x1p24f * __ldg(a.x_back + m);
+                            const int64_t o = m * a.y_stride + n;
+                            if (a.y_f32)
+                                static_cast<float*>(a.y)[o] = v;
+                            else if (a.x_bf16)
+                                static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+                            else
+                                static_cast<__half*>(a.y)[o] = __float2half_rn(v);
+                        }
+                    }
+                }
+            } else {
+                // every copy and product of this block is done: the rings give way to the block's sums
+                float* mine = reinterpret_cast<float*>(dyn);
+#pragma unroll
+                for (int i = 0; i < N; ++i) mine[i * 128 + tid] = (i & 1) ? y[i / 2].y : y[i / 2].x;
+            }
+        }
+    }
+    __syncthreads();
+    if (a.cluster > 1) {
+        // one item a cluster: each block adds up its share of the rows of x
+        cluster_sync_all();
+        const int item = first;
+        const int m0 = (item % a.halves) * N;
+        for (int i = rank * N * 128 / a.cluster + tid; i < (rank + 1) * N * 128 / a.cluster; i += kThreads) {
+            const int m = m0 + i / 128;
+            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + i % 128;
+            if (m >= a.rows || n >= a.outs) continue;
+            float v = 0.0f;
+            for (int c = 0; c < a.cluster; ++c) {
+                uint32_t remote;
+                float p;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(shared_of(dyn) + i * 4), "r"(c));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(remote));
+                v += p;
+            }
+            v = v * 0x1p24f * __ldg(a.x_back + m);
+            const int64_t o = m * a.y_stride + n;
+            if (a.y_f32)
+                static_cast<float*>(a.y)[o] = v;
+            else if (a.x_bf16)
+                static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
+            else
+                static_cast<__half*>(a.y)[o] = __float2half_rn(v);
+        }
+        __syncwarp();
+        cluster_sync_all();  // no block leaves while another reads its memory
+    }
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(M::kColumns) : "memory");
+}
+
+template <int N>
+int launch(const ManyArgs& a, int dev, int sms, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    static_assert(Many<N>::kSmem + sizeof(Bars) <= arc::kSmemPerBlock, "shared memory");
+    static_assert(Many<N>::kSums * N + Many<N>::kA * 64 <= Many<N>::kColumns, "tensor memory");
+    if (arc::prepare(many_kernel<N>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
+    const unsigned rows = static_cast<unsigned>(a.halves * a.columns);
+    if (a.x_bf16)
+        many_x_kernel<ARC_BF16><<<rows, 256, 0, st>>>(a);
+    else
+        many_x_kernel<ARC_F16><<<rows, 256, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return ARC_E_CUDA;
+    const int items = a.tiles * a.halves;
+    const int64_t grid = a.cluster > 1 ? int64_t{items} * a.cluster : (items < sms ? items : sms);
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Many<N>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, many_kernel<N>, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    return ARC_OK;
+}
+
+int columns_of(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+}  // namespace
+
+size_t many_workspace(int64_t ins, int64_t rows) {
+    const int64_t columns = columns_of(rows), halves = (rows + columns - 1) / columns;
+    const int64_t blocks = (ins + kInner - 1) / kInner;
+    return static_cast<size_t>(halves * columns * blocks * kInner * 2 + halves * columns * 4);
+}
+
+int launch_many(ManyArgs a, void* workspace, int dev, int sms, cudaStream_t st) {
+    a.columns = columns_of(a.rows);
+    a.halves = (a.rows + a.columns - 1) / a.columns;
+    a.blocks = (a.ins + kInner - 1) / kInner;
+    a.groups = a.ins / a.group;
+    a.tiles = static_cast<int32_t>((a.outs + 127) / 128);
+    a.x_ready = workspace;
+    a.x_back = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        static_cast<size_t>(a.halves) * a.columns * a.blocks * kInner * 2);
+    a.x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
+    a.s_vec = reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 && a.groups % 8 == 0;
+    a.z_vec = reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0 && a.groups % 8 == 0;
+    // few tiles: split the inner dimension while every block keeps four blocks of it and all run at once
+    a.cluster = 1;
+    while (a.cluster < 8 && int64_t{a.tiles} * a.halves * a.cluster * 2 <= sms && a.blocks >= a.cluster * 8) a.cluster *= 2;
+    if (a.columns == 16) return launch<16>(a, dev, sms, st);
+    if (a.columns == 32) return launch<32>(a, dev, sms, st);
+    if (a.columns == 64) return launch<64>(a, dev, sms, st);
+    return launch<128>(a, dev, sms, st);
+}
+
+}  // namespace arcs

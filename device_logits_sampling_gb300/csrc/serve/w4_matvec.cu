@@ -7,12 +7,11 @@
 #include "launch_util.cuh"
 #include "serve/arc_w4.h"
 #include "serve_util.cuh"
+#include "w4_many.cuh"
 
 namespace {
 
 using namespace arcs;
-
-constexpr int kThreads = 256;
 
 struct W4Args {
     arc_w4_weight w;
@@ -23,41 +22,6 @@ struct W4Args {
     int32_t y_f32;
     int32_t x_bf16;
 };
-
-// One warp for each output column, the rows in turn: a lane takes eight
-// weights (one 32-bit word) of every 256, whose group is one.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) w4_kernel(const __grid_constant__ W4Args a) {
-    using T = typename Half<DT>::T;
-    const int lane = threadIdx.x & 31;
-    const int64_t n = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    if (n >= a.w.outs) return;
-    const int groups = a.w.ins / a.w.group;
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const char*>(a.w.q) + n * a.w.row_bytes);
-    const T* s = static_cast<const T*>(a.w.scales) + n * groups;
-    const uint8_t* z = a.w.zeros ? a.w.zeros + n * groups : nullptr;
-    for (int m = 0; m < a.rows; ++m) {
-        const T* x = static_cast<const T*>(a.x) + m * a.x_stride;
-        float sum = 0.0f;
-        for (int k = lane * 8; k < a.w.ins; k += 256) {
-            const int g = k / a.w.group;
-            const uint32_t w = __ldg(q + (k >> 3));
-            const int zero = z ? z[g] : 8;
-            float part = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                part = fmaf(Half<DT>::to_float(x[k + i]), static_cast<float>(static_cast<int>((w >> (4 * i)) & 15) - zero), part);
-            sum = fmaf(part, Half<DT>::to_float(s[g]), sum);
-        }
-        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, i);
-        if (lane == 0) {
-            if (a.y_f32)
-                static_cast<float*>(a.y)[m * a.y_stride + n] = sum;
-            else
-                static_cast<T*>(a.y)[m * a.y_stride + n] = Half<DT>::from_float(sum);
-        }
-    }
-}
 
 // ------------------------------------------------------------------ few rows
 // 1 .. 16 rows of x: fp16 matrix instructions with 16 weight rows on the long
@@ -94,6 +58,7 @@ struct FewArgs {
     int32_t stages;   // 2, 3 or 4
     int32_t cluster;  // blocks that share a tile
     int32_t tiles;
+    int32_t period;   // tiles between joins
     int32_t x_vec;
     // shared-memory layout, bytes
     int32_t x_off, xs_off, scale_off, red_off, join_off, up_off;
@@ -109,8 +74,7 @@ __device__ __forceinline__ void copies_wait() {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -194,20 +158,9 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
 }
 
 template <int N>
-struct Words {
+struct alignas(4 * N) Words {
     uint32_t w[N];
 };
-__device__ __forceinline__ void load_words(uint32_t p, Words<4>& x) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]) : "r"(p));
-}
-__device__ __forceinline__ void load_words(uint32_t p, Words<2>& x) {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.w[0]), "=r"(x.w[1]) : "r"(p));
-}
-__device__ __forceinline__ void load_words(uint32_t p, Words<1>& x) {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.w[0]) : "r"(p));
-}
-
 // G: group. NT: tiles of 8 rows of x. P: inner values of a part at most (512 or
 // 256). Z: zero points are given.
 template <int G, int NT, int P, bool Z>
@@ -299,7 +252,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 
     const uint32_t read_at = g * PITCH;
     const uint32_t gbits = row_bits(g) * 16;  // those of row g + 8 too
-    int stage = 0, turn = 0;
+    int stage = 0, turn = 0, count = 0;
     for (int tile = first_tile; tile < f.tiles; tile += tile_step) {
         if (f.stages == 2)
             copies_wait<0>();
@@ -324,16 +277,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[nt][e] = 0.0f;
-        const uint32_t st = ring + stage * STAGE + read_at;
+        const uint8_t* st = dyn + (warp * f.stages + stage) * STAGE + read_at;
         stage = stage + 1 == f.stages ? 0 : stage + 1;
         auto one_group = [&](int gi) {
-            Words<WG> w0, w1;
             // chunk of the lane's words and the byte within it
             const int c = WG == 4 ? gi * 4 + t : WG == 2 ? gi * 2 + (t >> 1) : gi;
             const int o = WG == 4 ? 0 : WG == 2 ? (t & 1) * 8 : t * 4;
-            const uint32_t at = st + ((c * 16) ^ gbits) + o;
-            load_words(at, w0);
-            load_words(at + 8 * PITCH, w1);
+            const uint8_t* at = st + ((c * 16) ^ gbits) + o;
+            const Words<WG> w0 = *reinterpret_cast<const Words<WG>*>(at);
+            const Words<WG> w1 = *reinterpret_cast<const Words<WG>*>(at + 8 * PITCH);
             float acc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -377,33 +329,38 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             for (int gi = 0; gi < pg; ++gi) one_group(gi);
         }
 
-        // join the parts (and the cluster's slices); a value for each (weight row, row of x).
-        // Two buffers in turn: one barrier a tile.
-        constexpr int kVals = 16 * 8 * NT;
-        float* red = reinterpret_cast<float*>(dyn + f.red_off) + turn * kFewWarps * kVals;
-        float* mine = red + warp * kVals;
+        // Join the parts (and the cluster's slices): each warp leaves its sums, [row of x][weight row], in the
+        // tile's slot; after f.period tiles the warps of a row group meet and add them. Two sets of slots in
+        // turn: one barrier a period.
+        const int vals = 16 * a.rows;
+        float* mine = reinterpret_cast<float*>(dyn + f.red_off) + ((turn * f.period + count) * kFewWarps + warp) * vals;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            // [row of x][weight row]
-            if (8 * nt + 2 * t < a.rows) {
-                mine[(8 * nt + 2 * t) * 16 + g] = y[nt][0];
-                mine[(8 * nt + 2 * t) * 16 + g + 8] = y[nt][2];
-                mine[(8 * nt + 2 * t + 1) * 16 + g] = y[nt][1];
-                mine[(8 * nt + 2 * t + 1) * 16 + g + 8] = y[nt][3];
+            const int m = 8 * nt + 2 * t;
+            if (m < a.rows) {
+                mine[m * 16 + g] = y[nt][0];
+                mine[m * 16 + g + 8] = y[nt][2];
+            }
+            if (m + 1 < a.rows) {
+                mine[m * 16 + 16 + g] = y[nt][1];
+                mine[m * 16 + 16 + g + 8] = y[nt][3];
             }
         }
+        ++count;
+        if (count < f.period && tile + tile_step < f.tiles) continue;
         if (f.parts == 1)
             __syncwarp();
         else
             asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(f.parts * 32) : "memory");
-        const float* group = red + sub * f.parts * kVals;
-        const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;
+        const float* red = reinterpret_cast<const float*>(dyn + f.red_off) + (turn * f.period * kFewWarps + sub * f.parts) * vals;
         const float* up = reinterpret_cast<const float*>(dyn + f.up_off);
+        const int64_t n0 = static_cast<int64_t>(tile) * per_tile + sub * 16;  // the last tile's
         auto finish = [&](int i, float v) {
-            const int m = i >> 4, r = i & 15;
-            if (n0 + r >= a.w.outs) return;
+            const int c = i / vals, m = (i - c * vals) >> 4, r = i & 15;
+            const int64_t n = n0 + r - static_cast<int64_t>(count - 1 - c) * tile_step * per_tile;
+            if (n >= a.w.outs) return;
             v = v * 0x1p24f;
-            const int64_t at = m * a.y_stride + n0 + r;
+            const int64_t at = m * a.y_stride + n;
             if (a.y_f32)
                 static_cast<float*>(a.y)[at] = v;
             else if (a.x_bf16)
@@ -411,16 +368,20 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             else
                 static_cast<__half*>(a.y)[at] = __float2half_rn(v);
         };
-        for (int i = part * 32 + lane; i < a.rows * 16; i += f.parts * 32) {
+        const int join_at = (turn * f.cluster * (kFewWarps / f.parts) + sub) * f.period * vals;  // of rank 0
+        const int join_rank = (kFewWarps / f.parts) * f.period * vals;
+        for (int i = part * 32 + lane; i < count * vals; i += f.parts * 32) {
+            const int c = i / vals, e = i - c * vals;
+            const float* p = red + c * kFewWarps * vals + e;
             float v = 0.0f;
-            for (int p = 0; p < f.parts; ++p) v += group[p * kVals + i];
-            v = v / up[i >> 4];  // a power of two
+            for (int q = 0; q < f.parts; ++q) v += p[q * vals];
+            v = v / up[e >> 4];  // a power of two
             if (f.cluster == 1) {
                 finish(i, v);
             } else {
                 // into the first block's memory, a place for each rank
                 const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(
-                    dyn + f.join_off + (((turn * 8 + rank) * (kFewWarps / f.parts) + sub) * kVals + i) * 4));
+                    dyn + f.join_off + (join_at + rank * join_rank + i) * 4));
                 uint32_t remote;
                 asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(local));
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
@@ -430,14 +391,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             __syncwarp();
             cluster_sync_all();
             if (rank == 0)
-                for (int i = part * 32 + lane; i < a.rows * 16; i += f.parts * 32) {
+                for (int i = part * 32 + lane; i < count * vals; i += f.parts * 32) {
+                    const float* p = reinterpret_cast<const float*>(dyn + f.join_off) + join_at + i;
                     float v = 0.0f;
-                    for (int c = 0; c < f.cluster; ++c)
-                        v += reinterpret_cast<const float*>(dyn + f.join_off)[((turn * 8 + c) * (kFewWarps / f.parts) + sub) * kVals + i];
+                    for (int c = 0; c < f.cluster; ++c) v += p[c * join_rank];
                     finish(i, v);
                 }
         }
         turn ^= 1;
+        count = 0;
     }
     copies_wait<0>();
 }
@@ -502,17 +464,20 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
         f.x_off = take(a.rows * f.slice * 2);
         f.xs_off = take(groups * 8 * NT * 4);
         f.scale_off = take(kFewWarps * 16 * (most / G) * (a.w.zeros ? 8 : 4));
-        f.red_off = take(2 * kFewWarps * 16 * 8 * NT * 4);
-        f.join_off = take(f.cluster > 1 ? 2 * 8 * (kFewWarps / p) * 16 * 8 * NT * 4 : 0);
+        f.red_off = take(2 * f.period * kFewWarps * 16 * a.rows * 4);
+        f.join_off = take(f.cluster > 1 ? 2 * f.cluster * (kFewWarps / p) * f.period * 16 * a.rows * 4 : 0);
         f.up_off = take(8 * NT * 4);
         return off;
     };
+    f.period = 1;
     int best = 0;
     for (int p = parts; p <= kFewWarps && (p == parts || f.slice / p >= 128); p *= 2)
         if (layout(p, 2) <= arc::kSmemPerBlock && (best == 0 || cost_of(p) < cost_of(best))) best = p;
     if (best == 0) return ARC_E_UNSUPPORTED;
     int stages = 4;
     while (stages > 2 && layout(best, stages) > arc::kSmemPerBlock) --stages;
+    // what is left goes to rarer joins
+    for (f.period = 8; f.period > 1 && layout(best, stages) > arc::kSmemPerBlock;) f.period /= 2;
     const int off = layout(best, stages);
     parts = best;
     f.tiles = static_cast<int32_t>(tiles_of(parts));
@@ -532,6 +497,8 @@ int launch_few_group(const W4Args& a, int dev, int sms, cudaStream_t st) {
     return launch_few<32, NT>(a, dev, sms, st);
 }
 
+constexpr int kFewRows = 8;  // more rows take the 5th-generation tensor cores (w4_many.cu)
+
 int check_weight(const arc_w4_weight* w) {
     if (w == nullptr || w->q == nullptr || w->scales == nullptr) return ARC_E_NULL;
     if (w->group != 32 && w->group != 64 && w->group != 128) return ARC_E_UNSUPPORTED;
@@ -548,10 +515,13 @@ int check_weight(const arc_w4_weight* w) {
 
 extern "C" {
 
-size_t arc_w4_workspace_bytes(const arc_w4_weight*, int64_t) { return 0; }
+size_t arc_w4_workspace_bytes(const arc_w4_weight* weight, int64_t rows) {
+    if (check_weight(weight) != ARC_OK || rows <= kFewRows || rows > ARC_W4_MAX_ROWS) return 0;
+    return many_workspace(weight->ins, rows);
+}
 
 int arc_w4_matvec(const arc_w4_weight* weight, const void* x, int64_t rows, int64_t x_stride, int32_t x_dtype, void* y,
-                  int64_t y_stride, int32_t y_dtype, void*, size_t, void* stream) {
+                  int64_t y_stride, int32_t y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
     const int rc = check_weight(weight);
     if (rc != ARC_OK) return rc;
     if (x == nullptr || y == nullptr) return ARC_E_NULL;
@@ -560,6 +530,10 @@ int arc_w4_matvec(const arc_w4_weight* weight, const void* x, int64_t rows, int6
     if (rows <= 0 || rows > ARC_W4_MAX_ROWS || x_stride < weight->ins || y_stride < weight->outs) return ARC_E_SHAPE;
     if (reinterpret_cast<uintptr_t>(x) % 2 != 0 || reinterpret_cast<uintptr_t>(y) % (y_dtype == ARC_F32 ? 4 : 2) != 0)
         return ARC_E_ALIGN;
+    if (const size_t need = arc_w4_workspace_bytes(weight, rows)) {
+        if (workspace == nullptr || workspace_bytes < need) return ARC_E_WORKSPACE;
+        if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0) return ARC_E_ALIGN;
+    }
     W4Args a{*weight, x, y, x_stride, y_stride, static_cast<int32_t>(rows), y_dtype == ARC_F32,
              x_dtype == ARC_BF16};
     int dev = 0, sms = 0;
@@ -568,26 +542,24 @@ int arc_w4_matvec(const arc_w4_weight* weight, const void* x, int64_t rows, int6
         (void)cudaGetLastError();
         return ARC_E_CUDA;
     }
-    if (rows <= 16) {
-        cudaStream_t few = static_cast<cudaStream_t>(stream);
-        if (rows <= 8) return launch_few_group<1>(a, dev, sms, few);
-        // 16 rows reach 16,384 inner values in a cluster of 8 blocks
-        if (weight->ins <= 16384) return launch_few_group<2>(a, dev, sms, few);
-        W4Args first = a, second = a;
-        first.rows = 8;
-        second.rows = a.rows - 8;
-        second.x = static_cast<const char*>(x) + 8 * x_stride * 2;
-        second.y = static_cast<char*>(y) + 8 * y_stride * (a.y_f32 ? 4 : 2);
-        const int one = launch_few_group<1>(first, dev, sms, few);
-        return one != ARC_OK ? one : launch_few_group<1>(second, dev, sms, few);
-    }
-    const unsigned grid = static_cast<unsigned>((weight->outs * 32 + kThreads - 1) / kThreads);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (x_dtype == ARC_BF16)
-        w4_kernel<ARC_BF16><<<grid, kThreads, 0, st>>>(a);
-    else
-        w4_kernel<ARC_F16><<<grid, kThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
+    if (rows <= kFewRows) return launch_few_group<1>(a, dev, sms, st);
+    ManyArgs m{};
+    m.q = weight->q;
+    m.scales = weight->scales;
+    m.zeros = weight->zeros;
+    m.x = x;
+    m.y = y;
+    m.row_bytes = weight->row_bytes;
+    m.outs = weight->outs;
+    m.x_stride = x_stride;
+    m.y_stride = y_stride;
+    m.ins = weight->ins;
+    m.group = weight->group;
+    m.rows = static_cast<int32_t>(rows);
+    m.y_f32 = a.y_f32;
+    m.x_bf16 = a.x_bf16;
+    return launch_many(m, workspace, dev, sms, st);
 }
 
 }  // extern "C"
