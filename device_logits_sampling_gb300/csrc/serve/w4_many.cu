@@ -17,9 +17,9 @@
 // lie in tensor memory with the weight row as the lane, so its scale is one
 // number a thread and the running sums are the thread's registers.
 //
-// Roles of a block: warps 0-3 add up groups (and store the output), warps 4-7
-// copy and unpack weights, warp 8 issues the products, warp 9 copies x.  They
-// meet at barriers in shared memory: rings of unpacked A, of x and of group
+// Roles of a block: warps 0-3 add up groups (and store the output), warps 4-11
+// copy and unpack weights (two groups of four, taking turns), warp 12 issues the
+// products, warp 13 copies x.  They meet at barriers in shared memory: rings of unpacked A, of x and of group
 // sums, so that copying, unpacking, multiplying and adding up overlap across
 // groups and tiles.  Few tiles: the inner dimension is split over a cluster
 // whose blocks add each other's sums through distributed shared memory.
@@ -37,27 +37,30 @@
 namespace arcs {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 512;
+// registers of a thread once the roles part, of 128 at launch: adding up 64 or 128
+// columns takes most of them (208 + 2 * 104 + 40 <= 4 * 128)
+constexpr int kSumRegs = 208, kUnpackRegs = 104, kIssueRegs = 40;
 constexpr int kInner = 128;    // inner values of a block of A and x
 constexpr int kRawStage = 32 * 128;  // bytes of a warp's raw stage: 32 rows of 256 codes
 constexpr int kWaits = 1 << 24;
 
 template <int N>
 struct Many {
-    static constexpr int kSums = N == 128 ? 3 : 4;       // ring of group sums, N columns each
-    static constexpr int kA = 2;                         // ring of unpacked A, 64 columns each
+    static constexpr int kSums = N == 128 ? 2 : 4;       // ring of group sums, N columns each
+    static constexpr int kA = 4;                         // ring of unpacked A, 64 columns each
     static constexpr int kX = N == 128 ? 3 : 4;          // ring of x
-    static constexpr int kRaw = N == 128 ? 6 : 8;        // a warp's ring of raw weights
-    static constexpr int kColumns = N >= 64 ? 512 : 256; // tensor memory taken
+    static constexpr int kRaw = N == 128 ? 3 : 4;        // a warp's ring of raw weights
+    static constexpr int kColumns = 512; // tensor memory taken
     static constexpr int kXBytes = N * kInner * 2;
-    static constexpr int kRawBytes = 4 * kRaw * kRawStage;
+    static constexpr int kRawBytes = 8 * kRaw * kRawStage;
     static constexpr int kJoin = N * 128 * 4;            // over the rings, at the end
     static constexpr int kRings = kX * kXBytes + kRawBytes;
     static constexpr int kSmem = (kRings > kJoin ? kRings : kJoin) + 1024;
 };
 
 struct Bars {
-    uint64_t a_full[2], a_empty[2];
+    uint64_t a_full[4], a_empty[4];
     uint64_t x_full[4], x_empty[4];
     uint64_t s_full[4], s_empty[4];
     uint32_t tmem;
@@ -119,6 +122,20 @@ __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&x)[16]) {
         : "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&x)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : ARC_OUT8(x, 0), ARC_OUT8(x, 8), ARC_OUT8(x, 16), ARC_OUT8(x, 24)
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load64(uint32_t at, uint32_t (&x)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : ARC_OUT8(x, 0), ARC_OUT8(x, 8), ARC_OUT8(x, 16), ARC_OUT8(x, 24), ARC_OUT8(x, 32), ARC_OUT8(x, 40), ARC_OUT8(x, 48), ARC_OUT8(x, 56)
+        : "r"(at)
+        : "memory");
+}
 #undef ARC_OUT8
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -137,6 +154,20 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float half_of(uint64_t v, int i) {
+    return __uint_as_float(static_cast<uint32_t>(i ? v >> 32 : v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 // K-major operand in shared memory, rows of 128 bytes in swizzled groups of
@@ -216,11 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     uint8_t* const raw_ring = dyn + M::kX * M::kXBytes;
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             bar_init(&bars.a_full[i], 4);
             bar_init(&bars.a_empty[i], 1);
-        }
-        for (int i = 0; i < 4; ++i) {
             bar_init(&bars.x_full[i], 1);
             bar_init(&bars.x_empty[i], 1);
             bar_init(&bars.s_full[i], 1);
@@ -230,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 8) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_of(&bars.tmem)),
                      "n"(M::kColumns)
                      : "memory");
@@ -241,14 +270,19 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     fence_after();
     const uint32_t tmem = bars.tmem, tmem_a = tmem + M::kSums * N;
 
-    if (warp >= 4 && warp < 8) {
-        // ---- unpack: a thread for each weight row
-        const int w = warp - 4;
-        const uint32_t ring = shared_of(raw_ring) + w * M::kRaw * kRawStage;
-        const uint8_t* const ring_p = raw_ring + w * M::kRaw * kRawStage;
+    if (warp >= 4 && warp < 12) {
+        // ---- unpack: a thread for each weight row; the two groups take raw stages in turn
+        if constexpr (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kUnpackRegs));
+        const int w = warp & 3, turn = (warp >> 2) - 1;
+        const uint32_t ring = shared_of(raw_ring) + (warp - 4) * M::kRaw * kRawStage;
+        const uint8_t* const ring_p = raw_ring + (warp - 4) * M::kRaw * kRawStage;
         const int pairs = (nb + 1) / 2;  // raw stages of an item: two blocks each
-        int c_item = first, c_pair = 0, c_stage = 0;
+        int c_item = first, c_pair = turn, c_stage = 0;
         auto issue = [&]() {
+            while (c_pair >= pairs && c_item < items) {
+                c_pair -= pairs;
+                c_item += step;
+            }
             if (c_item < items) {
                 const int64_t n0 = static_cast<int64_t>(c_item / a.halves) * 128 + w * 32;
                 const int k = (b0 + 2 * c_pair) * kInner;         // first inner value
@@ -262,77 +296,67 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     const char* src = static_cast<const char*>(a.q) + (on ? (n0 + r) * a.row_bytes + k / 2 + c * 16 : 0);
                     copy16(ring + c_stage * kRawStage + r * 128 + ((c ^ (r & 7)) * 16), src, on);
                 }
-                if (++c_pair == pairs) {
-                    c_pair = 0;
-                    c_item += step;
-                }
+                c_pair += 2;
             }
             copies_end();
             c_stage = c_stage + 1 == M::kRaw ? 0 : c_stage + 1;
         };
         for (int i = 0; i < M::kRaw - 1; ++i) issue();
         int stage = 0;
-        uint32_t used = 0;  // blocks of A so far
+        uint32_t before = 0;  // blocks of the items before
+        int pair = turn;
         bool ok = true;
-        for (int item = first; ok && item < items; item += step) {
+        for (int item = first; ok && item < items; item += step, before += nb, pair -= pairs) {
             const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + w * 32 + lane;
             const uint8_t* zero_at = a.zeros && n < a.outs ? a.zeros + n * a.groups : nullptr;
-            int gi = b0 * per;
-            // eight zero points ahead in a register pair
+            // the zero points of a block's groups, one a byte; loaded a raw stage ahead
             auto zeros_of = [&](int g) {
-                uint2 z = make_uint2(0x08080808u, 0x08080808u);
-                if (zero_at && g < a.groups) {
-                    if (a.z_vec) {
-                        z = __ldg(reinterpret_cast<const uint2*>(zero_at + g));
-                    } else {
-                        uint32_t b[2] = {0, 0};
+                uint32_t z = 0x08080808u;
+                if (zero_at) {
+                    z = 0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (g + i < a.groups) b[i >> 2] |= static_cast<uint32_t>(__ldg(zero_at + g + i)) << (8 * (i & 3));
-                        z = make_uint2(b[0], b[1]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (i < per && g + i < a.groups) z |= static_cast<uint32_t>(__ldg(zero_at + g + i)) << (8 * i);
                 }
                 return z;
             };
-            uint2 z_now = zeros_of(gi & ~7), z_next = zeros_of((gi & ~7) + 8);
-            for (int i = 0; i < (gi & 7); ++i) {
-                z_now.x = __funnelshift_r(z_now.x, z_now.y, 8);
-                z_now.y >>= 8;
-            }
-            uint32_t z_lo = 0, z_hi = 0;
-            for (int pair = 0; ok && pair < pairs; ++pair) {
+            uint32_t z_now[2], z_next[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) z_next[h] = zeros_of((b0 + 2 * pair + h) * per);
+            for (; ok && pair < pairs; pair += 2) {
                 copies_wait<M::kRaw - 2>();
                 __syncwarp();
                 issue();
                 const uint8_t* row = ring_p + stage * kRawStage + lane * 128;
                 stage = stage + 1 == M::kRaw ? 0 : stage + 1;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    z_now[h] = z_next[h];
+                    z_next[h] = zeros_of((b0 + 2 * pair + 4 + h) * per);
+                }
+#pragma unroll 1
                 for (int h = 0; h < 2 && 2 * pair + h < nb; ++h) {
-                    const int buf = used & 1;
-                    ok = bar_wait(&bars.a_empty[buf], ((used >> 1) & 1) ^ 1, &bars.failed);
+                    const uint32_t used = before + 2 * pair + h;
+                    const int buf = used % M::kA;
+                    uint4 q[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) q[c] = *reinterpret_cast<const uint4*>(row + (((4 * h + c) ^ (lane & 7)) * 16));
+                    ok = bar_wait(&bars.a_empty[buf], ((used / M::kA) & 1) ^ 1, &bars.failed);
                     if (!__all_sync(0xFFFFFFFFu, ok)) {
                         ok = false;
                         break;
                     }
                     fence_after();
+                    const uint32_t zs = h ? z_now[1] : z_now[0];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         uint32_t v[32];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const int ci = 2 * s + c;  // chunk of 32 values within the block
-                            if ((ci * 32 & (a.group - 1)) == 0) {
-                                const uint32_t z = z_now.x & 0xFFu;
-                                z_lo = z | (z << 16);
-                                z_hi = z_lo << 4;
-                                z_now.x = __funnelshift_r(z_now.x, z_now.y, 8);
-                                z_now.y >>= 8;
-                                if ((++gi & 7) == 0) {
-                                    z_now = z_next;
-                                    z_next = zeros_of(gi + 8);
-                                }
-                            }
-                            const uint4 q = *reinterpret_cast<const uint4*>(row + (((4 * h + ci) ^ (lane & 7)) * 16));
-                            const uint32_t ws[4] = {q.x, q.y, q.z, q.w};
+                            const uint32_t z = (zs >> (8 * (ci * per / 4))) & 0xFFu;
+                            const uint32_t z_lo = z | (z << 16), z_hi = z_lo << 4;
+                            const uint32_t ws[4] = {q[ci].x, q[ci].y, q[ci].z, q[ci].w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const uint32_t u = ws[i] >> 8;
@@ -348,21 +372,22 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     fence_before();
                     __syncwarp();
                     if (lane == 0) bar_arrive(&bars.a_full[buf]);
-                    ++used;
                 }
             }
         }
         copies_wait<0>();
-    } else if (warp == 8) {
-        // ---- products
-        if (lane == 0) {
+    } else if (warp >= 12) {
+        // one instruction for the four warps that share it
+        if constexpr (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 12 && lane == 0) {
+            // ---- products
             constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
             uint32_t used = 0, sums = 0;
             bool ok = true;
             for (int item = first; ok && item < items; item += step)
                 for (int b = 0; ok && b < nb; ++b, ++used) {
-                    const int buf = used & 1, xs = used % M::kX;
-                    ok = bar_wait(&bars.a_full[buf], (used >> 1) & 1, &bars.failed) &&
+                    const int buf = used % M::kA, xs = used % M::kX;
+                    ok = bar_wait(&bars.a_full[buf], (used / M::kA) & 1, &bars.failed) &&
                          bar_wait(&bars.x_full[xs], (used / M::kX) & 1, &bars.failed);
                     if (!ok) break;
                     const uint32_t x_at = shared_of(x_ring) + xs * M::kXBytes;
@@ -384,10 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     commit_to(&bars.x_empty[xs]);
                 }
         }
-        __syncwarp();
-    } else if (warp == 9) {
-        // ---- x
-        if (lane == 0) {
+        if (warp == 13 && lane == 0) {
+            // ---- x
             asm volatile("griddepcontrol.wait;" ::: "memory");
             uint32_t used = 0;
             bool ok = true;
@@ -418,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         __syncwarp();
     } else {
         // ---- group sums: a thread for each weight row
+        if constexpr (N >= 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
         asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t sums = 0;
         bool ok = true;
@@ -439,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 }
                 return s;
             };
-            float2 y[N / 2];
+            uint64_t y[N / 2];  // pairs of columns
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) y[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < N / 2; ++i) y[i] = 0;
             int gi = b0 * per;
             uint4 now = scales_of(gi & ~7), next = scales_of((gi & ~7) + 8);
             auto shift = [&]() {
@@ -470,27 +494,31 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 // past the last group the weights are copied as zeros and x is zero, whatever the scale
                 const float ss = gi - 1 < a.groups ? s : 0.0f;
                 const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + slot * N;
+                constexpr int C = N < 64 ? N : 64;  // columns of a load
+                const uint64_t s2 = pack2(ss, ss);
 #pragma unroll
-                for (int c = 0; c < N; c += 16) {
-                    uint32_t d[16];
-                    tmem_load16(at + c, d);
+                for (int c = 0; c < N; c += C) {
+                    uint32_t d[C];
+                    if constexpr (C == 64)
+                        tmem_load64(at + c, d);
+                    else if constexpr (C == 32)
+                        tmem_load32(at + c, d);
+                    else
+                        tmem_load16(at + c, d);
                     tmem_wait_load();
-                    if (c + 16 == N) {
+                    if (c + C == N) {
                         fence_before();
                         __syncwarp();
                         if (lane == 0) bar_arrive(&bars.s_empty[slot]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2& acc = y[c / 2 + i];
-                        acc.x = fmaf(ss, __uint_as_float(d[2 * i]), acc.x);
-                        acc.y = fmaf(ss, __uint_as_float(d[2 * i + 1]), acc.y);
-                    }
+                    for (int i = 0; i < C / 2; ++i)
+                        y[c / 2 + i] = fma2(s2, pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), y[c / 2 + i]);
                 }
             }
             if (!ok) {
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) y[i] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+                for (int i = 0; i < N / 2; ++i) y[i] = 0x7FC000007FC00000ull;
             }
             const int m0 = (item % a.halves) * N;
             if (a.cluster == 1) {
@@ -499,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     for (int i = 0; i < N; ++i) {
                         const int m = m0 + i;
                         if (m < a.rows) {
-                            const float v = ((i & 1) ? y[i / 2].y : y[i / 2].x) * 0x1p24f * __ldg(a.x_back + m);
+                            const float v = half_of(y[i / 2], i & 1) * 0x1p24f * __ldg(a.x_back + m);
                             const int64_t o = m * a.y_stride + n;
                             if (a.y_f32)
                                 static_cast<float*>(a.y)[o] = v;
@@ -514,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 // every copy and product of this block is done: the rings give way to the block's sums
                 float* mine = reinterpret_cast<float*>(dyn);
 #pragma unroll
-                for (int i = 0; i < N; ++i) mine[i * 128 + tid] = (i & 1) ? y[i / 2].y : y[i / 2].x;
+                for (int i = 0; i < N; ++i) mine[i * 128 + tid] = half_of(y[i / 2], i & 1);
             }
         }
     }
@@ -548,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         __syncwarp();
         cluster_sync_all();  // no block leaves while another reads its memory
     }
-    if (warp == 8)
+    if (warp == 12)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(M::kColumns) : "memory");
 }
 
@@ -609,7 +637,6 @@ int launch_many(ManyArgs a, void* workspace, int dev, int sms, cudaStream_t st) 
                                         static_cast<size_t>(a.halves) * a.columns * a.blocks * kInner * 2);
     a.x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
     a.s_vec = reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 && a.groups % 8 == 0;
-    a.z_vec = reinterpret_cast<uintptr_t>(a.zeros) % 8 == 0 && a.groups % 8 == 0;
     // few tiles: split the inner dimension while every block keeps four blocks of it and all run at once
     a.cluster = 1;
     while (a.cluster < 8 && int64_t{a.tiles} * a.halves * a.cluster * 2 <= sms && a.blocks >= a.cluster * 8) a.cluster *= 2;

@@ -19,7 +19,7 @@ struct ManyArgs {
     int32_t columns;  // rows of x of a product
     int32_t halves;   // products that cover the rows
     int32_t blocks;   // 128 inner values each
-    int32_t groups, tiles, cluster, x_vec, s_vec, z_vec;
+    int32_t groups, tiles, cluster, x_vec, s_vec;
     void* x_ready;
     float* x_back;
 };
