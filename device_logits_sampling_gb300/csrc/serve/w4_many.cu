@@ -177,6 +177,57 @@ __device__ __forceinline__ uint64_t operand_at(uint32_t shared) {
            (uint64_t{1} << 46) | (uint64_t{2} << 61);
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The products of all items, by one thread: for each block of 128 inner values
+// its groups, each into the next slot of the ring of sums.
+template <int N, int G>
+__device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint32_t tmem, uint32_t tmem_a, int first, int step,
+                                               int items, int nb) {
+    using M = Many<N>;
+    constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
+    constexpr int kSteps = G / 16;
+    const uint64_t x0 = operand_at(x_ring);
+    uint32_t buf = 0, buf_phase = 0, xs = 0, xs_phase = 0, slot = 0, slot_phase = 1;
+    for (int item = first; item < items; item += step)
+        for (int b = 0; b < nb; ++b) {
+            if (!bar_wait(&bars.a_full[buf], buf_phase, &bars.failed) || !bar_wait(&bars.x_full[xs], xs_phase, &bars.failed)) return;
+            // addresses count 16 bytes
+            const uint64_t x_at = x0 + xs * (M::kXBytes / 16);
+            const uint32_t a_at = tmem_a + buf * 64;
+#pragma unroll
+            for (int g = 0; g < kInner / G; ++g) {
+                if (!bar_wait(&bars.s_empty[slot], slot_phase, &bars.failed)) return;
+                fence_after();
+                const uint32_t d = tmem + slot * N;
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    const int kk = g * kSteps + k;  // of the block's eight
+                    mma_f16(d, a_at + kk * 8, x_at + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc, k != 0);
+                }
+                commit_to(&bars.s_full[slot]);
+                if (++slot == M::kSums) {
+                    slot = 0;
+                    slot_phase ^= 1;
+                }
+            }
+            commit_to(&bars.a_empty[buf]);
+            commit_to(&bars.x_empty[xs]);
+            if (++buf == M::kA) {
+                buf = 0;
+                buf_phase ^= 1;
+            }
+            if (++xs == M::kX) {
+                xs = 0;
+                xs_phase ^= 1;
+            }
+        }
+}
+
 // ------------------------------------------------------------------ x
 // One block for each row (and each row of padding): fp16, scaled by a power of
 // two to [2^14, 2^15), in the order of the unpacked pairs: a word of eight
@@ -379,37 +430,16 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     } else if (warp >= 12) {
         // one instruction for the four warps that share it
         if constexpr (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 12 && lane == 0) {
+        if (warp == 12 && elect_one()) {
             // ---- products
-            constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
-            uint32_t used = 0, sums = 0;
-            bool ok = true;
-            for (int item = first; ok && item < items; item += step)
-                for (int b = 0; ok && b < nb; ++b, ++used) {
-                    const int buf = used % M::kA, xs = used % M::kX;
-                    ok = bar_wait(&bars.a_full[buf], (used / M::kA) & 1, &bars.failed) &&
-                         bar_wait(&bars.x_full[xs], (used / M::kX) & 1, &bars.failed);
-                    if (!ok) break;
-                    const uint32_t x_at = shared_of(x_ring) + xs * M::kXBytes;
-                    for (int g = 0; g < per; ++g, ++sums) {
-                        const int slot = sums % M::kSums;
-                        ok = bar_wait(&bars.s_empty[slot], ((sums / M::kSums) & 1) ^ 1, &bars.failed);
-                        if (!ok) break;
-                        fence_after();
-                        const int steps = a.group / 16;
-                        for (int k = 0; k < steps; ++k) {
-                            const int kk = g * steps + k;  // of the block's eight
-                            mma_f16(tmem + slot * N, tmem_a + buf * 64 + kk * 8,
-                                    operand_at(x_at + (kk >> 2) * (N * 128) + (kk & 3) * 32), idesc, k != 0);
-                        }
-                        commit_to(&bars.s_full[slot]);
-                    }
-                    if (!ok) break;
-                    commit_to(&bars.a_empty[buf]);
-                    commit_to(&bars.x_empty[xs]);
-                }
+            if (a.group == 128)
+                issue_products<N, 128>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
+            else if (a.group == 64)
+                issue_products<N, 64>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
+            else
+                issue_products<N, 32>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
         }
-        if (warp == 13 && lane == 0) {
+        if (warp == 13 && elect_one()) {
             // ---- x
             asm volatile("griddepcontrol.wait;" ::: "memory");
             uint32_t used = 0;
