@@ -17,9 +17,9 @@
 // lie in tensor memory with the weight row as the lane, so its scale is one
 // number a thread and the running sums are the thread's registers.
 //
-// Roles of a block: warps 0-3 add up groups (and store the output), warps 4-11
-// copy and unpack weights (two groups of four, taking turns), warp 12 issues the
-// products, warp 13 copies x.  They meet at barriers in shared memory: rings of unpacked A, of x and of group
+// Roles of a block: one or two groups of four warps add up group sums (and store
+// the output), each its share of the columns; two groups of four copy and unpack
+// weights, taking turns; a warp issues the products and one copies x.  They meet at barriers in shared memory: rings of unpacked A, of x and of group
 // sums, so that copying, unpacking, multiplying and adding up overlap across
 // groups and tiles.  Few tiles: the inner dimension is split over a cluster
 // whose blocks add each other's sums through distributed shared memory.
@@ -37,16 +37,19 @@
 namespace arcs {
 namespace {
 
-constexpr int kThreads = 512;
-// registers of a thread once the roles part, of 128 at launch: adding up 64 or 128
-// columns takes most of them (208 + 2 * 104 + 40 <= 4 * 128)
-constexpr int kSumRegs = 208, kUnpackRegs = 104, kIssueRegs = 40;
 constexpr int kInner = 128;    // inner values of a block of A and x
 constexpr int kRawStage = 32 * 128;  // bytes of a warp's raw stage: 32 rows of 256 codes
 constexpr int kWaits = 1 << 24;
 
 template <int N>
 struct Many {
+    // 64 columns and more are added up by two groups of warps: one took 1,100 clocks for the 128 sums of a row,
+    // the products 512
+    static constexpr int kAdders = N >= 64 ? 2 : 1;
+    static constexpr int kThreads = (kAdders + 3) * 128;
+    static constexpr int kCols = N / kAdders;            // columns of a group of warps
+    // registers of a thread once the roles part, of 96 at the launch of 640: 128 + 128 + 88 + 88 + 40 <= 5 * 96
+    static constexpr int kAddRegs = 128, kUnpackRegs = 88, kIssueRegs = 40;
     static constexpr int kSums = N == 128 ? 2 : 4;       // ring of group sums, N columns each
     static constexpr int kA = 4;                         // ring of unpacked A, 64 columns each
     static constexpr int kX = N == 128 ? 3 : 4;          // ring of x
@@ -92,6 +95,19 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, uint32_t*
     }
     *static_cast<volatile uint32_t*>(failed) = 1;
     return false;
+}
+// The same by a warp, all lanes together.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, uint32_t* failed) {
+    return __all_sync(0xFFFFFFFFu, bar_wait(b, parity, failed));
+}
+// One look at the barrier, whose answer may come while other work is issued.
+__device__ __forceinline__ uint32_t bar_done(uint64_t* b, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done)
+                 : "r"(shared_of(b)), "r"(parity)
+                 : "memory");
+    return done;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -193,15 +209,19 @@ __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint
     constexpr int kSteps = G / 16;
     const uint64_t x0 = operand_at(x_ring);
     uint32_t buf = 0, buf_phase = 0, xs = 0, xs_phase = 0, slot = 0, slot_phase = 1;
+    // a look at a barrier takes 240 clocks beside the copies and loads of the other warps, even at a finished
+    // phase: the next block's are under way while this block's products are issued
+    uint32_t a_ready = 0, x_ready = 0, s_ready = 0;
     for (int item = first; item < items; item += step)
         for (int b = 0; b < nb; ++b) {
-            if (!bar_wait(&bars.a_full[buf], buf_phase, &bars.failed) || !bar_wait(&bars.x_full[xs], xs_phase, &bars.failed)) return;
+            if (!a_ready && !bar_wait(&bars.a_full[buf], buf_phase, &bars.failed)) return;
+            if (!x_ready && !bar_wait(&bars.x_full[xs], xs_phase, &bars.failed)) return;
             // addresses count 16 bytes
             const uint64_t x_at = x0 + xs * (M::kXBytes / 16);
             const uint32_t a_at = tmem_a + buf * 64;
 #pragma unroll
             for (int g = 0; g < kInner / G; ++g) {
-                if (!bar_wait(&bars.s_empty[slot], slot_phase, &bars.failed)) return;
+                if (!s_ready && !bar_wait(&bars.s_empty[slot], slot_phase, &bars.failed)) return;
                 fence_after();
                 const uint32_t d = tmem + slot * N;
 #pragma unroll
@@ -214,6 +234,7 @@ __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint
                     slot = 0;
                     slot_phase ^= 1;
                 }
+                s_ready = bar_done(&bars.s_empty[slot], slot_phase);
             }
             commit_to(&bars.a_empty[buf]);
             commit_to(&bars.x_empty[xs]);
@@ -225,6 +246,8 @@ __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint
                 xs = 0;
                 xs_phase ^= 1;
             }
+            a_ready = bar_done(&bars.a_full[buf], buf_phase);
+            x_ready = bar_done(&bars.x_full[xs], xs_phase);
         }
 }
 
@@ -281,11 +304,12 @@ __global__ void __launch_bounds__(256) many_x_kernel(const __grid_constant__ Man
 
 // ------------------------------------------------------------------ products
 template <int N>
-__global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant__ ManyArgs a) {
+__global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid_constant__ ManyArgs a) {
     using M = Many<N>;
     extern __shared__ uint8_t raw_smem[];
     __shared__ Bars bars;
     uint8_t* const dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
+    constexpr int kUnpack = M::kAdders * 4, kIssue = kUnpack + 8;  // first warps of the roles
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x) % a.cluster;
     const int first = static_cast<int>(blockIdx.x) / a.cluster, step = static_cast<int>(gridDim.x) / a.cluster;
@@ -304,13 +328,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
             bar_init(&bars.x_full[i], 1);
             bar_init(&bars.x_empty[i], 1);
             bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.s_empty[i], 4);
+            bar_init(&bars.s_empty[i], 4 * M::kAdders);
         }
         bars.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == kIssue) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_of(&bars.tmem)),
                      "n"(M::kColumns)
                      : "memory");
@@ -321,12 +345,12 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
     fence_after();
     const uint32_t tmem = bars.tmem, tmem_a = tmem + M::kSums * N;
 
-    if (warp >= 4 && warp < 12) {
+    if (warp >= kUnpack && warp < kIssue) {
         // ---- unpack: a thread for each weight row; the two groups take raw stages in turn
-        if constexpr (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kUnpackRegs));
-        const int w = warp & 3, turn = (warp >> 2) - 1;
-        const uint32_t ring = shared_of(raw_ring) + (warp - 4) * M::kRaw * kRawStage;
-        const uint8_t* const ring_p = raw_ring + (warp - 4) * M::kRaw * kRawStage;
+        if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::kUnpackRegs));
+        const int w = warp & 3, turn = (warp - kUnpack) >> 2;
+        const uint32_t ring = shared_of(raw_ring) + (warp - kUnpack) * M::kRaw * kRawStage;
+        const uint8_t* const ring_p = raw_ring + (warp - kUnpack) * M::kRaw * kRawStage;
         const int pairs = (nb + 1) / 2;  // raw stages of an item: two blocks each
         int c_item = first, c_pair = turn, c_stage = 0;
         auto issue = [&]() {
@@ -392,11 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     uint4 q[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) q[c] = *reinterpret_cast<const uint4*>(row + (((4 * h + c) ^ (lane & 7)) * 16));
-                    ok = bar_wait(&bars.a_empty[buf], ((used / M::kA) & 1) ^ 1, &bars.failed);
-                    if (!__all_sync(0xFFFFFFFFu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(&bars.a_empty[buf], ((used / M::kA) & 1) ^ 1, &bars.failed);
+                    if (!ok) break;
                     fence_after();
                     const uint32_t zs = h ? z_now[1] : z_now[0];
 #pragma unroll
@@ -427,10 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
             }
         }
         copies_wait<0>();
-    } else if (warp >= 12) {
+    } else if (warp >= kIssue) {
         // one instruction for the four warps that share it
-        if constexpr (N >= 64) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 12 && elect_one()) {
+        if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::kIssueRegs));
+        if (warp == kIssue && elect_one()) {
             // ---- products
             if (a.group == 128)
                 issue_products<N, 128>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
@@ -439,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
             else
                 issue_products<N, 32>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
         }
-        if (warp == 13 && elect_one()) {
+        if (warp == kIssue + 1 && elect_one()) {
             // ---- x
             asm volatile("griddepcontrol.wait;" ::: "memory");
             uint32_t used = 0;
@@ -471,12 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         __syncwarp();
     } else {
         // ---- group sums: a thread for each weight row
-        if constexpr (N >= 64) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+        if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(M::kAddRegs));
+        constexpr int C = M::kCols;
+        const int c0 = (warp >> 2) * C, row = tid & 127;  // its columns, its weight row
         asm volatile("griddepcontrol.wait;" ::: "memory");
         uint32_t sums = 0;
         bool ok = true;
         for (int item = first; item < items; item += step) {
-            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + tid;
+            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + row;
             const uint16_t* scale_at = static_cast<const uint16_t*>(a.scales) + (n < a.outs ? n : 0) * a.groups;
             auto scales_of = [&](int g) {  // eight of them ahead
                 uint4 s = make_uint4(0u, 0u, 0u, 0u);
@@ -493,9 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 }
                 return s;
             };
-            uint64_t y[N / 2];  // pairs of columns
+            uint64_t y[C / 2];  // pairs of columns
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) y[i] = 0;
+            for (int i = 0; i < C / 2; ++i) y[i] = 0;
             int gi = b0 * per;
             uint4 now = scales_of(gi & ~7), next = scales_of((gi & ~7) + 8);
             auto shift = [&]() {
@@ -515,46 +538,37 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                     next = scales_of(gi + 8);
                 }
                 const int slot = sums % M::kSums;
-                ok = bar_wait(&bars.s_full[slot], (sums / M::kSums) & 1, &bars.failed);
-                if (!__all_sync(0xFFFFFFFFu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = warp_wait(&bars.s_full[slot], (sums / M::kSums) & 1, &bars.failed);
+                if (!ok) break;
                 fence_after();
                 // past the last group the weights are copied as zeros and x is zero, whatever the scale
                 const float ss = gi - 1 < a.groups ? s : 0.0f;
-                const uint32_t at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + slot * N;
-                constexpr int C = N < 64 ? N : 64;  // columns of a load
+                const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * N + c0;
                 const uint64_t s2 = pack2(ss, ss);
+                uint32_t d[C];
+                if constexpr (C == 64)
+                    tmem_load64(at, d);
+                else if constexpr (C == 32)
+                    tmem_load32(at, d);
+                else
+                    tmem_load16(at, d);
+                tmem_wait_load();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bars.s_empty[slot]);
 #pragma unroll
-                for (int c = 0; c < N; c += C) {
-                    uint32_t d[C];
-                    if constexpr (C == 64)
-                        tmem_load64(at + c, d);
-                    else if constexpr (C == 32)
-                        tmem_load32(at + c, d);
-                    else
-                        tmem_load16(at + c, d);
-                    tmem_wait_load();
-                    if (c + C == N) {
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(&bars.s_empty[slot]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < C / 2; ++i)
-                        y[c / 2 + i] = fma2(s2, pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), y[c / 2 + i]);
-                }
+                for (int i = 0; i < C / 2; ++i)
+                    y[i] = fma2(s2, pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), y[i]);
             }
             if (!ok) {
 #pragma unroll
-                for (int i = 0; i < N / 2; ++i) y[i] = 0x7FC000007FC00000ull;
+                for (int i = 0; i < C / 2; ++i) y[i] = 0x7FC000007FC00000ull;
             }
-            const int m0 = (item % a.halves) * N;
+            const int m0 = (item % a.halves) * N + c0;
             if (a.cluster == 1) {
                 if (n < a.outs) {
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
+                    for (int i = 0; i < C; ++i) {
                         const int m = m0 + i;
                         if (m < a.rows) {
                             const float v = half_of(y[i / 2], i & 1) * 0x1p24f * __ldg(a.x_back + m);
@@ -572,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
                 // every copy and product of this block is done: the rings give way to the block's sums
                 float* mine = reinterpret_cast<float*>(dyn);
 #pragma unroll
-                for (int i = 0; i < N; ++i) mine[i * 128 + tid] = half_of(y[i / 2], i & 1);
+                for (int i = 0; i < C; ++i) mine[(c0 + i) * 128 + row] = half_of(y[i / 2], i & 1);
             }
         }
     }
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         cluster_sync_all();
         const int item = first;
         const int m0 = (item % a.halves) * N;
-        for (int i = rank * N * 128 / a.cluster + tid; i < (rank + 1) * N * 128 / a.cluster; i += kThreads) {
+        for (int i = rank * N * 128 / a.cluster + tid; i < (rank + 1) * N * 128 / a.cluster; i += M::kThreads) {
             const int m = m0 + i / 128;
             const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + i % 128;
             if (m >= a.rows || n >= a.outs) continue;
@@ -606,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_kernel(const __grid_constant
         __syncwarp();
         cluster_sync_all();  // no block leaves while another reads its memory
     }
-    if (warp == 12)
+    if (warp == kIssue)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(M::kColumns) : "memory");
 }
 
@@ -627,7 +641,7 @@ int launch(const ManyArgs& a, int dev, int sms, cudaStream_t st) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(Many<N>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = Many<N>::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
