@@ -3,15 +3,15 @@
 //
 // Rotation.  Pair i at position p turns by p * turns[i] modulo 2^64: the low
 // 64 bits of the product are the exact fraction of a turn, so a far position
-// costs no accuracy.  The fraction is split into a quarter turn and a rest of
-// at most an eighth to either side, whose sine and cosine are taken in fp32:
+// costs no accuracy.  The fraction is split into quarter turns and a rest of
+// at most an eighth to either side, whose sine and cosine are fp32 Taylor sums:
 // a rotated value is off by less than 2^-21 (|a| + |b|) times the amplitude.
 //
 // Rounding.  The stored code is the nearest one to the exact rotated value:
 // where the two ends of that error interval round to different codes (about
 // one value in 10^5) the value is recomputed in fp64.  The same holds for the
 // page's largest magnitude, where the interval's ends give different scales.
-#include <atomic>
+#include <cstring>
 
 #include "kv_host.cuh"
 #include "serve_util.cuh"
@@ -22,7 +22,7 @@ using namespace arcs;
 
 constexpr int kThreads = 256;
 constexpr float kRotErr = 4.8e-7f;  // 2^-21
-constexpr int kKept = 4;            // row passes of a page job whose rows stay in registers
+constexpr int kKept = 2;            // row passes of a page job whose rows stay in registers
 
 struct AppendArgs {
     arc_kv_cache c;
@@ -33,19 +33,29 @@ struct AppendArgs {
     int32_t rot;
     int32_t layout;
     int32_t vec;      // bit 0: q and q_out, 1: k, 2: v allow 16-byte accesses
-    int64_t q_blocks; // blocks that rotate queries; the rest store keys and values
+    int64_t q_blocks; // blocks that rotate queries
     int32_t head_sets;  // the query heads of a token are shared by this many thread groups
+    int32_t page_heads; // heads of a page that a block stores
     uint32_t* err;
 };
 
-// cos and sin of the pair's angle, fp32, without the amplitude.
+// cos and sin of the pair's angle, fp32, without the amplitude: Taylor sums on
+// an eighth of a turn to either side (the first terms left out are below
+// 2e-9), then the quarter turns.
 __device__ __forceinline__ float2 turn32(uint64_t phase) {
     const uint32_t quarter = static_cast<uint32_t>((phase + (uint64_t{1} << 61)) >> 62);
-    const int64_t rest = static_cast<int64_t>(phase - (static_cast<uint64_t>(quarter) << 62));
-    // rest / 2^63 half turns, at most a quarter of a half turn to either side
-    const float x = static_cast<float>(static_cast<int32_t>(rest >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(x, &s, &c);
+    const int32_t rest = static_cast<int32_t>(static_cast<uint32_t>(phase >> 32) - (quarter << 30));
+    const float x = static_cast<float>(rest) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+    const float q = x * x;
+    float s = fmaf(q, 2.7557319e-6f, -1.9841270e-4f);  // 1 / 9!, -1 / 7!
+    s = fmaf(q, s, 8.3333333e-3f);
+    s = fmaf(q, s, -1.6666667e-1f);
+    s = fmaf(x * q, s, x);
+    float c = fmaf(q, -2.7557319e-7f, 2.4801587e-5f);  // -1 / 10!, 1 / 8!
+    c = fmaf(q, c, -1.3888889e-3f);
+    c = fmaf(q, c, 4.1666667e-2f);
+    c = fmaf(q, c, -0.5f);
+    c = fmaf(q, c, 1.0f);
     const float a = (quarter & 1) ? s : c, b = (quarter & 1) ? c : s;
     return make_float2(((quarter + 1) & 2) ? -a : a, (quarter & 2) ? -b : b);
 }
@@ -78,76 +88,108 @@ __device__ __forceinline__ PairOf pair_of(int d, int rot, int layout) {
     return (d & 1) ? PairOf{d >> 1, d - 1, -1.0f} : PairOf{d >> 1, d + 1, 1.0f};
 }
 
-// Eight values d0 .. d0 + 7 of one head: x and, with its sign, the partner of
-// each (b); elements past the rotation have b = 0.
-template <int DT>
-__device__ __forceinline__ void load_pairs(const char* head, int d0, int rot, int layout, bool vec, float (&a)[8],
-                                           float (&b)[8]) {
-    load8<DT>(head + d0 * 2, vec, a);
-    if (d0 >= rot) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0.0f;
-        return;
+// A thread owns sixteen values of a head: two vectors of eight, at d[0] and
+// d[1].  In the half layout (kHalves) they are each other's partners, so that a
+// pair is loaded and its angle computed once; vectors past the rotation pair up
+// as they lie.  A half rotation whose halves do not start on a vector (kOdd)
+// looks its partners up one by one.
+enum Turning { kHalves, kNeighbours, kOdd };
+struct Place {
+    int d[2];
+    bool turns;
+};
+template <int TURN>
+__device__ __forceinline__ Place place_of(const AppendArgs& a, int j) {
+    if (TURN == kHalves) {
+        const int h = a.rot >> 1, n = h >> 3;  // vectors of a half
+        if (j < n) return Place{{8 * j, 8 * j + h}, true};
+        return Place{{a.rot + 16 * (j - n), a.rot + 16 * (j - n) + 8}, false};
     }
-    if (layout == ARC_ROPE_INTERLEAVED) {
+    return Place{{16 * j, 16 * j + 8}, 16 * j < a.rot};
+}
+
+// cos and sin (times the amplitude) of the place's eight pairs.
+struct Turns {
+    float c[8], s[8];
+};
+template <int TURN>
+__device__ __forceinline__ void turns_of(const AppendArgs& a, const Place& p, int64_t pos, Turns& t) {
+    if (TURN == kOdd || !p.turns) return;
+    const int first = TURN == kHalves ? p.d[0] : p.d[0] >> 1;
+    uint64_t f[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const bool in = d0 + i < rot;
-            b[i] = in ? a[i + 1] : 0.0f;
-            b[i + 1] = in ? -a[i] : 0.0f;
-        }
-        return;
-    }
-    const int h = rot >> 1;
-    if ((h & 7) == 0) {  // the whole vector lies on one side
-        load8<DT>(head + (d0 < h ? d0 + h : d0 - h) * 2, vec, b);
-        if (d0 >= h) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = -b[i];
-        }
-        return;
-    }
-    const typename Half<DT>::T* e = reinterpret_cast<const typename Half<DT>::T*>(head);
+    for (int i = 0; i < 8; ++i) f[i] = TURN == kHalves || first + i < (a.rot >> 1) ? __ldg(a.turns + first + i) : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int d = d0 + i;
-        b[i] = 0.0f;
-        if (d < rot) {
-            const PairOf p = pair_of(d, rot, layout);
-            b[i] = p.sgn * Half<DT>::to_float(e[p.partner]);
+        const float2 cs = turn32(static_cast<uint64_t>(pos) * f[i]);
+        t.c[i] = cs.x * a.amp;
+        t.s[i] = cs.y * a.amp;
+    }
+}
+
+// The place's sixteen values of `head`, as they lie, and as fp32.
+__device__ __forceinline__ uint4 raw8(const char* p, bool vec) {
+    if (vec) return *reinterpret_cast<const uint4*>(p);
+    const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e[2 * i] | (static_cast<uint32_t>(e[2 * i + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+struct Raw {
+    uint4 v[2];
+};
+__device__ __forceinline__ Raw load16(const Place& p, const char* head, bool vec) {
+    return Raw{{raw8(head + p.d[0] * 2, vec), raw8(head + p.d[1] * 2, vec)}};
+}
+template <int DT>
+__device__ __forceinline__ void unpack16(const Raw& r, float (&x)[16]) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const uint32_t w[4] = {r.v[v].x, r.v[v].y, r.v[v].z, r.v[v].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Half<DT>::unpack(w[i]);
+            x[8 * v + 2 * i] = f.x;
+            x[8 * v + 2 * i + 1] = f.y;
         }
     }
 }
 
-// cos and sin (times the amplitude) of the eight elements' angles.
-__device__ __forceinline__ void load_turns(const AppendArgs& a, int64_t pos, int d0, float (&c)[8], float (&s)[8]) {
+// Turn them; returns the error bound of the turned values (0: exact).
+template <int DT, int TURN>
+__device__ __forceinline__ float turn16(const AppendArgs& a, const Place& p, const Turns& t, const char* head, int64_t pos,
+                                        float (&x)[16]) {
+    float most = 0.0f;
+    if (!p.turns) return 0.0f;
+    if (TURN == kOdd) {
+        const typename Half<DT>::T* e = reinterpret_cast<const typename Half<DT>::T*>(head);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = 1.0f;
-        s[i] = 0.0f;
-    }
-    if (d0 >= a.rot) return;
-    if (a.layout == ARC_ROPE_INTERLEAVED) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            if (d0 + i < a.rot) {
-                const float2 t = turn32(static_cast<uint64_t>(pos) * __ldg(a.turns + ((d0 + i) >> 1)));
-                c[i] = c[i + 1] = t.x * a.amp;
-                s[i] = s[i + 1] = t.y * a.amp;
+        for (int i = 0; i < 16; ++i) {
+            const int d = p.d[0] + i;
+            if (d < a.rot) {
+                const PairOf q = pair_of(d, a.rot, a.layout);
+                const float b = q.sgn * Half<DT>::to_float(e[q.partner]);
+                const float2 cs = turn32(static_cast<uint64_t>(pos) * __ldg(a.turns + q.pair));
+                most = fmaxf(most, fabsf(x[i]) + fabsf(b));
+                x[i] = fmaf(x[i], cs.x * a.amp, -(b * (cs.y * a.amp)));
             }
         }
-        return;
-    }
-    const int h = a.rot >> 1;
+    } else {
+        const int pairs = TURN == kHalves ? 8 : (a.rot - p.d[0]) >> 1;  // neighbours may end inside
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int d = d0 + i;
-        if (d < a.rot) {
-            const float2 t = turn32(static_cast<uint64_t>(pos) * __ldg(a.turns + (d < h ? d : d - h)));
-            c[i] = t.x * a.amp;
-            s[i] = t.y * a.amp;
+        for (int i = 0; i < 8; ++i) {
+            float& u = x[TURN == kHalves ? i : 2 * i];
+            float& w = x[TURN == kHalves ? 8 + i : 2 * i + 1];
+            if (TURN == kHalves || i < pairs) {
+                most = fmaxf(most, fabsf(u) + fabsf(w));
+                const float y = fmaf(u, t.c[i], -(w * t.s[i]));
+                w = fmaf(w, t.c[i], u * t.s[i]);
+                u = y;
+            }
         }
     }
+    return most * (kRotErr * a.amp);
 }
 
 // The sequence of row t: the last b with row_offsets[b] <= t.
@@ -181,13 +223,14 @@ __device__ __forceinline__ bool rows_of(const arc_kv_step& s, int64_t b, int64_t
     return true;
 }
 
-// A thread owns eight values of a token's heads h0, h0 + sets, ...: the
-// angles are computed once for all of them.
-template <int DT>
+// A thread owns sixteen values of a token's heads set, set + sets, ...: the
+// angles are computed once for all of them; kHeads heads are in flight at once.
+constexpr int kHeads = 4;
+template <int DT, int TURN>
 __device__ __forceinline__ void rotate_queries(const AppendArgs& a) {
-    const int L = a.c.head_dim >> 3;
+    const int L = a.c.head_dim >> 4;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    const int d0 = static_cast<int>(unit % L) * 8;
+    const Place p = place_of<TURN>(a, static_cast<int>(unit % L));
     const int64_t g = unit / L;
     const int set = static_cast<int>(g % a.head_sets);
     const int64_t t = g / a.head_sets;
@@ -200,67 +243,76 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a) {
             if (a.err) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
             on = false;
         } else {
-            const int p = __ldg(a.s.positions + b);
-            pos = p < 0 ? -1 : p + (t - first);
+            const int at = __ldg(a.s.positions + b);
+            pos = at < 0 ? -1 : at + (t - first);
         }
     }
-    float c[8], s[8];
-    load_turns(a, pos, d0, c, s);
+    Turns turns;
+    turns_of<TURN>(a, p, pos, turns);
     const bool vec = a.vec & 1;
-    for (int h0 = 0; h0 < a.r.q_heads; h0 += a.head_sets) {  // the same trips in every lane
-        const int h = h0 + set;
-        const bool here = on && h < a.r.q_heads;
-        float x[8], y[8];
-        if (here)
-            load_pairs<DT>(static_cast<const char*>(a.r.q) + (t * a.r.q_token_stride + h * a.r.q_head_stride) * 2, d0,
-                           a.rot, a.layout, vec, x, y);
-        __syncwarp();  // in place: a head's lanes are in one warp, its loads come before its stores
-        if (here) {
+    const char* const from = static_cast<const char*>(a.r.q) + t * a.r.q_token_stride * 2;
+    char* const to = static_cast<char*>(a.r.q_out) + t * a.r.out_token_stride * 2;
+    for (int h0 = 0; h0 < a.r.q_heads; h0 += kHeads * a.head_sets) {  // the same trips in every lane
+        Raw r[kHeads];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = pos < 0 ? 0.0f : fmaf(x[i], c[i], -(y[i] * s[i]));
-            store8<DT>(static_cast<char*>(a.r.q_out) + (t * a.r.out_token_stride + h * a.r.out_head_stride + d0) * 2,
-                       vec, x);
+        for (int k = 0; k < kHeads; ++k) {
+            const int h = h0 + k * a.head_sets + set;
+            if (on && h < a.r.q_heads) r[k] = load16(p, from + h * a.r.q_head_stride * 2, vec);
+        }
+        if (TURN != kOdd) __syncwarp();  // in place: a head's lanes are in one warp, its loads come before its stores
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+            const int h = h0 + k * a.head_sets + set;
+            const bool here = on && h < a.r.q_heads;
+            float x[16];
+            if (here) {
+                unpack16<DT>(r[k], x);
+                turn16<DT, TURN>(a, p, turns, from + h * a.r.q_head_stride * 2, pos, x);
+            }
+            if (TURN == kOdd) __syncwarp();  // the partners were read just now
+            if (here) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    float e[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] = pos < 0 ? 0.0f : x[8 * v + i];
+                    store8<DT>(to + (h * a.r.out_head_stride + p.d[v]) * 2, vec, e);
+                }
+            }
         }
         __syncwarp();
     }
 }
 
-// Eight rotated values of a key, or eight values (`turn` false), their error
-// bound, and what an exact recomputation needs.
-struct Eight {
-    float y[8];
-    float err;  // 0: exact
+// Sixteen turned values of a key, or sixteen values.
+struct Sixteen {
+    float y[16];
+    float err;  // their error bound; 0: exact
+    float top;  // their largest magnitude
 };
 
-template <int DT>
-__device__ __forceinline__ bool eight(const AppendArgs& a, const char* head, bool turn, int64_t pos, int d0, bool vec,
-                                      Eight& e) {
-    bool nan = false;
-    e.err = 0.0f;
-    if (turn && d0 < a.rot) {
-        float x[8], b[8], c[8], s[8];
-        load_pairs<DT>(head, d0, a.rot, a.layout, vec, x, b);
-        load_turns(a, pos, d0, c, s);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            e.y[i] = fmaf(x[i], c[i], -(b[i] * s[i]));
-            e.err = fmaxf(e.err, fabsf(x[i]) + fabsf(b[i]));
-        }
-        e.err *= kRotErr * a.amp;
-    } else {
-        load8<DT>(head + d0 * 2, vec, e.y);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (e.y[i] != e.y[i]) {
-            e.y[i] = 0.0f;
-            nan = true;
-        }
-    }
-    return nan;
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-// The exact value of element d of a rotated head.
+// The largest magnitude; NaN values become 0 (true where there was one).
+__device__ __forceinline__ bool finish16(Sixteen& v) {
+    v.top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v.top = max_nan(v.top, fabsf(v.y[i]));
+    if (v.top == v.top) return false;
+    v.top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (v.y[i] != v.y[i]) v.y[i] = 0.0f;
+        v.top = fmaxf(v.top, fabsf(v.y[i]));
+    }
+    return true;
+}
+
+// The exact value of element d of a key's head, turned.
 template <int DT>
 __device__ __noinline__ double exact_value(const AppendArgs& a, const char* head, int64_t pos, int d) {
     const typename Half<DT>::T* e = reinterpret_cast<const typename Half<DT>::T*>(head);
@@ -272,30 +324,43 @@ __device__ __noinline__ double exact_value(const AppendArgs& a, const char* head
     return y != y ? 0.0 : y;
 }
 
-// The codes of eight values under the scale 2^e.
-template <int DT>
-__device__ __forceinline__ uint2 codes(const AppendArgs& a, const char* head, int64_t pos, int d0, const Eight& v, int e) {
-    const float inv = exp2i(-e);
-    uint32_t lo[2], hi[2];
+// Store the codes of the place's values under the scale 2^e in the row at `out`.
+template <int DT, bool EXACT>
+__device__ __forceinline__ void put16(const AppendArgs& a, const Place& p, const char* head, int64_t pos, const Sixteen& v,
+                                      int e, char* out) {
+    const float inv = exp2i(-e), slack = v.err * inv;
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const float* y = v.y + 4 * w;
-        lo[w] = e4m3x2((y[0] - v.err) * inv, (y[1] - v.err) * inv) |
-                (e4m3x2((y[2] - v.err) * inv, (y[3] - v.err) * inv) << 16);
-        hi[w] = e4m3x2((y[0] + v.err) * inv, (y[1] + v.err) * inv) |
-                (e4m3x2((y[2] + v.err) * inv, (y[3] + v.err) * inv) << 16);
-    }
-    if (lo[0] != hi[0] || lo[1] != hi[1]) {
+    for (int half = 0; half < 2; ++half) {
+        uint32_t lo[2], hi[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int w = i >> 2, sh = (i & 3) * 8;
-            if (((lo[w] ^ hi[w]) >> sh) & 0xFFu) {
-                const uint32_t code = e4m3_of_double(exact_value<DT>(a, head, pos, d0 + i) * static_cast<double>(inv));
-                lo[w] = (lo[w] & ~(0xFFu << sh)) | (code << sh);
+        for (int w = 0; w < 2; ++w) {
+            const float* y = v.y + 8 * half + 4 * w;
+            if (EXACT) {
+                lo[w] = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
+            } else {
+                lo[w] = e4m3x2(fmaf(y[0], inv, -slack), fmaf(y[1], inv, -slack)) |
+                        (e4m3x2(fmaf(y[2], inv, -slack), fmaf(y[3], inv, -slack)) << 16);
+                hi[w] = e4m3x2(fmaf(y[0], inv, slack), fmaf(y[1], inv, slack)) |
+                        (e4m3x2(fmaf(y[2], inv, slack), fmaf(y[3], inv, slack)) << 16);
             }
         }
+        if (!EXACT && (lo[0] != hi[0] || lo[1] != hi[1])) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int sh = (i & 3) * 8;
+                const uint32_t l = i < 4 ? lo[0] : lo[1], g = i < 4 ? hi[0] : hi[1];
+                if (((l ^ g) >> sh) & 0xFFu) {
+                    const uint32_t code = e4m3_of_double(exact_value<DT>(a, head, pos, p.d[half] + i) * static_cast<double>(inv));
+                    const uint32_t n = (l & ~(0xFFu << sh)) | (code << sh);
+                    if (i < 4)
+                        lo[0] = n;
+                    else
+                        lo[1] = n;
+                }
+            }
+        }
+        *reinterpret_cast<uint2*>(out + p.d[half]) = make_uint2(lo[0], lo[1]);
     }
-    return make_uint2(lo[0], lo[1]);
 }
 
 // Four e4m3 codes times `f`, a power of two: shifts exponents, rounds below
@@ -318,19 +383,30 @@ __device__ __forceinline__ int held_exponent(float scale) {
     return e < -kScaleExp ? -kScaleExp : (e > kScaleExp ? kScaleExp : e);
 }
 
-// One new token of a (sequence, head, key or value): head_dim / 8 lanes.
-template <int DT>
+// One new token of a (sequence, head, key or value): head_dim / 16 lanes.
+template <int DT, int TURN>
 __device__ __forceinline__ void store_single(const AppendArgs& a) {
-    const int L = a.c.head_dim >> 3;
+    const int L = a.c.head_dim >> 4;
     const int64_t unit = (static_cast<int64_t>(blockIdx.x) - a.q_blocks) * kThreads + threadIdx.x;
     const int64_t job = unit / L;
-    const int d0 = static_cast<int>(unit % L) * 8;
+    const int j = static_cast<int>(unit % L);
     const bool is_v = job & 1;
     const int64_t bh = job >> 1;
     const int h = static_cast<int>(bh % a.c.heads);
     const int64_t b = bh / a.c.heads;
     bool on = b < a.s.B;
-    int pos = on ? __ldg(a.s.positions + b) : -1;
+    const char* head = static_cast<const char*>(is_v ? a.r.v : a.r.k) +
+                       (b * (is_v ? a.r.v_token_stride : a.r.k_token_stride) +
+                        h * (is_v ? a.r.v_head_stride : a.r.k_head_stride)) * 2;
+    const Place p = place_of<TURN>(a, j);
+    Sixteen v;
+    v.err = v.top = 0.0f;
+    Raw raw;
+    int pos = -1;
+    if (on) {
+        pos = __ldg(a.s.positions + b);  // these loads do not wait for each other
+        raw = load16(p, head, a.vec & (is_v ? 4 : 2));
+    }
     uint32_t err = 0;
     on = on && pos >= 0;
     const int pi = pos / a.c.page_size, slot = pos - pi * a.c.page_size;
@@ -342,28 +418,22 @@ __device__ __forceinline__ void store_single(const AppendArgs& a) {
     if (on && static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.c.pages)) {
         err |= ARC_KV_ERR_PAGE;
         on = false;
+        page = 0;
     }
-    const char* head = static_cast<const char*>(is_v ? a.r.v : a.r.k) +
-                       (b * (is_v ? a.r.v_token_stride : a.r.k_token_stride) +
-                        h * (is_v ? a.r.v_head_stride : a.r.k_head_stride)) * 2;
-    const bool vec = a.vec & (is_v ? 4 : 2);
     float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.heads + h;
-    Eight v;
-    v.err = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v.y[i] = 0.0f;
     float was = 0.0f;
     if (on) {
         was = *scale;
-        if (eight<DT>(a, head, !is_v, pos, d0, vec, v)) err |= ARC_KV_ERR_NAN;
+        unpack16<DT>(raw, v.y);
+        if (!is_v) {
+            Turns turns;
+            turns_of<TURN>(a, p, pos, turns);
+            v.err = turn16<DT, TURN>(a, p, turns, head, pos, v.y);
+        }
+        if (finish16(v)) err |= ARC_KV_ERR_NAN;
     }
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo = fmaxf(lo, fabsf(v.y[i]) - v.err);
-        hi = fmaxf(hi, fabsf(v.y[i]) + v.err);
-    }
-    for (int m = L >> 1 < 16 ? L >> 1 : 16; m; m >>= 1) {
+    float lo = fmaxf(v.top - v.err, 0.0f), hi = v.top + v.err;
+    for (int m = L >> 1; m; m >>= 1) {
         lo = fmaxf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m));
         hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m));
     }
@@ -372,53 +442,50 @@ __device__ __forceinline__ void store_single(const AppendArgs& a) {
     if (__any_sync(0xFFFFFFFFu, unsure)) {
         double y = 0.0;
         if (unsure)
-            for (int i = 0; i < 8; ++i) y = fmax(y, fabs(exact_value<DT>(a, head, pos, d0 + i)));
-        for (int m = L >> 1 < 16 ? L >> 1 : 16; m; m >>= 1) y = fmax(y, __shfl_xor_sync(0xFFFFFFFFu, y, m));
+            for (int i = 0; i < 16; ++i) y = fmax(y, fabs(exact_value<DT>(a, head, pos, p.d[i >> 3] + (i & 7))));
+        for (int m = L >> 1; m; m >>= 1) y = fmax(y, __shfl_xor_sync(0xFFFFFFFFu, y, m));
         // rounding up cannot pass a border from below: 448 * 2^e is an fp32 value
         if (unsure) e = scale_exponent(__double2float_ru(y));
     }
-    // the reads of the scale above come before any lane's write below
-    __syncwarp();
+    __syncwarp();  // every lane has read the scale
     if (on) {
-        char* base = static_cast<char*>(is_v ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride + d0;
+        char* base = static_cast<char*>(is_v ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
         if (slot > 0) {
             const int old = held_exponent(was);
             if (e > old) {
                 const float f = exp2i(old - e);
 #pragma unroll 4
                 for (int s = 0; s < slot; ++s) {
-                    uint2* p = reinterpret_cast<uint2*>(base + static_cast<int64_t>(s) * a.c.head_dim);
-                    const uint2 w = *p;
-                    *p = make_uint2(rescale4(w.x, f), rescale4(w.y, f));
+                    uint4* q = reinterpret_cast<uint4*>(base + static_cast<int64_t>(s) * a.c.head_dim + 16 * j);
+                    const uint4 w = *q;
+                    *q = make_uint4(rescale4(w.x, f), rescale4(w.y, f), rescale4(w.z, f), rescale4(w.w, f));
                 }
             } else {
                 e = old;
             }
         }
-        *reinterpret_cast<uint2*>(base + static_cast<int64_t>(slot) * a.c.head_dim) = codes<DT>(a, head, pos, d0, v, e);
-        if (d0 == 0) *scale = exp2i(e);
+        base += static_cast<int64_t>(slot) * a.c.head_dim;
+        if (is_v)
+            put16<DT, true>(a, p, head, pos, v, e, base);
+        else
+            put16<DT, false>(a, p, head, pos, v, e, base);
+        if (j == 0) *scale = exp2i(e);
     }
     if (err && a.err) atomicOr(a.err, err);
 }
 
-// All new tokens of a (sequence, page, head, key or value): one block, a row
-// of head_dim / 8 lanes for each token, the rows of the first kKept passes in
+// All new tokens of a (sequence, page, keys or values) and a.page_heads of its
+// heads, one after another: a block, head_dim / 16 lanes for each token.  The
+// angles are the heads' in common; the rows of the first kKept passes stay in
 // registers between the maximum and the rounding.
-template <int DT>
-__device__ __forceinline__ void store_pages(const AppendArgs& a) {
+template <int DT, int TURN, bool V>
+__device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, int set) {
     __shared__ int64_t wsum[kThreads / 32];
     __shared__ int64_t found[2];  // sequence, page within its new ones
-    __shared__ uint32_t red[2][kThreads / 32];
-    __shared__ unsigned long long red64[kThreads / 32];
+    __shared__ uint32_t red[2][2][kThreads / 32];
+    __shared__ double red64[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ps = a.c.page_size;
-    const int64_t jobs_per_page = int64_t{2} * a.c.heads;
-    const int64_t block = static_cast<int64_t>(blockIdx.x) - a.q_blocks;
-    const int64_t want = block / jobs_per_page;
-    const int sub = static_cast<int>(block % jobs_per_page);
-    const bool is_v = sub & 1;
-    const int h = sub >> 1;
-
     // pages touched by sequence b; the running total finds this block's
     auto touched = [&](int64_t b) -> int64_t {
         int64_t first, n;
@@ -478,114 +545,175 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a) {
     const int slot1 = static_cast<int>(end < ps ? end : ps);
     const int64_t row0 = first + (page0 + slot0 - p0);  // row of slot0
 
-    const int L = a.c.head_dim >> 3;
+    const int L = a.c.head_dim >> 4;
     const int per = kThreads / L;  // rows of a pass
-    const int my = tid / L, d0 = (tid % L) * 8;
+    const int my = tid / L;
+    const Place p = place_of<TURN>(a, tid % L);
     const int rows = slot1 - slot0, passes = (rows + per - 1) / per;
-    const int64_t ts = is_v ? a.r.v_token_stride : a.r.k_token_stride;
-    const char* src = static_cast<const char*>(is_v ? a.r.v : a.r.k) +
-                      (row0 * ts + h * (is_v ? a.r.v_head_stride : a.r.k_head_stride)) * 2;
-    const bool vec = a.vec & (is_v ? 4 : 2);
-    float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.heads + h;
-    const float was = *scale;
-    Eight kept[kKept];
-    float lo = 0.0f, hi = 0.0f;
-    bool nan = false;
-    auto fetch = [&](int r, Eight& v) {
-        v.err = 0.0f;
+    const int64_t ts = V ? a.r.v_token_stride : a.r.k_token_stride;
+    const int64_t hs = V ? a.r.v_head_stride : a.r.k_head_stride;
+    const bool vec = a.vec & (V ? 4 : 2);
+    const char* const src0 = static_cast<const char*>(V ? a.r.v : a.r.k) + row0 * ts * 2;
+    float* const scales = (V ? a.c.v_scale : a.c.k_scale) + static_cast<int64_t>(page) * a.c.heads;
+    Turns turns[kKept];
+    if (!V) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v.y[i] = 0.0f;
-        if (r < rows) nan |= eight<DT>(a, src + r * ts * 2, !is_v, page0 + slot0 + r, d0, vec, v);
-    };
-    auto widen = [&](const Eight& v) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fmaxf(lo, fabsf(v.y[i]) - v.err);
-            hi = fmaxf(hi, fabsf(v.y[i]) + v.err);
-        }
-    };
-#pragma unroll
-    for (int p = 0; p < kKept; ++p) {
-        if (p < passes) {
-            fetch(p * per + my, kept[p]);
-            widen(kept[p]);
-        }
+        for (int k = 0; k < kKept; ++k)
+            if (k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, turns[k]);
     }
-    for (int p = kKept; p < passes; ++p) {
-        Eight v;
-        fetch(p * per + my, v);
-        widen(v);
-    }
-    // magnitudes are not negative: their bits order as they do
-    const uint32_t wl = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(lo));
-    const uint32_t wh = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hi));
-    if (lane == 0) {
-        red[0][warp] = wl;
-        red[1][warp] = wh;
-    }
-    if (nan && a.err) atomicOr(a.err, ARC_KV_ERR_NAN);
-    __syncthreads();
-    uint32_t bl = 0, bh = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        bl = max(bl, red[0][w]);
-        bh = max(bh, red[1][w]);
-    }
-    int e = scale_exponent(__uint_as_float(bl));
-    if (e != scale_exponent(__uint_as_float(bh))) {  // the same in every thread
-        double y = 0.0;
-        for (int p = 0; p < passes; ++p) {
-            const int r = p * per + my;
-            if (r < rows)
-                for (int i = 0; i < 8; ++i)
-                    y = fmax(y, fabs(exact_value<DT>(a, src + r * ts * 2, page0 + slot0 + r, d0 + i)));
-        }
-        for (int m = 16; m; m >>= 1) y = fmax(y, __shfl_xor_sync(0xFFFFFFFFu, y, m));
-        if (lane == 0) red64[warp] = static_cast<unsigned long long>(__double_as_longlong(y));
-        __syncthreads();
-        for (int w = 0; w < kThreads / 32; ++w) y = fmax(y, __longlong_as_double(static_cast<long long>(red64[w])));
-        e = scale_exponent(__double2float_ru(y));
-    }
-    char* base = static_cast<char*>(is_v ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
-    if (slot0 > 0) {
-        const int old = held_exponent(was);
-        if (e > old) {
-            const float f = exp2i(old - e);
-            const int words = slot0 * (a.c.head_dim >> 3);
-            for (int w = tid; w < words; w += kThreads) {
-                uint2* p = reinterpret_cast<uint2*>(base) + w;
-                const uint2 x = *p;
-                *p = make_uint2(rescale4(x.x, f), rescale4(x.y, f));
+    const int h1 = set * a.page_heads + a.page_heads < a.c.heads ? set * a.page_heads + a.page_heads : a.c.heads;
+    for (int h = set * a.page_heads; h < h1; ++h) {
+        const char* src = src0 + h * hs * 2;
+        const float was = scales[h];
+        bool nan = false;
+        auto fetch = [&](int r, const Turns& t, Sixteen& v) {
+            v.err = v.top = 0.0f;
+            if (r < rows) {
+                unpack16<DT>(load16(p, src + r * ts * 2, vec), v.y);
+                if (!V) v.err = turn16<DT, TURN>(a, p, t, src + r * ts * 2, page0 + slot0 + r, v.y);
+                nan |= finish16(v);
             }
-        } else {
-            e = old;
-        }
-    }
-    auto put = [&](int r, const Eight& v) {
-        if (r < rows)
-            *reinterpret_cast<uint2*>(base + static_cast<int64_t>(slot0 + r) * a.c.head_dim + d0) =
-                codes<DT>(a, src + r * ts * 2, page0 + slot0 + r, d0, v, e);
-    };
+        };
+        Sixteen kept[kKept];
+        float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int p = 0; p < kKept; ++p)
-        if (p < passes) put(p * per + my, kept[p]);
-    for (int p = kKept; p < passes; ++p) {
-        Eight v;
-        fetch(p * per + my, v);
-        put(p * per + my, v);
+        for (int k = 0; k < kKept; ++k) {
+            fetch(k * per + my, turns[k], kept[k]);
+            lo = fmaxf(lo, kept[k].top - kept[k].err);
+            hi = fmaxf(hi, kept[k].top + kept[k].err);
+        }
+        for (int k = kKept; k < passes; ++k) {
+            Sixteen v;
+            Turns t;
+            if (!V && k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, t);
+            fetch(k * per + my, t, v);
+            lo = fmaxf(lo, v.top - v.err);
+            hi = fmaxf(hi, v.top + v.err);
+        }
+        // magnitudes are not negative: their bits order as they do
+        const uint32_t wl = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(lo));
+        const uint32_t wh = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hi));
+        if (lane == 0) {
+            red[h & 1][0][warp] = wl;
+            red[h & 1][1][warp] = wh;
+        }
+        if (nan && a.err) atomicOr(a.err, ARC_KV_ERR_NAN);
+        __syncthreads();  // two sets of sums in turn: the next head's are written before this one's are read by all
+        uint32_t bl = 0, bh = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            bl = max(bl, red[h & 1][0][w]);
+            bh = max(bh, red[h & 1][1][w]);
+        }
+        int e = scale_exponent(__uint_as_float(bl));
+        if (!V && e != scale_exponent(__uint_as_float(bh))) {  // the same in every thread
+            double y = 0.0;
+            for (int k = 0; k < passes; ++k) {
+                const int r = k * per + my;
+                if (r < rows)
+                    for (int i = 0; i < 16; ++i)
+                        y = fmax(y, fabs(exact_value<DT>(a, src + r * ts * 2, page0 + slot0 + r, p.d[i >> 3] + (i & 7))));
+            }
+            for (int m = 16; m; m >>= 1) y = fmax(y, __shfl_xor_sync(0xFFFFFFFFu, y, m));
+            if (lane == 0) red64[warp] = y;
+            __syncthreads();
+            for (int w = 0; w < kThreads / 32; ++w) y = fmax(y, red64[w]);
+            __syncthreads();
+            e = scale_exponent(__double2float_ru(y));
+        }
+        char* base = static_cast<char*>(V ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
+        if (slot0 > 0) {
+            const int old = held_exponent(was);
+            if (e > old) {
+                const float f = exp2i(old - e);
+                const int words = slot0 * (a.c.head_dim >> 4);
+                for (int w = tid; w < words; w += kThreads) {
+                    uint4* q = reinterpret_cast<uint4*>(base) + w;
+                    const uint4 x = *q;
+                    *q = make_uint4(rescale4(x.x, f), rescale4(x.y, f), rescale4(x.z, f), rescale4(x.w, f));
+                }
+            } else {
+                e = old;
+            }
+        }
+        auto put = [&](int r, const Sixteen& v) {
+            if (r < rows)
+                put16<DT, V>(a, p, src + r * ts * 2, page0 + slot0 + r, v, e,
+                             base + static_cast<int64_t>(slot0 + r) * a.c.head_dim);
+        };
+#pragma unroll
+        for (int k = 0; k < kKept; ++k) put(k * per + my, kept[k]);
+        for (int k = kKept; k < passes; ++k) {
+            Sixteen v;
+            Turns t;
+            if (!V && k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, t);
+            fetch(k * per + my, t, v);
+            put(k * per + my, v);
+        }
+        if (tid == 0) scales[h] = exp2i(e);  // every thread read it before the barrier
     }
-    // every thread read the scale before the barrier above
-    if (tid == 0) *scale = exp2i(e);
+}
+
+// A decode step: queries and new tokens in one launch.
+template <int DT, int TURN>
+__global__ void __launch_bounds__(kThreads, 3) single_kernel(const __grid_constant__ AppendArgs a) {
+    if (static_cast<int64_t>(blockIdx.x) < a.q_blocks)
+        rotate_queries<DT, TURN>(a);
+    else
+        store_single<DT, TURN>(a);
+}
+
+// Prompts: two launches side by side, so that the queries' blocks are not held
+// to the pages' registers.  The second starts with the first and ends after it.
+template <int DT, int TURN>
+__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_constant__ AppendArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    rotate_queries<DT, TURN>(a);
+}
+
+template <int DT, int TURN>
+__global__ void __launch_bounds__(kThreads, 2) pages_kernel(const __grid_constant__ AppendArgs a) {
+    const int sets = (a.c.heads + a.page_heads - 1) / a.page_heads;
+    const int64_t page = blockIdx.x / (2 * sets);
+    const int sub = static_cast<int>(blockIdx.x % (2 * sets));
+    if (sub & 1)
+        store_pages<DT, TURN, true>(a, page, sub >> 1);
+    else
+        store_pages<DT, TURN, false>(a, page, sub >> 1);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <int DT, int TURN>
+int launch(const AppendArgs& a, int64_t kv_blocks, cudaStream_t st) {
+    if (a.s.row_offsets == nullptr) {
+        single_kernel<DT, TURN><<<static_cast<unsigned>(a.q_blocks + kv_blocks), kThreads, 0, st>>>(a);
+        return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
+    }
+    if (a.q_blocks > 0) {
+        rotate_kernel<DT, TURN><<<static_cast<unsigned>(a.q_blocks), kThreads, 0, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return ARC_E_CUDA;
+    }
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(static_cast<unsigned>(kv_blocks), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.q_blocks > 0 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, pages_kernel<DT, TURN>, a) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    return ARC_OK;
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-    if (static_cast<int64_t>(blockIdx.x) < a.q_blocks)
-        rotate_queries<DT>(a);
-    else if (a.s.row_offsets == nullptr)
-        store_single<DT>(a);
-    else
-        store_pages<DT>(a);
+int launch_turning(const AppendArgs& a, int64_t kv_blocks, cudaStream_t st) {
+    if (a.layout == ARC_ROPE_INTERLEAVED) return launch<DT, kNeighbours>(a, kv_blocks, st);
+    return a.rot % 16 == 0 ? launch<DT, kHalves>(a, kv_blocks, st) : launch<DT, kOdd>(a, kv_blocks, st);
 }
 
 }  // namespace
@@ -632,13 +760,14 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
                  : 0) |
             (vectors(rows->k, rows->k_token_stride, rows->k_head_stride) ? 2 : 0) |
             (vectors(rows->v, rows->v_token_stride, rows->v_head_stride) ? 4 : 0);
-    const int L = cache->head_dim / 8;
+    const int L = cache->head_dim / 16;
     a.head_sets = 1;
+    a.page_heads = 1;
     a.q_blocks = 0;
     if (rows->q_heads > 0) {
         // few tokens: each head its own threads; many: one thread turns all heads of its eight values
         const int64_t units = step->T * L;
-        while (a.head_sets < rows->q_heads && units * a.head_sets < 152 * 2048) a.head_sets *= 2;
+        while (a.head_sets < rows->q_heads && units * a.head_sets < 152 * 1024) a.head_sets *= 2;
         if (a.head_sets > rows->q_heads) a.head_sets = rows->q_heads;
         a.q_blocks = (units * a.head_sets + kThreads - 1) / kThreads;
     }
@@ -649,14 +778,13 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
         // a sequence with n tokens touches at most n / page_size + 2 pages, and at most n
         const int64_t seqs = step->B < step->T ? step->B : step->T;
         const int64_t most = step->T / cache->page_size + 2 * seqs;
-        kv_blocks = (most < step->T ? most : step->T) * cache->heads * 2;
+        const int64_t pages = most < step->T ? most : step->T;
+        // many pages: a block stores several heads with one set of angles
+        while (a.page_heads < 4 && a.page_heads < cache->heads && pages * cache->heads / a.page_heads > 1024) a.page_heads *= 2;
+        kv_blocks = pages * 2 * ((cache->heads + a.page_heads - 1) / a.page_heads);
     }
     const int64_t grid = a.q_blocks + kv_blocks;
     if (grid > INT_MAX) return ARC_E_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (rows->dtype == ARC_BF16)
-        append_kernel<ARC_BF16><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
-    else
-        append_kernel<ARC_F16><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
+    return rows->dtype == ARC_BF16 ? launch_turning<ARC_BF16>(a, kv_blocks, st) : launch_turning<ARC_F16>(a, kv_blocks, st);
 }

@@ -24,7 +24,7 @@ struct W4Args {
 };
 
 // ------------------------------------------------------------------ few rows
-// 1 .. 16 rows of x: fp16 matrix instructions with 16 weight rows on the long
+// 1 .. 8 rows of x: fp16 matrix instructions with 16 weight rows on the long
 // side and the rows of x on the short one.
 //
 // Mathematics.  A row of x is scaled by a power of two to [2^14, 2^15) and
@@ -47,6 +47,7 @@ struct W4Args {
 // whose first block adds the others' sums.
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kXVecs = 8;               // 16-byte vectors of x a thread stages
 constexpr int kPart = 512;              // inner values of a warp's stage
 constexpr int kTileCost = 4;
 
@@ -96,52 +97,91 @@ __device__ __forceinline__ int weight_at(int r, int c) {
     return r * PITCH + ((c & 8) | ((c & 7) ^ row_bits(r))) * 16;
 }
 
+// Eight 16-bit values as they lie.
+__device__ __forceinline__ uint4 raw8(const void* p, bool vec) {
+    if (vec) return *static_cast<const uint4*>(p);
+    const uint16_t* e = static_cast<const uint16_t*>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e[2 * i] | (static_cast<uint32_t>(e[2 * i + 1]) << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // x of the block's slice to shared memory: fp16, scaled row by row, in the
-// order of the products, and the sums of each group.
+// order of the products, and the sums of each group.  All of it is loaded at
+// once (64 KB at most: eight vectors a thread), so the block waits for memory
+// once before its first product.
 template <int DT, int G, int NT, bool Z>
 __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, int ks) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rows = f.a.rows;
-    float* up = reinterpret_cast<float*>(dyn + f.up_off);
-    for (int m = warp; m < 8 * NT; m += kFewWarps) {
-        float top = 0.0f;
-        if (m < rows) {
-            const char* x = static_cast<const char*>(f.a.x) + (m * f.a.x_stride + k0) * 2;
-            for (int k = lane * 8; k < ks; k += 256) {
-                float v[8];
-                load8<DT>(x + k * 2, f.x_vec, v);
+    const int tid = threadIdx.x;
+    const int rows = f.a.rows, units = ks >> 3, groups = ks / G, all = units * rows;
+    uint32_t* top = reinterpret_cast<uint32_t*>(dyn + f.up_off);  // then the rows' factors
+    uint4 raw[kXVecs];
+    int row[kXVecs];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float z = fabsf(v[i]);
-                    if (z <= 3.4028235e38f) top = fmaxf(top, z);  // the largest finite one
-                }
-            }
+    for (int j = 0; j < kXVecs; ++j) {
+        const int i = j * kFewThreads + tid;
+        raw[j] = make_uint4(0u, 0u, 0u, 0u);
+        row[j] = 0;
+        if (i < all) {
+            row[j] = i / units;
+            raw[j] = raw8(static_cast<const char*>(f.a.x) + (row[j] * f.a.x_stride + k0 + (i - row[j] * units) * 8) * 2, f.x_vec);
         }
-        top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-        if (lane == 0) {
-            const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            const int e = top == 0.0f ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
-            up[m] = exp2i(e);
+    }
+    if (tid < 8 * NT) top[tid] = 0;
+    __syncthreads();
+    float v[8];
+    auto unpack = [&](const uint4& r) {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = Half<DT>::unpack(w[i]);
+            v[2 * i] = p.x;
+            v[2 * i + 1] = p.y;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kXVecs; ++j) {
+        if (j * kFewThreads >= all) break;
+        unpack(raw[j]);
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float z = fabsf(v[i]);
+            if (z <= 3.4028235e38f) most = fmaxf(most, z);  // the largest finite one
+        }
+        if ((units & 31) == 0) {  // a warp's vectors are of one row
+            const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
+            if ((tid & 31) == 0) atomicMax(top + row[j], w);
+        } else {
+            atomicMax(top + row[j], __float_as_uint(most));
         }
     }
     __syncthreads();
-    const int units = ks >> 3, groups = ks / G;
+    if (tid < 8 * NT) {
+        const int ex = static_cast<int>(top[tid] >> 23) - 127;
+        const int e = top[tid] == 0 ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
+        reinterpret_cast<float*>(top)[tid] = exp2i(e);
+    }
+    __syncthreads();
+    const float* up = reinterpret_cast<const float*>(top);
     float* xs = reinterpret_cast<float*>(dyn + f.xs_off);
     for (int i = tid; i < groups * 8 * NT; i += kFewThreads)
         if (i % (8 * NT) >= rows) xs[i] = 0.0f;
-    for (int base = 0; base < units * rows; base += kFewThreads) {  // the same trips in every lane
-        // units of a group are neighbouring lanes: units is a multiple of G / 8
-        const int i = base + tid;
-        const bool on = i < units * rows;
-        const int m = on ? i / units : 0, u = i - m * units, k = on ? u * 8 : 0;
-        float v[8];
-        load8<DT>(static_cast<const char*>(f.a.x) + (m * f.a.x_stride + k0 + k) * 2, f.x_vec, v);
+#pragma unroll
+    for (int j = 0; j < kXVecs; ++j) {
+        if (j * kFewThreads >= all) break;
+        // vectors of a group are neighbouring lanes: units is a multiple of G / 8
+        const int i = j * kFewThreads + tid;
+        const bool on = i < all;
+        const int m = row[j], u = i - m * units, k = on ? u * 8 : 0;
+        unpack(raw[j]);
         const float s = up[m];
         float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] *= s;
-            sum += v[j];
+        for (int e = 0; e < 8; ++e) {
+            v[e] *= s;
+            sum += v[e];
         }
         const int gi = k / G, in = k % G, t = in / (G / 4), w = (in % (G / 4)) >> 3;
         const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
@@ -432,8 +472,9 @@ template <int G, int NT>
 int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
     FewArgs f;
     f.a = a;
-    // a block's x stays within 64 KB: 4,096 inner values of 8 rows, 2,048 of 16
-    const int reach = NT == 1 ? 4096 : 2048;
+    // a block's x stays within 64 KB: 4,096 inner values of 8 rows
+    constexpr int reach = kXVecs * kFewThreads;
+    static_assert(NT == 1, "x is staged for one tile of 8 rows");
     int c = 1;
     while (c * reach < a.w.ins) c *= 2;
     f.cluster = c;

@@ -10,8 +10,10 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import numpy as np
+import torch
 
 from . import sampler, serve
 from .serve import want
@@ -24,6 +26,12 @@ E4M3_MAX = 448.0
 SCALE_EXP = 32  # page scales written by append lie in [2^-32, 2^32]
 LAYOUTS = {"half": 0, "interleaved": 1}
 
+# arc_kv_step, arc_kv_rows and arc_kv_query, packed for a call (a ctypes structure takes three times as long)
+_STEP = struct.Struct("@PqPPqqii")
+_ROWS = struct.Struct("@PPPPqqqqqqqqii")
+_QUERY = struct.Struct("@PPqqqqiifi")
+_I32 = torch.int32
+
 
 class PagedCache:
     """Keys and values as e4m3 codes [pages, heads, page_size, head_dim] (float8_e4m3fn or
@@ -31,8 +39,6 @@ class PagedCache:
     value = code * scale.  page_size 16, 32, 64, 128 or 256; head_dim 64, 128 or 256."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
-
         for x in (k, v):
             want(x.dim() == 4 and x.shape == k.shape, "k and v must be [pages, heads, page_size, head_dim]")
             if x.dtype not in (torch.float8_e4m3fn, torch.uint8):
@@ -48,6 +54,8 @@ class PagedCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page_size, self.head_dim = pages, heads, ps, d
         self.device = k.device
+        self.index = k.get_device()
+        self.default_scale = d ** -0.5
         self._c = serve.KvCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0),
                                 k.stride(1), pages, heads, ps, d)
         self._ref = ctypes.addressof(self._c)
@@ -55,8 +63,6 @@ class PagedCache:
     @classmethod
     def empty(cls, pages: int, heads: int, page_size: int, head_dim: int, device="cuda"):
         """A cache whose pages hold nothing yet."""
-        import torch
-
         shape = (pages, heads, page_size, head_dim)
         k, v = (torch.empty(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
         ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
@@ -64,8 +70,6 @@ class PagedCache:
 
     def attend_workspace(self):
         """Zero-filled workspace for `attend` over caches of this shape (one per stream that uses it)."""
-        import torch
-
         n = int(serve.load().arc_kv_attend_workspace_bytes(self._ref))
         want(n > 0, "arc_kv_attend_workspace_bytes rejected the cache")
         return torch.zeros(n, dtype=torch.uint8, device=self.device)
@@ -77,8 +81,6 @@ class Rope:
     "interleaved") and the factor on the rotated values."""
 
     def __init__(self, turns, layout: str = "half", amplitude: float = 1.0):
-        import torch
-
         want(layout in LAYOUTS, f"layout must be one of {sorted(LAYOUTS)}")
         want(turns.dim() == 1 and turns.is_contiguous(), "turns must be contiguous [rot_dim / 2]")
         if turns.dtype != torch.int64:
@@ -121,31 +123,44 @@ def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str | None = None, 
     return np.floor(freq / (2.0 * math.pi) * 2.0 ** 64).astype(np.uint64).astype(np.int64), amplitude
 
 
-def _check_heads(x, T, heads, dim, name):
+def _bad_heads(x, T, heads, dim, name):
     want(x.dim() == 3 and x.shape[0] == T and x.shape[2] == dim and (heads is None or x.shape[1] == heads),
          f"{name} must be [tokens, heads, head_dim] with head_dim {dim}" + ("" if heads is None else f", {heads} heads"))
     want(x.stride(2) == 1, f"the values of a head of {name} must be contiguous")
 
 
-def _step(cache, T, positions, page_table, row_offsets):
-    import torch
+def _heads(x, T, heads, dim, name):
+    """(token stride, head stride, heads) of a checked [T, heads, dim] tensor."""
+    if x.dim() == 3:
+        t, h, d = x.shape
+        a, b, c = x.stride()
+        if t == T and d == dim and c == 1 and (heads is None or h == heads):
+            return a, b, h
+    _bad_heads(x, T, heads, dim, name)
+    raise ValueError(f"{name} has a shape that cannot be used")
 
-    want(page_table.dim() == 2 and page_table.stride(1) == 1, "page_table must be [sequences, pages], rows contiguous")
-    B = page_table.shape[0]
+
+def _step(cache, T, positions, page_table, row_offsets):
+    """arc_kv_step as bytes."""
+    want(page_table.dim() == 2, "page_table must be [sequences, pages]")
+    B, pages = page_table.shape
+    stride, one = page_table.stride()
+    want(one == 1 or pages == 1, "rows of page_table must be contiguous")
     want(positions.shape == (B,) and positions.is_contiguous(), "positions must be contiguous [sequences]")
-    ints = [page_table, positions]
+    offsets = 0
     if row_offsets is not None:
         want(row_offsets.shape == (B + 1,) and row_offsets.is_contiguous(), "row_offsets must be contiguous [sequences + 1]")
-        ints.append(row_offsets)
+        if row_offsets.dtype != _I32:
+            raise TypeError("row_offsets must be int32")
+        want(row_offsets.get_device() == cache.index, "every tensor must be on the cache's device")
+        offsets = row_offsets.data_ptr()
     else:
         want(T == B, "without row_offsets there is one new token for each sequence")
-    for x in ints:
-        if x.dtype != torch.int32:
-            raise TypeError("page_table, positions and row_offsets must be int32")
-        want(x.device == cache.device, "every tensor must be on the cache's device")
-    return serve.KvStep(page_table.data_ptr(), page_table.stride(0) if B > 1 else page_table.shape[1],
-                        positions.data_ptr(), None if row_offsets is None else row_offsets.data_ptr(), B, T,
-                        page_table.shape[1], 0)
+    if page_table.dtype != _I32 or positions.dtype != _I32:
+        raise TypeError("page_table and positions must be int32")
+    want(page_table.get_device() == cache.index and positions.get_device() == cache.index,
+         "every tensor must be on the cache's device")
+    return _STEP.pack(page_table.data_ptr(), stride if B > 1 else pages, positions.data_ptr(), offsets, B, T, pages, 0)
 
 
 def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, rope: Rope | None = None,
@@ -156,33 +171,30 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
     returned.  positions int32 [B]: tokens each sequence holds before these (negative:
     parked); page_table int32 [B, pages]; row_offsets int32 [B + 1] or None for one new
     token each; err_word int32 [1]: ARC_KV_ERR_* bits."""
-    import torch
-
-    T = k.shape[0]
-    _check_heads(k, T, cache.heads, cache.head_dim, "k")
-    _check_heads(v, T, cache.heads, cache.head_dim, "v")
-    want(k.dtype == v.dtype, "k and v must have one type")
-    want(k.device == cache.device and v.device == cache.device, "every tensor must be on the cache's device")
-    rows = serve.KvRows(None, k.data_ptr(), v.data_ptr(), None, 0, 0, k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                        0, 0, 0, serve.dtype_code(k))
+    T, dim, dev = k.shape[0], cache.head_dim, cache.index
+    kt, kh, _ = _heads(k, T, cache.heads, dim, "k")
+    vt, vh, _ = _heads(v, T, cache.heads, dim, "v")
+    dtype = k.dtype
+    want(v.dtype == dtype, "k and v must have one type")
+    want(k.get_device() == dev and v.get_device() == dev, "every tensor must be on the cache's device")
+    qp = op = qt = qh = ot = oh = heads = 0
     if q is not None:
-        _check_heads(q, T, None, cache.head_dim, "q")
-        want(q.dtype == k.dtype and q.device == cache.device, "q must have k's type and device")
+        qt, qh, heads = _heads(q, T, None, dim, "q")
+        want(q.dtype == dtype and q.get_device() == dev, "q must have k's type and device")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = q.new_empty((T, heads, dim))
         elif q_out is not q:
-            _check_heads(q_out, T, q.shape[1], cache.head_dim, "q_out")
-            want(q_out.dtype == q.dtype and q_out.device == q.device, "q_out must have q's type and device")
-        rows.q, rows.q_out, rows.q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        rows.q_token_stride, rows.q_head_stride = q.stride(0), q.stride(1)
-        rows.out_token_stride, rows.out_head_stride = q_out.stride(0), q_out.stride(1)
+            want(q_out.dtype == dtype and q_out.get_device() == dev, "q_out must have q's type and device")
+        ot, oh, _ = _heads(q_out, T, heads, dim, "q_out")
+        qp, op = q.data_ptr(), q_out.data_ptr()
     else:
         want(q_out is None, "q_out without q")
     if rope is not None:
-        want(rope.turns.device == cache.device, "every tensor must be on the cache's device")
-    step = _step(cache, T, positions, page_table, row_offsets)
-    rc = serve.load().arc_kv_append(cache._ref, ctypes.addressof(step), ctypes.addressof(rows),
-                                    None if rope is None else rope._ref, sampler._ptr(err_word), serve.stream_of(stream, cache.device))
+        want(rope.turns.get_device() == dev, "every tensor must be on the cache's device")
+    rows = _ROWS.pack(qp, k.data_ptr(), v.data_ptr(), op, qt, qh, kt, kh, vt, vh, ot, oh, heads, serve.dtype_code(k))
+    rc = serve.load().arc_kv_append(cache._ref, _step(cache, T, positions, page_table, row_offsets), rows,
+                                    None if rope is None else rope._ref, sampler._ptr(err_word),
+                                    serve.stream_of(stream, dev))
     serve.finish(rc, check)
     return q_out
 
@@ -193,22 +205,22 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
     that `append` has just extended (the same positions, page_table and row_offsets).  scale:
     head_dim ** -0.5 where None.  window > 0: each token sees its last `window` tokens alone.
     workspace: cache.attend_workspace(), made for the call where None.  Returns out."""
-    import torch
-
-    T = q.shape[0]
-    _check_heads(q, T, None, cache.head_dim, "q")
+    T, dim, dev = q.shape[0], cache.head_dim, cache.index
+    qt, qh, heads = _heads(q, T, None, dim, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty((T, heads, dim))
+        ot, oh = heads * dim, dim
     else:
-        _check_heads(out, T, q.shape[1], cache.head_dim, "out")
+        ot, oh, _ = _heads(out, T, heads, dim, "out")
         want(out.dtype == q.dtype, "out must have q's type")
-    want(q.device == cache.device and out.device == cache.device, "every tensor must be on the cache's device")
+    want(q.get_device() == dev and out.get_device() == dev, "every tensor must be on the cache's device")
+    code = serve.dtype_code(q)
     if workspace is None:
         workspace = cache.attend_workspace()
-    query = serve.KvQuery(q.data_ptr(), out.data_ptr(), q.stride(0), q.stride(1), out.stride(0), out.stride(1),
-                          q.shape[1], serve.dtype_code(q), cache.head_dim ** -0.5 if scale is None else scale, int(window))
-    step = _step(cache, T, positions, page_table, row_offsets)
-    rc = serve.load().arc_kv_attend(cache._ref, ctypes.addressof(step), ctypes.addressof(query), sampler._ptr(err_word),
-                                    workspace.data_ptr(), workspace.numel(), serve.stream_of(stream, cache.device))
+    query = _QUERY.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, heads, code,
+                        cache.default_scale if scale is None else scale, window)
+    rc = serve.load().arc_kv_attend(cache._ref, _step(cache, T, positions, page_table, row_offsets), query,
+                                    sampler._ptr(err_word), workspace.data_ptr(), workspace.numel(),
+                                    serve.stream_of(stream, dev))
     serve.finish(rc, check)
     return out

@@ -9,6 +9,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 from . import sampler
 from .workloads import DTYPE_BF16, DTYPE_F16, DTYPE_F32
 
@@ -91,27 +93,23 @@ class ServeError(sampler.ArcError):
         self.rc = rc
 
 
+_CODES = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
 def dtype_code(t, f32: bool = False) -> int:
     """ARC_* code of a tensor's type: bfloat16 or float16 (or float32 where allowed)."""
-    import torch
-
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float16:
-        return DTYPE_F16
+    code = _CODES.get(t.dtype)
+    if code is not None:
+        return code
     if f32 and t.dtype == torch.float32:
         return DTYPE_F32
     raise TypeError(f"must be bfloat16 or float16{' or float32' if f32 else ''}, not {t.dtype}")
 
 
-def stream_of(stream, device) -> int:
-    """The stream's handle; the device's current stream where None.  torch.cuda.current_stream()
-    builds a Stream object and resolves the device's name, 7 us of a 20 us call on the Arm host."""
-    import torch
-
-    if stream is not None:
-        return int(stream.cuda_stream)
-    return torch._C._cuda_getCurrentRawStream(device.index or 0)
+def stream_of(stream, device: int) -> int:
+    """The stream's handle; the device's current stream where None (torch.cuda.current_stream()
+    builds a Stream object and resolves the device's name, 7 us of a 20 us call on the Arm host)."""
+    return int(stream.cuda_stream) if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 def want(ok: bool, text: str) -> None:

@@ -1,12 +1,17 @@
 """Products of a few rows with 4-bit weights and group scales (include/serve/arc_w4.h)."""
 from __future__ import annotations
 
-import ctypes
+import struct
 
-from . import sampler, serve
+import torch
+
+from . import serve
 from .serve import want
 
 MAX_ROWS = 256
+FEW_ROWS = 8  # more rows need a workspace
+
+_WEIGHT = struct.Struct("@PPPqqii")  # arc_w4_weight
 
 
 def pack(q):
@@ -19,39 +24,43 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
     (q - zero) * scale, weight uint8 [outs, ins / 2] (see pack), scales [outs, ins / group] of
     x's type with group 32, 64 or 128, zeros uint8 [outs, ins / group] or None for 8.  Returns
     out [rows, outs] of x's type, or float32 with out_dtype."""
-    import torch
-
     want(x.dim() == 2 and weight.dim() == 2 and scales.dim() == 2, "x, weight and scales must be matrices")
     rows, ins = x.shape
     outs, groups = scales.shape
-    want(x.stride(1) == 1, "rows of x must be contiguous")
+    xs, one = x.stride()
+    want(one == 1, "rows of x must be contiguous")
     if weight.dtype != torch.uint8:
         raise TypeError(f"weight must be uint8, not {weight.dtype}")
-    want(weight.shape == (outs, ins // 2) and weight.stride(1) == 1 and ins % 2 == 0,
-         "weight must be [outs, ins / 2], rows contiguous")
+    ws, one = weight.stride()
+    want(weight.shape == (outs, ins // 2) and one == 1 and ins % 2 == 0, "weight must be [outs, ins / 2], rows contiguous")
     want(groups > 0 and ins % groups == 0 and scales.is_contiguous(), "scales must be contiguous [outs, ins / group]")
     if scales.dtype != x.dtype:
         raise TypeError("scales must have x's type")
+    dev, zp = x.get_device(), 0
     if zeros is not None:
         want(zeros.shape == scales.shape and zeros.is_contiguous(), "zeros must be contiguous [outs, ins / group]")
         if zeros.dtype != torch.uint8:
             raise TypeError(f"zeros must be uint8, not {zeros.dtype}")
+        want(zeros.get_device() == dev, "every tensor must be on x's device")
+        zp = zeros.data_ptr()
+    code = serve.dtype_code(x)
     if out is None:
-        out = torch.empty((rows, outs), dtype=out_dtype or x.dtype, device=x.device)
+        out = x.new_empty((rows, outs), dtype=out_dtype)
+        os = outs
     else:
         want(out.shape == (rows, outs) and out.stride(1) == 1, "out must be [rows, outs], rows contiguous")
         want(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
-    for t in (weight, scales, zeros, out):
-        want(t is None or t.device == x.device, "every tensor must be on x's device")
-    w = serve.W4Weight(weight.data_ptr(), scales.data_ptr(), sampler._ptr(zeros),
-                       weight.stride(0) if outs > 1 else weight.shape[1], outs, ins, ins // groups)
+        os = out.stride(0) if rows > 1 else outs
+    want(weight.get_device() == dev and scales.get_device() == dev and out.get_device() == dev,
+         "every tensor must be on x's device")
+    w = _WEIGHT.pack(weight.data_ptr(), scales.data_ptr(), zp, ws if outs > 1 else ins // 2, outs, ins, ins // groups)
     lib = serve.load()
-    ref = ctypes.addressof(w)
-    need = lib.arc_w4_workspace_bytes(ref, rows)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    rc = lib.arc_w4_matvec(ref, x.data_ptr(), rows, x.stride(0) if rows > 1 else ins, serve.dtype_code(x), out.data_ptr(),
-                           out.stride(0) if rows > 1 else outs, serve.dtype_code(out, f32=True),
-                           sampler._ptr(workspace), 0 if workspace is None else workspace.numel(), serve.stream_of(stream, x.device))
+    wp, wn = 0, 0
+    if rows > FEW_ROWS:
+        if workspace is None:
+            workspace = x.new_empty(lib.arc_w4_workspace_bytes(w, rows), dtype=torch.uint8)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    rc = lib.arc_w4_matvec(w, x.data_ptr(), rows, xs if rows > 1 else ins, code, out.data_ptr(), os,
+                           serve.dtype_code(out, True), wp, wn, serve.stream_of(stream, dev))
     serve.finish(rc, check)
     return out
