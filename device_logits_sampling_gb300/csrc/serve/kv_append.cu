@@ -366,11 +366,11 @@ __device__ __forceinline__ void put16(const AppendArgs& a, const Place& p, const
 // Four e4m3 codes times `f`, a power of two: shifts exponents, rounds below
 // the normal range.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
-    uint32_t out = 0;
+    uint32_t h[2], out = 0;
+    e4m3x4_to_half2(w, h[0], h[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t h = e4m3x2_to_half2(w >> (16 * i));
-        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
         out |= e4m3x2(x.x * f, x.y * f) << (16 * i);
     }
     return out;
@@ -561,24 +561,34 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
         for (int k = 0; k < kKept; ++k)
             if (k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, turns[k]);
     }
+    Raw ahead[kKept];  // the next head's values
+    auto look = [&](int h) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (k * per + my < rows) ahead[k] = load16(p, src0 + h * hs * 2 + (k * per + my) * ts * 2, vec);
+    };
     const int h1 = set * a.page_heads + a.page_heads < a.c.heads ? set * a.page_heads + a.page_heads : a.c.heads;
+    look(set * a.page_heads);
     for (int h = set * a.page_heads; h < h1; ++h) {
         const char* src = src0 + h * hs * 2;
         const float was = scales[h];
         bool nan = false;
-        auto fetch = [&](int r, const Turns& t, Sixteen& v) {
+        auto fetch = [&](int r, const Raw& raw, const Turns& t, Sixteen& v) {
             v.err = v.top = 0.0f;
             if (r < rows) {
-                unpack16<DT>(load16(p, src + r * ts * 2, vec), v.y);
+                unpack16<DT>(raw, v.y);
                 if (!V) v.err = turn16<DT, TURN>(a, p, t, src + r * ts * 2, page0 + slot0 + r, v.y);
                 nan |= finish16(v);
             }
+        };
+        auto again = [&](int k) {
+            return k * per + my < rows ? load16(p, src + (k * per + my) * ts * 2, vec) : Raw{};
         };
         Sixteen kept[kKept];
         float lo = 0.0f, hi = 0.0f;
 #pragma unroll
         for (int k = 0; k < kKept; ++k) {
-            fetch(k * per + my, turns[k], kept[k]);
+            fetch(k * per + my, ahead[k], turns[k], kept[k]);
             lo = fmaxf(lo, kept[k].top - kept[k].err);
             hi = fmaxf(hi, kept[k].top + kept[k].err);
         }
@@ -586,10 +596,11 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
             Sixteen v;
             Turns t;
             if (!V && k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, t);
-            fetch(k * per + my, t, v);
+            fetch(k * per + my, again(k), t, v);
             lo = fmaxf(lo, v.top - v.err);
             hi = fmaxf(hi, v.top + v.err);
         }
+        if (h + 1 < h1) look(h + 1);
         // magnitudes are not negative: their bits order as they do
         const uint32_t wl = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(lo));
         const uint32_t wh = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(hi));
@@ -647,7 +658,7 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
             Sixteen v;
             Turns t;
             if (!V && k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, t);
-            fetch(k * per + my, t, v);
+            fetch(k * per + my, again(k), t, v);
             put(k * per + my, v);
         }
         if (tid == 0) scales[h] = exp2i(e);  // every thread read it before the barrier
@@ -767,7 +778,7 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
     if (rows->q_heads > 0) {
         // few tokens: each head its own threads; many: one thread turns all heads of its eight values
         const int64_t units = step->T * L;
-        while (a.head_sets < rows->q_heads && units * a.head_sets < 152 * 1024) a.head_sets *= 2;
+        while (a.head_sets < rows->q_heads && units * a.head_sets < 152 * 4096) a.head_sets *= 2;
         if (a.head_sets > rows->q_heads) a.head_sets = rows->q_heads;
         a.q_blocks = (units * a.head_sets + kThreads - 1) / kThreads;
     }
@@ -780,7 +791,7 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
         const int64_t most = step->T / cache->page_size + 2 * seqs;
         const int64_t pages = most < step->T ? most : step->T;
         // many pages: a block stores several heads with one set of angles
-        while (a.page_heads < 4 && a.page_heads < cache->heads && pages * cache->heads / a.page_heads > 1024) a.page_heads *= 2;
+        while (a.page_heads < 4 && a.page_heads < cache->heads && pages * cache->heads / a.page_heads > 512) a.page_heads *= 2;
         kv_blocks = pages * 2 * ((cache->heads + a.page_heads - 1) / a.page_heads);
     }
     const int64_t grid = a.q_blocks + kv_blocks;

@@ -61,7 +61,7 @@ struct Shape<64, 1> {
 };
 template <>
 struct Shape<64, 2> {
-    static constexpr int kWarps = 16, kStages = 4;
+    static constexpr int kWarps = 12, kStages = 4;
 };
 template <>
 struct Shape<128, 1> {
@@ -69,7 +69,7 @@ struct Shape<128, 1> {
 };
 template <>
 struct Shape<128, 2> {
-    static constexpr int kWarps = 10, kStages = 3;
+    static constexpr int kWarps = 8, kStages = 4;
 };
 template <>
 struct Shape<256, 1> {
@@ -221,21 +221,6 @@ struct Cursor {
             q = load_seq<R>(a, b);
         } while (q.cost == 0);
     }
-    // to the next unit that is a step; false at the end of the piece
-    __device__ __forceinline__ bool to_step(const AttendArgs& a) {
-        while (left > 0) {
-            if (unit == q.cost) {
-                next_item(a);
-            } else if (unit < kItemCost) {
-                ++unit;
-                --left;
-            } else {
-                return true;
-            }
-        }
-        return false;
-    }
-    __device__ __forceinline__ int step() const { return q.step0 + unit - kItemCost; }
 };
 
 template <int D, int NT>
@@ -336,48 +321,74 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
         Cursor<R> ahead = at;
 
         // ---- copies
-        const int ps_shift = 31 - __clz(a.c.page_size);
-        int issued = 0;           // stage of the next copy
-        int page = -1, page_of = -1, page_next = -1;  // current page id, its index, the id after it
-        int64_t page_seq = -1;
+        int issued = 0;                 // stage of the next copy
+        int step = 0, step_end = 0;     // of the item that is being copied
+        int first = 0, last = 0;        // tokens that its rows see; the others are filled with zeros
+        const int32_t* table = nullptr;
+        const char *k_head = nullptr, *v_head = nullptr;  // its head, this lane's 16 bytes
+        const float *k_scale = nullptr, *v_scale = nullptr;
+        int page = 0, page_of = -1, page_next = 0;  // current page id, its index, the id after it
+        int64_t page_at = 0;
+        bool ok = true;
+        const int ps_shift = 31 - __clz(a.c.page_size), ps_mask = a.c.page_size - 1;
+        auto enter = [&]() {  // the next item that has a step
+            while (step == step_end && ahead.left > 0) {
+                if (ahead.unit == ahead.q.cost) ahead.next_item(a);
+                if (ahead.left <= 0) return;
+                const int n = ahead.q.cost - ahead.unit < ahead.left ? ahead.q.cost - ahead.unit : static_cast<int>(ahead.left);
+                step = ahead.q.step0 + (ahead.unit > kItemCost ? ahead.unit - kItemCost : 0);
+                ahead.unit += n;
+                ahead.left -= n;
+                step_end = ahead.q.step0 + (ahead.unit > kItemCost ? ahead.unit - kItemCost : 0);
+            }
+            const int row0 = ahead.tile * R, rows = ahead.q.n * a.group;
+            last = ahead.q.pos + ((row0 + R < rows ? row0 + R : rows) - 1) / a.group;
+            first = a.q.window > 0 ? ahead.q.pos + row0 / a.group - a.q.window + 1 : 0;
+            table = a.s.page_table + ahead.b * a.s.table_stride;
+            const int64_t head = ahead.head * a.c.head_stride + lane * 16;
+            k_head = static_cast<const char*>(a.c.k) + head;
+            v_head = static_cast<const char*>(a.c.v) + head;
+            k_scale = a.c.k_scale + ahead.head;
+            v_scale = a.c.v_scale + ahead.head;
+            page_of = -1;
+        };
+        uint32_t to[2];  // a lane's copies alternate between two places of a pattern that moves on by rows
+        to[0] = ring + chunk_at<D>(lane / (D / 16), lane % (D / 16));
+        to[1] = ring + chunk_at<D>((lane + 32) / (D / 16), (lane + 32) % (D / 16));
         auto issue = [&]() {
-            if (ahead.to_step(a)) {
-                const int tok0 = ahead.step() << 4, pi = tok0 >> ps_shift;
-                const int32_t* table = a.s.page_table + ahead.b * a.s.table_stride;
-                if (ahead.b != page_seq || pi != page_of) {
-                    page = ahead.b == page_seq && pi == page_of + 1 ? page_next : __ldg(table + pi);
-                    page_seq = ahead.b;
+            if (step == step_end) enter();
+            if (step < step_end) {
+                const int tok0 = step << 4, pi = tok0 >> ps_shift;
+                if (pi != page_of) {
+                    page = page_of >= 0 ? page_next : __ldg(table + pi);
                     page_of = pi;
-                    const int more = pi + 1 < a.s.max_pages ? pi + 1 : pi;
-                    page_next = __ldg(table + more);
+                    if (((pi + 1) << ps_shift) >> 4 < step_end) page_next = __ldg(table + pi + 1);
+                    ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+                    page_at = ok ? page * a.c.page_stride : 0;
+                    if (!ok && lane == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
                 }
-                const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
-                const int id = ok ? page : 0;
-                // tokens that no row of the tile sees are filled with zeros
-                const int row0 = ahead.tile * R, rows = ahead.q.n * a.group;
-                const int last = ahead.q.pos + ((row0 + R < rows ? row0 + R : rows) - 1) / a.group;
-                const int first = a.q.window > 0 ? ahead.q.pos + row0 / a.group - a.q.window + 1 : 0;
-                const int64_t base = id * a.c.page_stride + ahead.head * a.c.head_stride +
-                                     int64_t{tok0 - (pi << ps_shift)} * D;
-                const uint32_t dst = ring + issued * S::kStage;
+                const int64_t at = page_at + (tok0 & ps_mask) * D;
+                const char *kp = k_head + at, *vp = v_head + at;
+                const uint32_t move = issued * S::kStage;
+                const bool whole = ok && tok0 >= first && tok0 + 15 <= last;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    const int c = lane + 32 * i, r = c / (D / 16), cc = c % (D / 16);
-                    const bool on = ok && tok0 + r <= last && tok0 + r >= first;
-                    copy16(dst + chunk_at<D>(r, cc), static_cast<const char*>(a.c.k) + base + c * 16, on);
-                    copy16(dst + 16 * D + chunk_at<D>(r, cc), static_cast<const char*>(a.c.v) + base + c * 16, on);
+                    // D = 256: the pattern of chunk_at has a period of 16 rows, eight copies
+                    const uint32_t dst = (D == 256 ? ring + chunk_at<D>((lane + 32 * i) / 16, (lane + 32 * i) % 16)
+                                                   : to[i & 1] + (i >> 1) * 1024) + move;
+                    const bool on = whole || (ok && tok0 + (lane + 32 * i) / (D / 16) <= last && tok0 + (lane + 32 * i) / (D / 16) >= first);
+                    copy16(dst, kp + i * 512, on);
+                    copy16(dst + 16 * D, vp + i * 512, on);
                 }
-                const int64_t si = static_cast<int64_t>(id) * a.c.heads + ahead.head;
+                const int64_t si = static_cast<int64_t>(ok ? page : 0) * a.c.heads;
                 if (ok) {
                     if (lane < 2)
                         copy4(static_cast<uint32_t>(__cvta_generic_to_shared(&sm.scales[warp][issued][lane])),
-                              (lane ? a.c.v_scale : a.c.k_scale) + si);
-                } else {
-                    if (lane < 2) sm.scales[warp][issued][lane] = __int_as_float(0x7FC00000);
-                    if (lane == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
+                              (lane ? v_scale : k_scale) + si);
+                } else if (lane < 2) {
+                    sm.scales[warp][issued][lane] = __int_as_float(0x7FC00000);
                 }
-                ++ahead.unit;
-                --ahead.left;
+                ++step;
             }
             copies_end();
             issued = issued + 1 == ST ? 0 : issued + 1;
@@ -481,8 +492,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                     const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const uint32_t a0 = e4m3x2_to_half2(w0[w]), a2 = e4m3x2_to_half2(w0[w] >> 16);
-                        const uint32_t a1 = e4m3x2_to_half2(w1[w]), a3 = e4m3x2_to_half2(w1[w] >> 16);
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_half2(w0[w], a0, a2);
+                        e4m3x4_to_half2(w1[w], a1, a3);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
@@ -614,8 +626,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                     const int w = i >> 1;
                     const uint32_t x = __byte_perm(v[0][w], v[1][w], (i & 1) ? 0x7362 : 0x5140);
                     const uint32_t y = __byte_perm(v[2][w], v[3][w], (i & 1) ? 0x7362 : 0x5140);
-                    const uint32_t a0 = e4m3x2_to_half2(x), a1 = e4m3x2_to_half2(x >> 16);
-                    const uint32_t a2 = e4m3x2_to_half2(y), a3 = e4m3x2_to_half2(y >> 16);
+                    uint32_t a0, a1, a2, a3;
+                    e4m3x4_to_half2(x, a0, a1);
+                    e4m3x4_to_half2(y, a2, a3);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
                 }

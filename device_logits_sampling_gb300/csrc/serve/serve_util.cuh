@@ -83,10 +83,11 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The two e4m3 codes in the low 16 bits of w as f16x2 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t w) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// The four e4m3 codes of w as two f16x2 (exact), the lower two first.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 // Least e in [-32, 32] with amax <= 448 * 2^e; 448 = 1.75 * 2^8, so the
