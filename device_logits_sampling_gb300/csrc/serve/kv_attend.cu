@@ -98,6 +98,7 @@ struct Smem {
     int64_t before[kThreads + 1];
     int64_t wsum[kW];
     uint32_t last;
+    float weight[kMaxBlocks][kR];  // of the blocks' partials in their join
     static constexpr int kBytes = kW * kPerWarp;
 };
 
@@ -285,10 +286,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     const int64_t blocks = want < gridDim.x ? want : gridDim.x;
     if (blockIdx.x >= blocks) return;
     const int64_t pieces = blocks * W, piece = static_cast<int64_t>(blockIdx.x) * W + warp;
-    // floor(total * i / of), without the product
+    // floor(total * i / of), without the product; four lanes find the four cuts
     auto cut = [total](int64_t i, int64_t of) { return total / of * i + total % of * i / of; };
-    const int64_t from = cut(piece, pieces), to = cut(piece + 1, pieces);
-    const int64_t block_from = cut(blockIdx.x, blocks), block_to = cut(blockIdx.x + 1, blocks);
+    const int64_t cuts = cut(lane < 2 ? piece + lane : int64_t{blockIdx.x} + (lane & 1), lane < 2 ? pieces : blocks);
+    const int64_t from = __shfl_sync(0xFFFFFFFFu, cuts, 0), to = __shfl_sync(0xFFFFFFFFu, cuts, 1);
+    const int64_t block_from = __shfl_sync(0xFFFFFFFFu, cuts, 2), block_to = __shfl_sync(0xFFFFFFFFu, cuts, 3);
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(dyn)) + warp * S::kPerWarp;
     float* const head_store = reinterpret_cast<float*>(dyn + warp * S::kPerWarp + S::kRing);
@@ -312,9 +314,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 rest -= units_of(a, at.q);
                 at.q = load_seq<R>(a, ++at.b);
             }
-            const int64_t item = at.q.cost > 0 ? rest / at.q.cost : 0;
+            const int64_t item = at.q.cost <= 0     ? 0
+                                 : rest >> 31 == 0 ? static_cast<uint32_t>(rest) / static_cast<uint32_t>(at.q.cost)
+                                                   : rest / at.q.cost;
             at.unit = static_cast<int32_t>(rest - item * at.q.cost);
-            at.tile = static_cast<int32_t>(item / a.c.heads);
+            at.tile = static_cast<int32_t>(item >> 31 == 0 ? static_cast<uint32_t>(item) / static_cast<uint32_t>(a.c.heads)
+                                                           : item / a.c.heads);
             at.head = static_cast<int32_t>(item - int64_t{at.tile} * a.c.heads);
             at.left = at.q.cost > 0 ? to - from : 0;
         }
@@ -754,31 +759,60 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
         e0 = e1;
         if (whole) continue;
         // ---- an item over several blocks: the last of them to arrive joins all, in order
-        auto block_of = [&](int64_t f) { return ((f + 1) * blocks - 1) / total; };
-        const int64_t c0 = block_of(p.from), c1 = block_of(p.to - 1);
+        // (the block of unit f is floor(((f + 1) * blocks - 1) / total))
+        const int64_t ends = (((lane ? p.to - 1 : p.from) + 1) * blocks - 1) / total;
+        const int64_t c0 = __shfl_sync(0xFFFFFFFFu, ends, 0), c1 = __shfl_sync(0xFFFFFFFFu, ends, 1);
         __threadfence();
         __syncthreads();
         if (tid == 0) sm.last = atomicInc(a.arrived + c0, static_cast<uint32_t>(c1 - c0)) == static_cast<uint32_t>(c1 - c0);
         __syncthreads();
         if (sm.last) {
             __threadfence();
+            const int n = static_cast<int>(c1 - c0) + 1;
+            const float* first = a.partial + (c0 * 2 + 1) * kSlot;  // the item starts in c0's second slot,
+            auto slot_of = [&](int c) { return first + (c == 0 ? 0 : (2 * c - 1) * kSlot); };  // then the first ones
+            // a warp for each row: the blocks' weights, whose sum of sums is 1
+            for (int r = warp; r < R; r += W) {
+                float mc[kMaxBlocks / 32], lc[kMaxBlocks / 32];
+#pragma unroll
+                for (int k = 0; k < kMaxBlocks / 32; ++k) {
+                    const int c = lane + 32 * k;
+                    mc[k] = c < n ? __ldcg(slot_of(c) + R * D + r) : -INFINITY;
+                    lc[k] = c < n ? __ldcg(slot_of(c) + R * D + R + r) : 0.0f;
+                }
+                float mm = -INFINITY, l = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kMaxBlocks / 32; ++k) mm = fmaxf(mm, mc[k]);
+#pragma unroll
+                for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
+#pragma unroll
+                for (int k = 0; k < kMaxBlocks / 32; ++k) {
+                    mc[k] = mc[k] == -INFINITY ? (lc[k] != lc[k] ? 1.0f : 0.0f) : ex2(mc[k] - mm);
+                    l = fmaf(lc[k], mc[k], l);
+                }
+#pragma unroll
+                for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+#pragma unroll
+                for (int k = 0; k < kMaxBlocks / 32; ++k) {
+                    const int c = lane + 32 * k;
+                    if (c < n) sm.weight[c][r] = mc[k] / l;
+                }
+            }
+            __syncthreads();
             for (int i = tid; i < R * D / 2; i += kThreads) {
                 const int r = i / (D / 2), d = (i % (D / 2)) * 2;
                 if (p.row0 + r >= p.rows) continue;
-                float mm = -INFINITY;
-                for (int64_t c = c0; c <= c1; ++c)
-                    mm = fmaxf(mm, __ldcg(a.partial + (c * 2 + (c == c0)) * kSlot + R * D + r));
-                float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
-                for (int64_t c = c0; c <= c1; ++c) {
-                    const float* q = a.partial + (c * 2 + (c == c0)) * kSlot;
-                    const float mc = __ldcg(q + R * D + r), lc = __ldcg(q + R * D + R + r);
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(q + r * D + d));
-                    const float f = mc == -INFINITY ? (lc != lc ? 1.0f : 0.0f) : ex2(mc - mm);
-                    l = fmaf(lc, f, l);
-                    x0 = fmaf(v.x, f, x0);
-                    x1 = fmaf(v.y, f, x1);
+                const float* q = first + r * D + d;
+                float2 v = __ldcg(reinterpret_cast<const float2*>(q));
+                float x0 = v.x * sm.weight[0][r], x1 = v.y * sm.weight[0][r];
+                q += kSlot;
+#pragma unroll 8
+                for (int c = 1; c < n; ++c, q += 2 * kSlot) {
+                    v = __ldcg(reinterpret_cast<const float2*>(q));
+                    x0 = fmaf(v.x, sm.weight[c][r], x0);
+                    x1 = fmaf(v.y, sm.weight[c][r], x1);
                 }
-                write_row(p, r, d, x0 / l, x1 / l);
+                write_row(p, r, d, x0, x1);
             }
         }
         __syncthreads();
