@@ -347,8 +347,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 step_end = ahead.q.step0 + (ahead.unit > kItemCost ? ahead.unit - kItemCost : 0);
             }
             const int row0 = ahead.tile * R, rows = ahead.q.n * a.group;
-            last = ahead.q.pos + ((row0 + R < rows ? row0 + R : rows) - 1) / a.group;
-            first = a.q.window > 0 ? ahead.q.pos + row0 / a.group - a.q.window + 1 : 0;
+            const bool one = ahead.q.n == 1;
+            last = ahead.q.pos + (one ? 0 : ((row0 + R < rows ? row0 + R : rows) - 1) / a.group);
+            first = a.q.window > 0 ? ahead.q.pos + (one ? 0 : row0 / a.group) - a.q.window + 1 : 0;
             table = a.s.page_table + ahead.b * a.s.table_stride;
             const int64_t head = ahead.head * a.c.head_stride + lane * 16;
             k_head = static_cast<const char*>(a.c.k) + head;
@@ -412,6 +413,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             const int32_t unit1 = at.q.cost - unit0 < at.left ? at.q.cost : unit0 + static_cast<int32_t>(at.left);
             const int row0 = at.tile * R, rows = at.q.n * a.group;
 
+            const bool one = at.q.n == 1;  // a row's token, without the division where there is one
+            auto token_of = [&](int r) { return one ? 0 : r / a.group; };
+
             // queries: fp16, each row scaled by a power of two to [2^14, 2^15)
             uint32_t qf[NT][KS][2];
             float rf[NT][2];
@@ -420,7 +424,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             for (int nt = 0; nt < NT; ++nt) {
                 float x[D / 4];
                 const int r = row0 + 8 * nt + g;
-                const int tok = (r < rows ? r : rows - 1) / a.group;
+                const int tok = token_of(r < rows ? r : rows - 1);
                 if (r < rows) {
                     const char* p = static_cast<const char*>(a.q.q) +
                                     ((at.q.first + tok) * a.q.q_token_stride +
@@ -458,11 +462,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 for (int e = 0; e < 2; ++e) {
                     rf[nt][e] = __shfl_sync(0xFFFFFFFFu, back, (2 * t + e) * 4);
                     const int rr = row0 + 8 * nt + 2 * t + e;
-                    hi[nt][e] = at.q.pos + (rr < rows ? rr : rows - 1) / a.group;
+                    hi[nt][e] = at.q.pos + token_of(rr < rows ? rr : rows - 1);
                 }
             }
-            const int hi_first = at.q.pos + row0 / a.group;
-            const int hi_last = at.q.pos + ((row0 + R < rows ? row0 + R : rows) - 1) / a.group;
+            const int hi_first = at.q.pos + token_of(row0);
+            const int hi_last = at.q.pos + token_of((row0 + R < rows ? row0 + R : rows) - 1);
 
             float o[NT][KS][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -657,7 +661,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                     for (int e = 0; e < 2; ++e) {
                         const int rr = row0 + 8 * nt + 2 * t + e;
                         if (rr >= rows) continue;
-                        const int tok = rr / a.group;
+                        const int tok = token_of(rr);
                         const float inv = 1.0f / l[nt][e];
                         char* p = static_cast<char*>(a.q.out) +
                                   ((at.q.first + tok) * a.q.out_token_stride +
@@ -705,65 +709,104 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     }
     __syncthreads();
 
-    // ---- join the block's partials: neighbours on the line that belong to one item
-    auto write_row = [&](const Part& p, int r, int d, float x0, float x1) {
-        const int rr = p.row0 + r;
-        if (rr >= p.rows) return;
-        const int tok = rr / a.group;
-        const int64_t at = (p.first + tok) * a.q.out_token_stride +
-                           (p.head * a.group + rr - tok * a.group) * a.q.out_head_stride + d;
-        uint16_t* out = static_cast<uint16_t*>(a.q.out) + at;
-        const uint32_t w = a.bf16 ? Half<ARC_BF16>::pack(x0, x1) : Half<ARC_F16>::pack(x0, x1);
-        out[0] = static_cast<uint16_t>(w);
-        out[1] = static_cast<uint16_t>(w >> 16);
-    };
-    auto store_of = [&](int slot) {
-        return reinterpret_cast<const float*>(dyn + (slot >> 1) * S::kPerWarp + ((slot & 1) ? 0 : S::kRing));
-    };
-    constexpr int kSlot = R * D + 2 * R;  // floats of a block's partial: output, maxima, sums
-    int e0 = 0;
-    while (e0 < 2 * W) {
-        const Part p = sm.part[e0];
-        if (p.from < 0) {
-            ++e0;
-            continue;
-        }
-        int e1 = e0 + 1;
-        while (e1 < 2 * W && (sm.part[e1].from == p.from || sm.part[e1].from < 0)) ++e1;
-        const bool whole = p.from >= block_from && p.to <= block_to;
-        float* slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (p.from >= block_from ? 1 : 0)) * kSlot;
-        for (int i = tid; i < R * D / 2; i += kThreads) {
-            const int r = i / (D / 2), d = (i % (D / 2)) * 2;
-            float mm = -INFINITY;
-            for (int e = e0; e < e1; ++e)
-                if (sm.part[e].from >= 0) mm = fmaxf(mm, sm.m[e][r]);
-            float l = 0.0f, x0 = 0.0f, x1 = 0.0f;
-            for (int e = e0; e < e1; ++e) {
-                if (sm.part[e].from < 0) continue;
-                const float f = sm.m[e][r] == -INFINITY ? (sm.l[e][r] != sm.l[e][r] ? 1.0f : 0.0f) : ex2(sm.m[e][r] - mm);
-                const float2 v = *reinterpret_cast<const float2*>(store_of(e) + r * D + d);
-                l = fmaf(sm.l[e][r], f, l);
-                x0 = fmaf(v.x, f, x0);
-                x1 = fmaf(v.y, f, x1);
-            }
-            if (whole) {
-                write_row(p, r, d, x0 / l, x1 / l);
-            } else {
-                __stcg(reinterpret_cast<float2*>(slot + r * D + d), make_float2(x0, x1));
-                if (d == 0) {
-                    __stcg(slot + R * D + r, mm);
-                    __stcg(slot + R * D + R + r, l);
-                }
+    // ---- join the block's partials.  Those of one item are a run; a warp takes a row of a run, lane e
+    // holds partial e's maximum and sum.
+    static_assert(2 * W <= 32, "a lane for each partial");
+    constexpr int DV = D / 32;                // values of a lane
+    constexpr int kSlot = R * D + 2 * R;      // floats of a block's partial: output, maxima, sums
+    auto write = [&](const Part& p, int r, const float (&x)[DV]) {
+        const int rr = p.row0 + r, tok = rr / a.group;
+        uint16_t* out = static_cast<uint16_t*>(a.q.out) + (p.first + tok) * a.q.out_token_stride +
+                        (p.head * a.group + rr - tok * a.group) * a.q.out_head_stride + lane * DV;
+        uint32_t w[DV / 2];
+#pragma unroll
+        for (int i = 0; i < DV / 2; ++i)
+            w[i] = a.bf16 ? Half<ARC_BF16>::pack(x[2 * i], x[2 * i + 1]) : Half<ARC_F16>::pack(x[2 * i], x[2 * i + 1]);
+        if (a.vec & 2) {
+            if constexpr (DV == 2)
+                *reinterpret_cast<uint32_t*>(out) = w[0];
+            else if constexpr (DV == 4)
+                *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+            else
+                *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < DV / 2; ++i) {
+                out[2 * i] = static_cast<uint16_t>(w[i]);
+                out[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
             }
         }
-        e0 = e1;
-        if (whole) continue;
-        // ---- an item over several blocks: the last of them to arrive joins all, in order
+    };
+    const int64_t my_from = lane < 2 * W ? sm.part[lane].from : -1;
+    const uint32_t run_of = __match_any_sync(0xFFFFFFFFu, my_from);
+    const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, my_from >= 0 && lane == __ffs(run_of) - 1);
+    const int runs = __popc(leaders);
+    for (int task = warp; task < runs * R; task += W) {
+        const int r = task % R;
+        const int lead = __fns(leaders, 0, task / R + 1);
+        const Part p = sm.part[lead];
+        if (p.row0 + r >= p.rows) continue;
+        const uint32_t run_mask = __shfl_sync(0xFFFFFFFFu, run_of, lead);
+        const bool in = (run_mask >> lane) & 1;
+        const float me = in ? sm.m[lane][r] : -INFINITY, le = in ? sm.l[lane][r] : 0.0f;
+        float mm = me;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
+        // a partial without a visible token counts nothing, but for a NaN
+        const float f = me == -INFINITY ? (le != le ? 1.0f : 0.0f) : ex2(me - mm);
+        float l = le * f;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+        float x[DV];
+#pragma unroll
+        for (int i = 0; i < DV; ++i) x[i] = 0.0f;
+        for (uint32_t left = run_mask; left; left &= left - 1) {
+            const int e = __ffs(left) - 1;
+            const float fe = __shfl_sync(0xFFFFFFFFu, f, e);
+            const float* v = reinterpret_cast<const float*>(dyn + (e >> 1) * S::kPerWarp + ((e & 1) ? 0 : S::kRing)) + r * D + lane * DV;
+#pragma unroll
+            for (int i = 0; i < DV; i += 2) {
+                const float2 y = *reinterpret_cast<const float2*>(v + i);
+                x[i] = fmaf(y.x, fe, x[i]);
+                x[i + 1] = fmaf(y.y, fe, x[i + 1]);
+            }
+        }
+        if (p.from >= block_from && p.to <= block_to) {
+#pragma unroll
+            for (int i = 0; i < DV; ++i) x[i] /= l;
+            write(p, r, x);
+        } else {
+            float* slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (p.from >= block_from ? 1 : 0)) * kSlot;
+#pragma unroll
+            for (int i = 0; i < DV; i += 2) __stcg(reinterpret_cast<float2*>(slot + r * D + lane * DV + i), make_float2(x[i], x[i + 1]));
+            if (lane == 0) {
+                __stcg(slot + R * D + r, mm);
+                __stcg(slot + R * D + R + r, l);
+            }
+        }
+    }
+    if (leaders == 0) return;  // the same in every warp
+
+    // ---- items over several blocks (this block's first, and its last): the last block to arrive joins all,
+    // in their order
+    const int ends[2] = {__ffs(leaders) - 1, 31 - __clz(leaders)};
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const Part p = sm.part[ends[k]];
+        any = any || p.from < block_from || p.to > block_to;
+    }
+    if (!any) return;
+    __threadfence();
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        if (k == 1 && ends[1] == ends[0]) break;
+        const Part p = sm.part[ends[k]];
+        if (p.from >= block_from && p.to <= block_to) continue;
         // (the block of unit f is floor(((f + 1) * blocks - 1) / total))
-        const int64_t ends = (((lane ? p.to - 1 : p.from) + 1) * blocks - 1) / total;
-        const int64_t c0 = __shfl_sync(0xFFFFFFFFu, ends, 0), c1 = __shfl_sync(0xFFFFFFFFu, ends, 1);
-        __threadfence();
-        __syncthreads();
+        const int64_t at = (((lane ? p.to - 1 : p.from) + 1) * blocks - 1) / total;
+        const int64_t c0 = __shfl_sync(0xFFFFFFFFu, at, 0), c1 = __shfl_sync(0xFFFFFFFFu, at, 1);
         if (tid == 0) sm.last = atomicInc(a.arrived + c0, static_cast<uint32_t>(c1 - c0)) == static_cast<uint32_t>(c1 - c0);
         __syncthreads();
         if (sm.last) {
@@ -771,48 +814,51 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             const int n = static_cast<int>(c1 - c0) + 1;
             const float* first = a.partial + (c0 * 2 + 1) * kSlot;  // the item starts in c0's second slot,
             auto slot_of = [&](int c) { return first + (c == 0 ? 0 : (2 * c - 1) * kSlot); };  // then the first ones
-            // a warp for each row: the blocks' weights, whose sum of sums is 1
             for (int r = warp; r < R; r += W) {
+                if (p.row0 + r >= p.rows) break;
                 float mc[kMaxBlocks / 32], lc[kMaxBlocks / 32];
-#pragma unroll
-                for (int k = 0; k < kMaxBlocks / 32; ++k) {
-                    const int c = lane + 32 * k;
-                    mc[k] = c < n ? __ldcg(slot_of(c) + R * D + r) : -INFINITY;
-                    lc[k] = c < n ? __ldcg(slot_of(c) + R * D + R + r) : 0.0f;
-                }
                 float mm = -INFINITY, l = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kMaxBlocks / 32; ++k) mm = fmaxf(mm, mc[k]);
+                for (int i = 0; i < kMaxBlocks / 32; ++i) {
+                    const int c = lane + 32 * i;
+                    mc[i] = c < n ? __ldcg(slot_of(c) + R * D + r) : -INFINITY;
+                    lc[i] = c < n ? __ldcg(slot_of(c) + R * D + R + r) : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < kMaxBlocks / 32; ++i) mm = fmaxf(mm, mc[i]);
 #pragma unroll
                 for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
 #pragma unroll
-                for (int k = 0; k < kMaxBlocks / 32; ++k) {
-                    mc[k] = mc[k] == -INFINITY ? (lc[k] != lc[k] ? 1.0f : 0.0f) : ex2(mc[k] - mm);
-                    l = fmaf(lc[k], mc[k], l);
+                for (int i = 0; i < kMaxBlocks / 32; ++i) {
+                    mc[i] = mc[i] == -INFINITY ? (lc[i] != lc[i] ? 1.0f : 0.0f) : ex2(mc[i] - mm);
+                    l = fmaf(lc[i], mc[i], l);
                 }
 #pragma unroll
                 for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
 #pragma unroll
-                for (int k = 0; k < kMaxBlocks / 32; ++k) {
-                    const int c = lane + 32 * k;
-                    if (c < n) sm.weight[c][r] = mc[k] / l;
+                for (int i = 0; i < kMaxBlocks / 32; ++i) {
+                    const int c = lane + 32 * i;
+                    if (c < n) sm.weight[c][r] = mc[i] / l;
                 }
             }
             __syncthreads();
-            for (int i = tid; i < R * D / 2; i += kThreads) {
-                const int r = i / (D / 2), d = (i % (D / 2)) * 2;
-                if (p.row0 + r >= p.rows) continue;
-                const float* q = first + r * D + d;
-                float2 v = __ldcg(reinterpret_cast<const float2*>(q));
-                float x0 = v.x * sm.weight[0][r], x1 = v.y * sm.weight[0][r];
-                q += kSlot;
+            for (int r = warp; r < R; r += W) {
+                if (p.row0 + r >= p.rows) break;
+                float x[DV];
+#pragma unroll
+                for (int i = 0; i < DV; ++i) x[i] = 0.0f;
 #pragma unroll 8
-                for (int c = 1; c < n; ++c, q += 2 * kSlot) {
-                    v = __ldcg(reinterpret_cast<const float2*>(q));
-                    x0 = fmaf(v.x, sm.weight[c][r], x0);
-                    x1 = fmaf(v.y, sm.weight[c][r], x1);
+                for (int c = 0; c < n; ++c) {
+                    const float f = sm.weight[c][r];
+                    const float* q = slot_of(c) + r * D + lane * DV;
+#pragma unroll
+                    for (int i = 0; i < DV; i += 2) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2*>(q + i));
+                        x[i] = fmaf(v.x, f, x[i]);
+                        x[i + 1] = fmaf(v.y, f, x[i + 1]);
+                    }
                 }
-                write_row(p, r, d, x0, x1);
+                write(p, r, x);
             }
         }
         __syncthreads();
