@@ -37,6 +37,7 @@ namespace {
 using namespace arcs;
 
 constexpr int kMaxBlocks = 256;  // blocks of a launch: at most one for each SM
+constexpr float kNothing = -3.0e38f;  // maximum of no score: finite, so that differences need no special case
 constexpr int kItemCost = 1;     // an item's fixed cost in steps (query load, output store), for the cut
 constexpr int kStatusBytes = kMaxBlocks * 4;
 
@@ -73,7 +74,7 @@ struct Shape<128, 2> {
 };
 template <>
 struct Shape<256, 1> {
-    static constexpr int kWarps = 6, kStages = 3;
+    static constexpr int kWarps = 8, kStages = 2;
 };
 
 struct Part {        // a partial's item
@@ -82,6 +83,7 @@ struct Part {        // a partial's item
     int32_t rows;      // query rows of its sequence and head (tokens * group)
     int32_t row0;      // first row of its tile
     int32_t head;
+    int32_t tokens;    // new tokens of the sequence
 };
 
 template <int D, int NT>
@@ -95,6 +97,7 @@ struct Smem {
     float scales[kW][kS][2];
     float m[2 * kW][kR], l[2 * kW][kR];
     Part part[2 * kW];
+    uint32_t run[32];  // partials of the same item, as a mask
     int64_t before[kThreads + 1];
     int64_t wsum[kW];
     uint32_t last;
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 for (int i = 0; i < KS; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.0f;
-                m[nt][0] = m[nt][1] = -INFINITY;
+                m[nt][0] = m[nt][1] = kNothing;
                 l[nt][0] = l[nt][1] = 0.0f;
             }
 
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float mn = fmaxf(m[nt][e], top[nt][e]);
-                            f[e] = m[nt][e] == -INFINITY ? 0.0f : ex2(m[nt][e] - mn);
+                            f[e] = ex2(m[nt][e] - mn);
                             m[nt][e] = mn;
                             l[nt][e] *= f[e];
                         }
@@ -562,8 +565,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float ref = m[nt][e & 1] == -INFINITY ? 0.0f : m[nt][e & 1];
-                        p[e] = ex2(s[nt][e] - ref);
+                        p[e] = ex2(s[nt][e] - m[nt][e & 1]);
                         l[nt][e & 1] = fmaf(p[e], vi, l[nt][e & 1]);
                     }
                     // token-major to row-major: what the products take
@@ -702,20 +704,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                         }
                     }
                 if (lane == 0)
-                    sm.part[slot] = Part{item_from, item_from + at.q.cost, at.q.first, rows, row0, at.head};
+                    sm.part[slot] = Part{item_from, item_from + at.q.cost, at.q.first, rows, row0, at.head, at.q.n};
             }
         }
         copies_wait<0>();
     }
     __syncthreads();
 
-    // ---- join the block's partials.  Those of one item are a run; a warp takes a row of a run, lane e
-    // holds partial e's maximum and sum.
+    // ---- join the block's partials.  Those of one item are a run; a warp takes a row of a run.
     static_assert(2 * W <= 32, "a lane for each partial");
     constexpr int DV = D / 32;                // values of a lane
     constexpr int kSlot = R * D + 2 * R;      // floats of a block's partial: output, maxima, sums
     auto write = [&](const Part& p, int r, const float (&x)[DV]) {
-        const int rr = p.row0 + r, tok = rr / a.group;
+        const int rr = p.row0 + r, tok = p.tokens == 1 ? 0 : rr / a.group;
         uint16_t* out = static_cast<uint16_t*>(a.q.out) + (p.first + tok) * a.q.out_token_stride +
                         (p.head * a.group + rr - tok * a.group) * a.q.out_head_stride + lane * DV;
         uint32_t w[DV / 2];
@@ -741,28 +742,42 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     const uint32_t run_of = __match_any_sync(0xFFFFFFFFu, my_from);
     const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, my_from >= 0 && lane == __ffs(run_of) - 1);
     const int runs = __popc(leaders);
+    if (warp == 0) sm.run[lane] = my_from >= 0 ? run_of : 0;
+    __syncthreads();
+    // a thread for each partial and row: its weight in its run, from the run's maximum
+    for (int i = tid; i < 2 * W * R; i += kThreads) {
+        const int e = i / R, r = i % R;
+        const uint32_t run = sm.run[e];
+        float mm = kNothing, l = 0.0f;
+        for (uint32_t left = run; left; left &= left - 1) mm = fmaxf(mm, sm.m[__ffs(left) - 1][r]);
+        for (uint32_t left = run; left; left &= left - 1) {
+            const int k = __ffs(left) - 1;
+            l = fmaf(sm.l[k][r], ex2(sm.m[k][r] - mm), l);
+        }
+        if (run) {
+            const Part& p = sm.part[e];
+            const bool whole = p.from >= block_from && p.to <= block_to;
+            const float f = ex2(sm.m[e][r] - mm);
+            sm.weight[e][r] = whole ? f / l : f;
+            if (!whole && e == __ffs(run) - 1 && p.row0 + r < p.rows) {
+                float* slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (p.from >= block_from ? 1 : 0)) * kSlot;
+                __stcg(slot + R * D + r, mm);
+                __stcg(slot + R * D + R + r, l);
+            }
+        }
+    }
+    __syncthreads();
     for (int task = warp; task < runs * R; task += W) {
         const int r = task % R;
         const int lead = __fns(leaders, 0, task / R + 1);
         const Part p = sm.part[lead];
         if (p.row0 + r >= p.rows) continue;
-        const uint32_t run_mask = __shfl_sync(0xFFFFFFFFu, run_of, lead);
-        const bool in = (run_mask >> lane) & 1;
-        const float me = in ? sm.m[lane][r] : -INFINITY, le = in ? sm.l[lane][r] : 0.0f;
-        float mm = me;
-#pragma unroll
-        for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
-        // a partial without a visible token counts nothing, but for a NaN
-        const float f = me == -INFINITY ? (le != le ? 1.0f : 0.0f) : ex2(me - mm);
-        float l = le * f;
-#pragma unroll
-        for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
         float x[DV];
 #pragma unroll
         for (int i = 0; i < DV; ++i) x[i] = 0.0f;
-        for (uint32_t left = run_mask; left; left &= left - 1) {
+        for (uint32_t left = sm.run[lead]; left; left &= left - 1) {
             const int e = __ffs(left) - 1;
-            const float fe = __shfl_sync(0xFFFFFFFFu, f, e);
+            const float fe = sm.weight[e][r];
             const float* v = reinterpret_cast<const float*>(dyn + (e >> 1) * S::kPerWarp + ((e & 1) ? 0 : S::kRing)) + r * D + lane * DV;
 #pragma unroll
             for (int i = 0; i < DV; i += 2) {
@@ -772,17 +787,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             }
         }
         if (p.from >= block_from && p.to <= block_to) {
-#pragma unroll
-            for (int i = 0; i < DV; ++i) x[i] /= l;
             write(p, r, x);
         } else {
             float* slot = a.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (p.from >= block_from ? 1 : 0)) * kSlot;
 #pragma unroll
             for (int i = 0; i < DV; i += 2) __stcg(reinterpret_cast<float2*>(slot + r * D + lane * DV + i), make_float2(x[i], x[i + 1]));
-            if (lane == 0) {
-                __stcg(slot + R * D + r, mm);
-                __stcg(slot + R * D + R + r, l);
-            }
         }
     }
     if (leaders == 0) return;  // the same in every warp
@@ -817,11 +826,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             for (int r = warp; r < R; r += W) {
                 if (p.row0 + r >= p.rows) break;
                 float mc[kMaxBlocks / 32], lc[kMaxBlocks / 32];
-                float mm = -INFINITY, l = 0.0f;
+                float mm = kNothing, l = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kMaxBlocks / 32; ++i) {
                     const int c = lane + 32 * i;
-                    mc[i] = c < n ? __ldcg(slot_of(c) + R * D + r) : -INFINITY;
+                    mc[i] = c < n ? __ldcg(slot_of(c) + R * D + r) : kNothing;
                     lc[i] = c < n ? __ldcg(slot_of(c) + R * D + R + r) : 0.0f;
                 }
 #pragma unroll
@@ -830,7 +839,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 for (int x = 16; x; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, x));
 #pragma unroll
                 for (int i = 0; i < kMaxBlocks / 32; ++i) {
-                    mc[i] = mc[i] == -INFINITY ? (lc[i] != lc[i] ? 1.0f : 0.0f) : ex2(mc[i] - mm);
+                    mc[i] = ex2(mc[i] - mm);
                     l = fmaf(lc[i], mc[i], l);
                 }
 #pragma unroll
