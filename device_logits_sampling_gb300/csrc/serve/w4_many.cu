@@ -41,23 +41,26 @@ constexpr int kInner = 128;    // inner values of a block of A and x
 constexpr int kRawStage = 32 * 128;  // bytes of a warp's raw stage: 32 rows of 256 codes
 constexpr int kWaits = 1 << 24;
 
-template <int N>
+// N: rows of x of a product (16, 32, 64 or 128). H: products that share A: 2
+// for more than 128 rows, so that weights are unpacked once for 256 of them.
+template <int N, int H>
 struct Many {
-    // 64 columns and more are added up by two groups of warps: one took 1,100 clocks for the 128 sums of a row,
-    // the products 512
+    // 64 columns and more are added up by two groups of warps, each half of the columns: one took 1,100 clocks
+    // for the 128 sums of a row, the products 512
     static constexpr int kAdders = N >= 64 ? 2 : 1;
     static constexpr int kThreads = (kAdders + 3) * 128;
-    static constexpr int kCols = N / kAdders;            // columns of a group of warps
-    // registers of a thread once the roles part, of 96 at the launch of 640: 128 + 128 + 88 + 88 + 40 <= 5 * 96
-    static constexpr int kAddRegs = 128, kUnpackRegs = 88, kIssueRegs = 40;
-    static constexpr int kSums = N == 128 ? 2 : 4;       // ring of group sums, N columns each
-    static constexpr int kA = 4;                         // ring of unpacked A, 64 columns each
-    static constexpr int kX = N == 128 ? 3 : 4;          // ring of x
-    static constexpr int kRaw = N == 128 ? 3 : 4;        // a warp's ring of raw weights
-    static constexpr int kColumns = 512; // tensor memory taken
-    static constexpr int kXBytes = N * kInner * 2;
+    static constexpr int kCols = N * H / kAdders;        // columns of a group of warps
+    // registers of a thread once the roles part, of 96 at the launch of 640 threads (5 * 96 = 480)
+    static constexpr int kAddRegs = H == 2 ? 160 : 128, kUnpackRegs = H == 2 ? 64 : 88, kIssueRegs = H == 2 ? 32 : 40;
+    static_assert(kAdders == 1 || 2 * kAddRegs + 2 * kUnpackRegs + kIssueRegs <= 480, "registers of the launch");
+    static constexpr int kSums = H == 2 ? 3 : N == 128 ? 2 : 4;  // ring of group sums, N columns each
+    static constexpr int kA = H == 2 ? 2 : 4;            // ring of unpacked A, 64 columns each
+    static constexpr int kX = H == 2 ? 2 : N == 128 ? 3 : 4;     // ring of x
+    static constexpr int kRaw = H == 2 ? 2 : N == 128 ? 3 : 4;   // a warp's ring of raw weights
+    static constexpr int kColumns = 512;                 // tensor memory taken
+    static constexpr int kXHalf = N * kInner * 2, kXBytes = H * kXHalf;
     static constexpr int kRawBytes = 8 * kRaw * kRawStage;
-    static constexpr int kJoin = N * 128 * 4;            // over the rings, at the end
+    static constexpr int kJoin = H * N * 128 * 4;        // over the rings, at the end
     static constexpr int kRings = kX * kXBytes + kRawBytes;
     static constexpr int kSmem = (kRings > kJoin ? kRings : kJoin) + 1024;
 };
@@ -122,11 +125,10 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint
         : "memory");
 }
 #define ARC_REGS8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&x)[32]) {
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&x)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-        ARC_REGS8(x, 0), ARC_REGS8(x, 8), ARC_REGS8(x, 16), ARC_REGS8(x, 24)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        ARC_REGS8(x, 0), ARC_REGS8(x, 8)
         : "memory");
 }
 #undef ARC_REGS8
@@ -201,10 +203,10 @@ __device__ __forceinline__ bool elect_one() {
 
 // The products of all items, by one thread: for each block of 128 inner values
 // its groups, each into the next slot of the ring of sums.
-template <int N, int G>
+template <int N, int H, int G>
 __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint32_t tmem, uint32_t tmem_a, int first, int step,
                                                int items, int nb) {
-    using M = Many<N>;
+    using M = Many<N, H>;
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
     constexpr int kSteps = G / 16;
     const uint64_t x0 = operand_at(x_ring);
@@ -220,14 +222,15 @@ __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint
             const uint64_t x_at = x0 + xs * (M::kXBytes / 16);
             const uint32_t a_at = tmem_a + buf * 64;
 #pragma unroll
-            for (int g = 0; g < kInner / G; ++g) {
+            for (int gh = 0; gh < kInner / G * H; ++gh) {
+                const int g = gh / H, h = gh % H;
                 if (!s_ready && !bar_wait(&bars.s_empty[slot], slot_phase, &bars.failed)) return;
                 fence_after();
                 const uint32_t d = tmem + slot * N;
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k) {
                     const int kk = g * kSteps + k;  // of the block's eight
-                    mma_f16(d, a_at + kk * 8, x_at + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc, k != 0);
+                    mma_f16(d, a_at + kk * 8, x_at + h * (M::kXHalf / 16) + (kk >> 2) * (N * 128 / 16) + (kk & 3) * 2, idesc, k != 0);
                 }
                 commit_to(&bars.s_full[slot]);
                 if (++slot == M::kSums) {
@@ -303,9 +306,9 @@ __global__ void __launch_bounds__(256) many_x_kernel(const __grid_constant__ Man
 }
 
 // ------------------------------------------------------------------ products
-template <int N>
-__global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid_constant__ ManyArgs a) {
-    using M = Many<N>;
+template <int N, int H>
+__global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __grid_constant__ ManyArgs a) {
+    using M = Many<N, H>;
     extern __shared__ uint8_t raw_smem[];
     __shared__ Bars bars;
     uint8_t* const dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x) % a.cluster;
     const int first = static_cast<int>(blockIdx.x) / a.cluster, step = static_cast<int>(gridDim.x) / a.cluster;
-    const int items = a.tiles * a.halves;
+    const int items = a.tiles;
     // blocks of the inner dimension that this block takes
     const int b0 = static_cast<int>(static_cast<int64_t>(a.blocks) * rank / a.cluster);
     const int nb = static_cast<int>(static_cast<int64_t>(a.blocks) * (rank + 1) / a.cluster) - b0;
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
             bar_init(&bars.x_full[i], 1);
             bar_init(&bars.x_empty[i], 1);
             bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.s_empty[i], 4 * M::kAdders);
+            bar_init(&bars.s_empty[i], H == 2 ? 4 : 4 * M::kAdders);
         }
         bars.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -346,32 +349,35 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
     const uint32_t tmem = bars.tmem, tmem_a = tmem + M::kSums * N;
 
     if (warp >= kUnpack && warp < kIssue) {
-        // ---- unpack: a thread for each weight row; the two groups take raw stages in turn
+        // ---- unpack: a thread for each weight row; the two groups take blocks in turn, counted over all items, so
+        // that neither waits for a buffer more than one use behind the other.  A raw stage holds two of a
+        // group's blocks: 64 bytes of each row, and 64 bytes 128 further on.
         if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::kUnpackRegs));
         const int w = warp & 3, turn = (warp - kUnpack) >> 2;
         const uint32_t ring = shared_of(raw_ring) + (warp - kUnpack) * M::kRaw * kRawStage;
         const uint8_t* const ring_p = raw_ring + (warp - kUnpack) * M::kRaw * kRawStage;
-        const int pairs = (nb + 1) / 2;  // raw stages of an item: two blocks each
-        int c_item = first, c_pair = turn, c_stage = 0;
+        const int end = (b0 + nb) * kInner < a.ins ? (b0 + nb) * kInner : a.ins;
+        int c_item = first, c_block = turn, c_stage = 0;  // the next raw stage's item and first block
         auto issue = [&]() {
-            while (c_pair >= pairs && c_item < items) {
-                c_pair -= pairs;
+            while (c_block >= nb && c_item < items) {  // the group's next block, of a later item
+                c_block -= nb;
+                c_block &= 1;
                 c_item += step;
             }
             if (c_item < items) {
-                const int64_t n0 = static_cast<int64_t>(c_item / a.halves) * 128 + w * 32;
-                const int k = (b0 + 2 * c_pair) * kInner;         // first inner value
-                const int end = (b0 + nb) * kInner < a.ins ? (b0 + nb) * kInner : a.ins;
+                const int64_t n0 = static_cast<int64_t>(c_item) * 128 + w * 32;
                 const int c = lane & 7;
-                const bool inner = k + c * 32 < end;
+                const int b = c_block + (c >> 2) * 2;
+                const int k = (b0 + b) * kInner + (c & 3) * 32;  // first inner value of the lane's chunk
+                const bool inner = b < nb && k < end;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 4 * i + (lane >> 3);
                     const bool on = inner && n0 + r < a.outs;
-                    const char* src = static_cast<const char*>(a.q) + (on ? (n0 + r) * a.row_bytes + k / 2 + c * 16 : 0);
+                    const char* src = static_cast<const char*>(a.q) + (on ? (n0 + r) * a.row_bytes + k / 2 : 0);
                     copy16(ring + c_stage * kRawStage + r * 128 + ((c ^ (r & 7)) * 16), src, on);
                 }
-                c_pair += 2;
+                c_block += 4;
             }
             copies_end();
             c_stage = c_stage + 1 == M::kRaw ? 0 : c_stage + 1;
@@ -379,10 +385,10 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
         for (int i = 0; i < M::kRaw - 1; ++i) issue();
         int stage = 0;
         uint32_t before = 0;  // blocks of the items before
-        int pair = turn;
         bool ok = true;
-        for (int item = first; ok && item < items; item += step, before += nb, pair -= pairs) {
-            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + w * 32 + lane;
+        for (int item = first; ok && item < items; item += step, before += nb) {
+            int block = (turn ^ before) & 1;
+            const int64_t n = static_cast<int64_t>(item) * 128 + w * 32 + lane;
             const uint8_t* zero_at = a.zeros && n < a.outs ? a.zeros + n * a.groups : nullptr;
             // the zero points of a block's groups, one a byte; loaded a raw stage ahead
             auto zeros_of = [&](int g) {
@@ -397,8 +403,8 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
             };
             uint32_t z_now[2], z_next[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) z_next[h] = zeros_of((b0 + 2 * pair + h) * per);
-            for (; ok && pair < pairs; pair += 2) {
+            for (int h = 0; h < 2; ++h) z_next[h] = zeros_of((b0 + block + 2 * h) * per);
+            for (; ok && block < nb; block += 4) {
                 copies_wait<M::kRaw - 2>();
                 __syncwarp();
                 issue();
@@ -407,11 +413,11 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     z_now[h] = z_next[h];
-                    z_next[h] = zeros_of((b0 + 2 * pair + 4 + h) * per);
+                    z_next[h] = zeros_of((b0 + block + 4 + 2 * h) * per);
                 }
 #pragma unroll 1
-                for (int h = 0; h < 2 && 2 * pair + h < nb; ++h) {
-                    const uint32_t used = before + 2 * pair + h;
+                for (int h = 0; h < 2 && block + 2 * h < nb; ++h) {
+                    const uint32_t used = before + block + 2 * h;
                     const int buf = used % M::kA;
                     uint4 q[4];
 #pragma unroll
@@ -421,24 +427,22 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
                     fence_after();
                     const uint32_t zs = h ? z_now[1] : z_now[0];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        uint32_t v[32];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int ci = 2 * s + c;  // chunk of 32 values within the block
+                    for (int ci = 0; ci < 4; ++ci) {  // chunks of 32 values
+                        uint32_t v[16];
+                        {
                             const uint32_t z = (zs >> (8 * (ci * per / 4))) & 0xFFu;
                             const uint32_t z_lo = z | (z << 16), z_hi = z_lo << 4;
                             const uint32_t ws[4] = {q[ci].x, q[ci].y, q[ci].z, q[ci].w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const uint32_t u = ws[i] >> 8;
-                                v[16 * c + 4 * i] = sub2(ws[i] & 0x000F000Fu, z_lo);
-                                v[16 * c + 4 * i + 1] = sub2(u & 0x000F000Fu, z_lo);
-                                v[16 * c + 4 * i + 2] = sub2(ws[i] & 0x00F000F0u, z_hi);
-                                v[16 * c + 4 * i + 3] = sub2(u & 0x00F000F0u, z_hi);
+                                v[4 * i] = sub2(ws[i] & 0x000F000Fu, z_lo);
+                                v[4 * i + 1] = sub2(u & 0x000F000Fu, z_lo);
+                                v[4 * i + 2] = sub2(ws[i] & 0x00F000F0u, z_hi);
+                                v[4 * i + 3] = sub2(u & 0x00F000F0u, z_hi);
                             }
                         }
-                        tmem_store32(tmem_a + (static_cast<uint32_t>(w * 32) << 16) + buf * 64 + s * 32, v);
+                        tmem_store16(tmem_a + (static_cast<uint32_t>(w * 32) << 16) + buf * 64 + ci * 16, v);
                     }
                     tmem_wait_store();
                     fence_before();
@@ -454,11 +458,11 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
         if (warp == kIssue && elect_one()) {
             // ---- products
             if (a.group == 128)
-                issue_products<N, 128>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
+                issue_products<N, H, 128>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
             else if (a.group == 64)
-                issue_products<N, 64>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
+                issue_products<N, H, 64>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
             else
-                issue_products<N, 32>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
+                issue_products<N, H, 32>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
         }
         if (warp == kIssue + 1 && elect_one()) {
             // ---- x
@@ -466,18 +470,20 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
             uint32_t used = 0;
             bool ok = true;
             for (int item = first; ok && item < items; item += step) {
-                const uint8_t* src = static_cast<const uint8_t*>(a.x_ready) +
-                                     (static_cast<size_t>(item % a.halves) * a.blocks + b0) * M::kXBytes;
+                const uint8_t* src = static_cast<const uint8_t*>(a.x_ready) + static_cast<size_t>(b0) * M::kXHalf;
                 for (int b = 0; b < nb; ++b, ++used) {
                     const int xs = used % M::kX;
                     ok = bar_wait(&bars.x_empty[xs], ((used / M::kX) & 1) ^ 1, &bars.failed);
                     if (!ok) break;
                     bar_expect(&bars.x_full[xs], M::kXBytes);
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            shared_of(x_ring) + xs * M::kXBytes),
-                        "l"(src + static_cast<size_t>(b) * M::kXBytes), "r"(M::kXBytes), "r"(shared_of(&bars.x_full[xs]))
-                        : "memory");
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                shared_of(x_ring) + xs * M::kXBytes + h * M::kXHalf),
+                            "l"(src + (static_cast<size_t>(h) * a.blocks + b) * M::kXHalf), "r"(M::kXHalf),
+                            "r"(shared_of(&bars.x_full[xs]))
+                            : "memory");
                 }
             }
             // a failed block still waits for its copies in flight before its memory goes away
@@ -494,12 +500,13 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
         // ---- group sums: a thread for each weight row
         if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(M::kAddRegs));
         constexpr int C = M::kCols;
-        const int c0 = (warp >> 2) * C, row = tid & 127;  // its columns, its weight row
+        const int who = warp >> 2, c0 = who * C, row = tid & 127;  // its columns, its weight row
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        uint32_t sums = 0;
+        // with two products the sums of each are a slot of their own, in turn
+        uint32_t sums = H == 2 ? who : 0;
         bool ok = true;
         for (int item = first; item < items; item += step) {
-            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + row;
+            const int64_t n = static_cast<int64_t>(item) * 128 + row;
             const uint16_t* scale_at = static_cast<const uint16_t*>(a.scales) + (n < a.outs ? n : 0) * a.groups;
             auto scales_of = [&](int g) {  // eight of them ahead
                 uint4 s = make_uint4(0u, 0u, 0u, 0u);
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
             };
             for (int i = 0; i < (gi & 7); ++i) shift();
             const int end = gi + nb * per;
-            for (; ok && gi < end; ++sums) {
+            for (; ok && gi < end; sums += H) {
                 const uint32_t bits = now.x & 0xFFFFu;
                 const float s = a.x_bf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half(bits));
                 shift();
@@ -543,28 +550,34 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
                 fence_after();
                 // past the last group the weights are copied as zeros and x is zero, whatever the scale
                 const float ss = gi - 1 < a.groups ? s : 0.0f;
-                const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * N + c0;
+                const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + slot * N + (H == 2 ? 0 : c0);
                 const uint64_t s2 = pack2(ss, ss);
-                uint32_t d[C];
-                if constexpr (C == 64)
-                    tmem_load64(at, d);
-                else if constexpr (C == 32)
-                    tmem_load32(at, d);
-                else
-                    tmem_load16(at, d);
-                tmem_wait_load();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&bars.s_empty[slot]);
+                constexpr int L = C == 128 ? 16 : C == 64 ? 32 : C;  // columns of a load: what the running sums leave registers for
 #pragma unroll
-                for (int i = 0; i < C / 2; ++i)
-                    y[i] = fma2(s2, pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), y[i]);
+                for (int c = 0; c < C; c += L) {
+                    uint32_t d[L];
+                    if constexpr (L == 64)
+                        tmem_load64(at + c, d);
+                    else if constexpr (L == 32)
+                        tmem_load32(at + c, d);
+                    else
+                        tmem_load16(at + c, d);
+                    tmem_wait_load();
+                    if (c + L == C) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&bars.s_empty[slot]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < L / 2; ++i)
+                        y[c / 2 + i] = fma2(s2, pack2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), y[c / 2 + i]);
+                }
             }
             if (!ok) {
 #pragma unroll
                 for (int i = 0; i < C / 2; ++i) y[i] = 0x7FC000007FC00000ull;
             }
-            const int m0 = (item % a.halves) * N + c0;
+            const int m0 = c0;
             if (a.cluster == 1) {
                 if (n < a.outs) {
 #pragma unroll
@@ -595,10 +608,9 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
         // one item a cluster: each block adds up its share of the rows of x
         cluster_sync_all();
         const int item = first;
-        const int m0 = (item % a.halves) * N;
-        for (int i = rank * N * 128 / a.cluster + tid; i < (rank + 1) * N * 128 / a.cluster; i += M::kThreads) {
-            const int m = m0 + i / 128;
-            const int64_t n = static_cast<int64_t>(item / a.halves) * 128 + i % 128;
+        for (int i = rank * H * N * 128 / a.cluster + tid; i < (rank + 1) * H * N * 128 / a.cluster; i += M::kThreads) {
+            const int m = i / 128;
+            const int64_t n = static_cast<int64_t>(item) * 128 + i % 128;
             if (m >= a.rows || n >= a.outs) continue;
             float v = 0.0f;
             for (int c = 0; c < a.cluster; ++c) {
@@ -624,25 +636,25 @@ __global__ void __launch_bounds__(Many<N>::kThreads, 1) many_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(M::kColumns) : "memory");
 }
 
-template <int N>
+template <int N, int H>
 int launch(const ManyArgs& a, int dev, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    static_assert(Many<N>::kSmem + sizeof(Bars) <= arc::kSmemPerBlock, "shared memory");
-    static_assert(Many<N>::kSums * N + Many<N>::kA * 64 <= Many<N>::kColumns, "tensor memory");
-    if (arc::prepare(many_kernel<N>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
+    static_assert(Many<N, H>::kSmem + sizeof(Bars) <= arc::kSmemPerBlock, "shared memory");
+    static_assert(Many<N, H>::kSums * N + Many<N, H>::kA * 64 <= Many<N, H>::kColumns, "tensor memory");
+    if (arc::prepare(many_kernel<N, H>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
     const unsigned rows = static_cast<unsigned>(a.halves * a.columns);
     if (a.x_bf16)
         many_x_kernel<ARC_BF16><<<rows, 256, 0, st>>>(a);
     else
         many_x_kernel<ARC_F16><<<rows, 256, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return ARC_E_CUDA;
-    const int items = a.tiles * a.halves;
+    const int items = a.tiles;
     const int64_t grid = a.cluster > 1 ? int64_t{items} * a.cluster : (items < sms ? items : sms);
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(Many<N>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Many<N>::kSmem;
+    cfg.blockDim = dim3(Many<N, H>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Many<N, H>::kSmem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -653,7 +665,7 @@ int launch(const ManyArgs& a, int dev, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, many_kernel<N>, a) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, many_kernel<N, H>, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return ARC_E_CUDA;
     }
@@ -683,11 +695,11 @@ int launch_many(ManyArgs a, void* workspace, int dev, int sms, cudaStream_t st) 
     a.s_vec = reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 && a.groups % 8 == 0;
     // few tiles: split the inner dimension while every block keeps four blocks of it and all run at once
     a.cluster = 1;
-    while (a.cluster < 8 && int64_t{a.tiles} * a.halves * a.cluster * 2 <= sms && a.blocks >= a.cluster * 8) a.cluster *= 2;
-    if (a.columns == 16) return launch<16>(a, dev, sms, st);
-    if (a.columns == 32) return launch<32>(a, dev, sms, st);
-    if (a.columns == 64) return launch<64>(a, dev, sms, st);
-    return launch<128>(a, dev, sms, st);
+    while (a.cluster < 8 && int64_t{a.tiles} * a.cluster * 2 <= sms && a.blocks >= a.cluster * 8) a.cluster *= 2;
+    if (a.columns == 16) return launch<16, 1>(a, dev, sms, st);
+    if (a.columns == 32) return launch<32, 1>(a, dev, sms, st);
+    if (a.columns == 64) return launch<64, 1>(a, dev, sms, st);
+    return a.halves == 1 ? launch<128, 1>(a, dev, sms, st) : launch<128, 2>(a, dev, sms, st);
 }
 
 }  // namespace arcs
