@@ -71,6 +71,7 @@ struct Bars {
     uint64_t s_full[4], s_empty[4];
     uint32_t tmem;
     uint32_t failed;
+    float back[256];  // each row of x's factor
 };
 
 __device__ __forceinline__ uint32_t shared_of(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -199,6 +200,35 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+template <class T>
+__device__ __forceinline__ T as_output(float v);
+template <>
+__device__ __forceinline__ float as_output<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 as_output<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half as_output<__half>(float v) { return __float2half_rn(v); }
+
+// A weight row's sums for C rows of x: 32 rows of a warp are neighbours in y.
+template <class T, int C>
+__device__ __forceinline__ void store_sums(const ManyArgs& a, const float* back, const uint64_t (&y)[C / 2], int m0, int64_t n) {
+    T* out = static_cast<T*>(a.y) + m0 * a.y_stride + n;
+    const int left = a.rows - m0;
+    if (left >= C) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            *out = as_output<T>(half_of(y[i / 2], i & 1) * 0x1p24f * back[m0 + i]);
+            out += a.y_stride;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if (i < left) *out = as_output<T>(half_of(y[i / 2], i & 1) * 0x1p24f * back[m0 + i]);
+            out += a.y_stride;
+        }
+    }
 }
 
 // The products of all items, by one thread: for each block of 128 inner values
@@ -357,6 +387,8 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
         const uint32_t ring = shared_of(raw_ring) + (warp - kUnpack) * M::kRaw * kRawStage;
         const uint8_t* const ring_p = raw_ring + (warp - kUnpack) * M::kRaw * kRawStage;
         const int end = (b0 + nb) * kInner < a.ins ? (b0 + nb) * kInner : a.ins;
+        const int cc = lane & 7;  // the lane's chunk, of the rows lane / 8, + 4, ...
+        const uint32_t copy_to = ring + (lane >> 3) * 128 + ((cc ^ (lane >> 3)) * 16);
         int c_item = first, c_block = turn, c_stage = 0;  // the next raw stage's item and first block
         auto issue = [&]() {
             while (c_block >= nb && c_item < items) {  // the group's next block, of a later item
@@ -365,17 +397,19 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
                 c_item += step;
             }
             if (c_item < items) {
-                const int64_t n0 = static_cast<int64_t>(c_item) * 128 + w * 32;
-                const int c = lane & 7;
-                const int b = c_block + (c >> 2) * 2;
-                const int k = (b0 + b) * kInner + (c & 3) * 32;  // first inner value of the lane's chunk
+                const int64_t n0 = static_cast<int64_t>(c_item) * 128 + w * 32 + (lane >> 3);
+                const int b = c_block + (cc >> 2) * 2;
+                const int k = (b0 + b) * kInner + (cc & 3) * 32;  // first inner value of the lane's chunk
                 const bool inner = b < nb && k < end;
+                const char* src = static_cast<const char*>(a.q) + n0 * a.row_bytes + k / 2;
+                const uint32_t to = copy_to + c_stage * kRawStage;
+                const bool whole = inner && n0 + 28 < a.outs;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3);
-                    const bool on = inner && n0 + r < a.outs;
-                    const char* src = static_cast<const char*>(a.q) + (on ? (n0 + r) * a.row_bytes + k / 2 : 0);
-                    copy16(ring + c_stage * kRawStage + r * 128 + ((c ^ (r & 7)) * 16), src, on);
+                    // (a row four further on changes the third bit of its permutation)
+                    const bool on = whole || (inner && n0 + 4 * i < a.outs);
+                    copy16((to ^ ((i & 1) * 64)) + i * 512, on ? src : static_cast<const char*>(a.q), on);
+                    src += 4 * a.row_bytes;
                 }
                 c_block += 4;
             }
@@ -503,6 +537,8 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
         const int who = warp >> 2, c0 = who * C, row = tid & 127;  // its columns, its weight row
         asm volatile("griddepcontrol.wait;" ::: "memory");
         // with two products the sums of each are a slot of their own, in turn
+        for (int i = tid; i < H * N; i += M::kAdders * 128) bars.back[i] = a.x_back[i];
+        asm volatile("bar.sync 1, %0;" ::"n"(M::kAdders * 128) : "memory");
         uint32_t sums = H == 2 ? who : 0;
         bool ok = true;
         for (int item = first; item < items; item += step) {
@@ -580,20 +616,12 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
             const int m0 = c0;
             if (a.cluster == 1) {
                 if (n < a.outs) {
-#pragma unroll
-                    for (int i = 0; i < C; ++i) {
-                        const int m = m0 + i;
-                        if (m < a.rows) {
-                            const float v = half_of(y[i / 2], i & 1) * 0x1p24f * __ldg(a.x_back + m);
-                            const int64_t o = m * a.y_stride + n;
-                            if (a.y_f32)
-                                static_cast<float*>(a.y)[o] = v;
-                            else if (a.x_bf16)
-                                static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(v);
-                            else
-                                static_cast<__half*>(a.y)[o] = __float2half_rn(v);
-                        }
-                    }
+                    if (a.y_f32)
+                        store_sums<float, C>(a, bars.back, y, m0, n);
+                    else if (a.x_bf16)
+                        store_sums<__nv_bfloat16, C>(a, bars.back, y, m0, n);
+                    else
+                        store_sums<__half, C>(a, bars.back, y, m0, n);
                 }
             } else {
                 // every copy and product of this block is done: the rings give way to the block's sums
@@ -620,7 +648,7 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
                 asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(remote));
                 v += p;
             }
-            v = v * 0x1p24f * __ldg(a.x_back + m);
+            v = v * 0x1p24f * bars.back[m];
             const int64_t o = m * a.y_stride + n;
             if (a.y_f32)
                 static_cast<float*>(a.y)[o] = v;
