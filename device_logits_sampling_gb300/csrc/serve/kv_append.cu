@@ -5,11 +5,13 @@
 // 64 bits of the product are the exact fraction of a turn, so a far position
 // costs no accuracy.  The fraction is split into quarter turns and a rest of
 // at most an eighth to either side, whose sine and cosine are fp32 Taylor sums:
-// a rotated value is off by less than 2^-21 (|a| + |b|) times the amplitude.
+// a rotated value is off by less than 3.4e-7 (|a| + |b|) times the amplitude
+// (the angle's two roundings 1.2e-7, the sums' 4e-8, the amplitude's, the
+// product's and the difference's 6e-8 each).
 //
 // Rounding.  The stored code is the nearest one to the exact rotated value:
 // where the two ends of that error interval round to different codes (about
-// one value in 10^5) the value is recomputed in fp64.  The same holds for the
+// one value in 10^5) the value is recomputed in fp64, with Taylor sums too.  The same holds for the
 // page's largest magnitude, where the interval's ends give different scales.
 #include <cstring>
 
@@ -21,7 +23,9 @@ namespace {
 using namespace arcs;
 
 constexpr int kThreads = 256;
-constexpr float kRotErr = 4.8e-7f;  // 2^-21
+constexpr float kRotErr = 3.4e-7f;
+// |a| + |b| is at most sqrt(2) of the pair's length, and that at most the sum of the turned pair's magnitudes
+constexpr float kTurnedErr = 1.42f * kRotErr;
 constexpr int kKept = 2;            // row passes of a page job whose rows stay in registers
 
 struct AppendArgs {
@@ -60,10 +64,32 @@ __device__ __forceinline__ float2 turn32(uint64_t phase) {
     return make_float2(((quarter + 1) & 2) ? -a : a, (quarter & 2) ? -b : b);
 }
 
+// a c - b s in fp64: Taylor sums up to the first term below 2^-53.
 __device__ __noinline__ double turn64(uint64_t phase, float a, float b, float amp) {
-    double s, c;
-    sincospi(static_cast<double>(static_cast<int64_t>(phase)) * 0x1p-63, &s, &c);
-    return static_cast<double>(amp) * (static_cast<double>(a) * c - static_cast<double>(b) * s);
+    const uint32_t quarter = static_cast<uint32_t>((phase + (uint64_t{1} << 61)) >> 62);
+    const int64_t rest = static_cast<int64_t>(phase - (static_cast<uint64_t>(quarter) << 62));
+    const double x = static_cast<double>(rest) * 3.40612158008655459e-19;  // 2 pi / 2^64
+    const double q = x * x;
+    double s = -1.0 / 1307674368000.0;  // 15!
+    s = fma(q, s, 1.0 / 6227020800.0);
+    s = fma(q, s, -1.0 / 39916800.0);
+    s = fma(q, s, 1.0 / 362880.0);
+    s = fma(q, s, -1.0 / 5040.0);
+    s = fma(q, s, 1.0 / 120.0);
+    s = fma(q, s, -1.0 / 6.0);
+    s = fma(x * q, s, x);
+    double c = 1.0 / 20922789888000.0;  // 16!
+    c = fma(q, c, -1.0 / 87178291200.0);
+    c = fma(q, c, 1.0 / 479001600.0);
+    c = fma(q, c, -1.0 / 3628800.0);
+    c = fma(q, c, 1.0 / 40320.0);
+    c = fma(q, c, -1.0 / 720.0);
+    c = fma(q, c, 1.0 / 24.0);
+    c = fma(q, c, -0.5);
+    c = fma(q, c, 1.0);
+    const double u = (quarter & 1) ? s : c, w = (quarter & 1) ? c : s;
+    const double cs = ((quarter + 1) & 2) ? -u : u, sn = (quarter & 2) ? -w : w;
+    return static_cast<double>(amp) * (static_cast<double>(a) * cs - static_cast<double>(b) * sn);
 }
 
 // Round a double to e4m3 once: to odd in fp32 first (fp32 keeps more than two
@@ -156,7 +182,7 @@ __device__ __forceinline__ void unpack16(const Raw& r, float (&x)[16]) {
     }
 }
 
-// Turn them; returns the error bound of the turned values (0: exact).
+// Turn them; for kOdd returns the error bound of the turned values (elsewhere the pair itself gives it later).
 template <int DT, int TURN>
 __device__ __forceinline__ float turn16(const AppendArgs& a, const Place& p, const Turns& t, const char* head, int64_t pos,
                                         float (&x)[16]) {
@@ -182,7 +208,6 @@ __device__ __forceinline__ float turn16(const AppendArgs& a, const Place& p, con
             float& u = x[TURN == kHalves ? i : 2 * i];
             float& w = x[TURN == kHalves ? 8 + i : 2 * i + 1];
             if (TURN == kHalves || i < pairs) {
-                most = fmaxf(most, fabsf(u) + fabsf(w));
                 const float y = fmaf(u, t.c[i], -(w * t.s[i]));
                 w = fmaf(w, t.c[i], u * t.s[i]);
                 u = y;
@@ -287,9 +312,18 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a) {
 // Sixteen turned values of a key, or sixteen values.
 struct Sixteen {
     float y[16];
-    float err;  // their error bound; 0: exact
+    float err;  // kOdd: their error bound
     float top;  // their largest magnitude
 };
+
+// Bounds of the largest magnitude's exact value (EXACT: the value is exact).
+template <int TURN, bool EXACT>
+__device__ __forceinline__ void bounds(const Place& p, const Sixteen& v, float& lo, float& hi) {
+    // two values of a pair are at most the largest one each
+    const float err = EXACT || !p.turns ? 0.0f : TURN == kOdd ? v.err : v.top * (2.0f * kTurnedErr);
+    lo = fmaxf(lo, v.top - err);
+    hi = fmaxf(hi, v.top + err);
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -325,10 +359,12 @@ __device__ __noinline__ double exact_value(const AppendArgs& a, const char* head
 }
 
 // Store the codes of the place's values under the scale 2^e in the row at `out`.
-template <int DT, bool EXACT>
+template <int DT, int TURN, bool EXACT>
 __device__ __forceinline__ void put16(const AppendArgs& a, const Place& p, const char* head, int64_t pos, const Sixteen& v,
                                       int e, char* out) {
-    const float inv = exp2i(-e), slack = v.err * inv;
+    const float inv = exp2i(-e);
+    // values that do not turn are exact, and often lie on a tie: no slack for them
+    const float rel = p.turns ? kTurnedErr * inv : 0.0f;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t lo[2], hi[2];
@@ -338,10 +374,17 @@ __device__ __forceinline__ void put16(const AppendArgs& a, const Place& p, const
             if (EXACT) {
                 lo[w] = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
             } else {
-                lo[w] = e4m3x2(fmaf(y[0], inv, -slack), fmaf(y[1], inv, -slack)) |
-                        (e4m3x2(fmaf(y[2], inv, -slack), fmaf(y[3], inv, -slack)) << 16);
-                hi[w] = e4m3x2(fmaf(y[0], inv, slack), fmaf(y[1], inv, slack)) |
-                        (e4m3x2(fmaf(y[2], inv, slack), fmaf(y[3], inv, slack)) << 16);
+                float l[4], h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // the other value of the pair
+                    const float z = TURN == kHalves ? v.y[8 * (half ^ 1) + 4 * w + i] : y[i ^ 1];
+                    const float slack = TURN == kOdd ? v.err * inv : (fabsf(y[i]) + fabsf(z)) * rel;
+                    l[i] = fmaf(y[i], inv, -slack);
+                    h[i] = fmaf(y[i], inv, slack);
+                }
+                lo[w] = e4m3x2(l[0], l[1]) | (e4m3x2(l[2], l[3]) << 16);
+                hi[w] = e4m3x2(h[0], h[1]) | (e4m3x2(h[2], h[3]) << 16);
             }
         }
         if (!EXACT && (lo[0] != hi[0] || lo[1] != hi[1])) {
@@ -374,6 +417,14 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float f) {
         out |= e4m3x2(x.x * f, x.y * f) << (16 * i);
     }
     return out;
+}
+
+// Whether value i can be the largest one, of which `lo` is a lower bound.
+__device__ __forceinline__ bool may_be_largest(const Sixteen& v, int i, float lo) {
+    float y = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) y = k == i ? fabsf(v.y[k]) : y;
+    return !(y + v.err < lo * (1.0f - 4.0f * kTurnedErr));
 }
 
 // Scale exponent of a page that keeps older tokens (`held`): what is stored is
@@ -432,7 +483,11 @@ __device__ __forceinline__ void store_single(const AppendArgs& a) {
         }
         if (finish16(v)) err |= ARC_KV_ERR_NAN;
     }
-    float lo = fmaxf(v.top - v.err, 0.0f), hi = v.top + v.err;
+    float lo = 0.0f, hi = 0.0f;
+    if (is_v)
+        bounds<TURN, true>(p, v, lo, hi);
+    else
+        bounds<TURN, false>(p, v, lo, hi);
     for (int m = L >> 1; m; m >>= 1) {
         lo = fmaxf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m));
         hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m));
@@ -442,7 +497,12 @@ __device__ __forceinline__ void store_single(const AppendArgs& a) {
     if (__any_sync(0xFFFFFFFFu, unsure)) {
         double y = 0.0;
         if (unsure)
-            for (int i = 0; i < 16; ++i) y = fmax(y, fabs(exact_value<DT>(a, head, pos, p.d[i >> 3] + (i & 7))));
+            // (only values that can be the largest one)
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                const int d = p.d[i >> 3] + (i & 7);
+                if (may_be_largest(v, i, lo)) y = fmax(y, fabs(exact_value<DT>(a, head, pos, d)));
+            }
         for (int m = L >> 1; m; m >>= 1) y = fmax(y, __shfl_xor_sync(0xFFFFFFFFu, y, m));
         // rounding up cannot pass a border from below: 448 * 2^e is an fp32 value
         if (unsure) e = scale_exponent(__double2float_ru(y));
@@ -466,9 +526,9 @@ __device__ __forceinline__ void store_single(const AppendArgs& a) {
         }
         base += static_cast<int64_t>(slot) * a.c.head_dim;
         if (is_v)
-            put16<DT, true>(a, p, head, pos, v, e, base);
+            put16<DT, TURN, true>(a, p, head, pos, v, e, base);
         else
-            put16<DT, false>(a, p, head, pos, v, e, base);
+            put16<DT, TURN, false>(a, p, head, pos, v, e, base);
         if (j == 0) *scale = exp2i(e);
     }
     if (err && a.err) atomicOr(a.err, err);
@@ -589,16 +649,14 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
 #pragma unroll
         for (int k = 0; k < kKept; ++k) {
             fetch(k * per + my, ahead[k], turns[k], kept[k]);
-            lo = fmaxf(lo, kept[k].top - kept[k].err);
-            hi = fmaxf(hi, kept[k].top + kept[k].err);
+            bounds<TURN, V>(p, kept[k], lo, hi);
         }
         for (int k = kKept; k < passes; ++k) {
             Sixteen v;
             Turns t;
             if (!V && k * per + my < rows) turns_of<TURN>(a, p, page0 + slot0 + k * per + my, t);
             fetch(k * per + my, again(k), t, v);
-            lo = fmaxf(lo, v.top - v.err);
-            hi = fmaxf(hi, v.top + v.err);
+            bounds<TURN, V>(p, v, lo, hi);
         }
         if (h + 1 < h1) look(h + 1);
         // magnitudes are not negative: their bits order as they do
@@ -649,7 +707,7 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
         }
         auto put = [&](int r, const Sixteen& v) {
             if (r < rows)
-                put16<DT, V>(a, p, src + r * ts * 2, page0 + slot0 + r, v, e,
+                put16<DT, TURN, V>(a, p, src + r * ts * 2, page0 + slot0 + r, v, e,
                              base + static_cast<int64_t>(slot0 + r) * a.c.head_dim);
         };
 #pragma unroll
