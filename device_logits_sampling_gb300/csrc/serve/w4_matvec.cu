@@ -117,15 +117,22 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
     const int rows = f.a.rows, units = ks >> 3, groups = ks / G, all = units * rows;
     uint32_t* top = reinterpret_cast<uint32_t*>(dyn + f.up_off);  // then the rows' factors
     uint4 raw[kXVecs];
-    int row[kXVecs];
+    int row[kXVecs], unit[kXVecs];  // the vectors tid, tid + 512, ..., without a division each
+    {
+        const int rows_on = kFewThreads / units, units_on = kFewThreads - rows_on * units;
+        int m = tid / units, u = tid - m * units;
 #pragma unroll
-    for (int j = 0; j < kXVecs; ++j) {
-        const int i = j * kFewThreads + tid;
-        raw[j] = make_uint4(0u, 0u, 0u, 0u);
-        row[j] = 0;
-        if (i < all) {
-            row[j] = i / units;
-            raw[j] = raw8(static_cast<const char*>(f.a.x) + (row[j] * f.a.x_stride + k0 + (i - row[j] * units) * 8) * 2, f.x_vec);
+        for (int j = 0; j < kXVecs; ++j) {
+            row[j] = m;
+            unit[j] = u;
+            raw[j] = m < rows ? raw8(static_cast<const char*>(f.a.x) + (m * f.a.x_stride + k0 + u * 8) * 2, f.x_vec)
+                              : make_uint4(0u, 0u, 0u, 0u);
+            m += rows_on;
+            u += units_on;
+            if (u >= units) {
+                u -= units;
+                ++m;
+            }
         }
     }
     if (tid < 8 * NT) top[tid] = 0;
@@ -143,24 +150,23 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
 #pragma unroll
     for (int j = 0; j < kXVecs; ++j) {
         if (j * kFewThreads >= all) break;
-        unpack(raw[j]);
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float z = fabsf(v[i]);
-            if (z <= 3.4028235e38f) most = fmaxf(most, z);  // the largest finite one
-        }
+        // magnitudes of 16-bit floats order as their bits do; a row with an infinite or NaN value comes out as
+        // such whatever its factor
+        const uint4 r = raw[j];
+        const uint32_t w = __vmaxu2(__vmaxu2(r.x & 0x7FFF7FFFu, r.y & 0x7FFF7FFFu), __vmaxu2(r.z & 0x7FFF7FFFu, r.w & 0x7FFF7FFFu));
+        const uint32_t most = max(w & 0xFFFFu, w >> 16);
         if ((units & 31) == 0) {  // a warp's vectors are of one row
-            const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most));
-            if ((tid & 31) == 0) atomicMax(top + row[j], w);
-        } else {
-            atomicMax(top + row[j], __float_as_uint(most));
+            const uint32_t largest = __reduce_max_sync(0xFFFFFFFFu, most);
+            if ((tid & 31) == 0 && row[j] < rows) atomicMax(top + row[j], largest);
+        } else if (row[j] < rows) {
+            atomicMax(top + row[j], most);
         }
     }
     __syncthreads();
     if (tid < 8 * NT) {
-        const int ex = static_cast<int>(top[tid] >> 23) - 127;
-        const int e = top[tid] == 0 ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
+        const float largest = Half<DT>::unpack(top[tid]).x;
+        const int ex = static_cast<int>(__float_as_uint(largest) >> 23) - 127;
+        const int e = largest == 0.0f ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
         reinterpret_cast<float*>(top)[tid] = exp2i(e);
     }
     __syncthreads();
@@ -172,11 +178,10 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
     for (int j = 0; j < kXVecs; ++j) {
         if (j * kFewThreads >= all) break;
         // vectors of a group are neighbouring lanes: units is a multiple of G / 8
-        const int i = j * kFewThreads + tid;
-        const bool on = i < all;
-        const int m = row[j], u = i - m * units, k = on ? u * 8 : 0;
+        const int m = row[j], u = unit[j], k = u * 8;
+        const bool on = m < rows;
         unpack(raw[j]);
-        const float s = up[m];
+        const float s = on ? up[m] : 0.0f;
         float sum = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
