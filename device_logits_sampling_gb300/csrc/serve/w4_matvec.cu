@@ -450,12 +450,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
 }
 
 template <int G, int NT, int P, bool Z>
-int start_few(const FewArgs& f, int64_t grid, int smem, int dev, cudaStream_t st) {
+int start_few(const FewArgs& f, int smem, int dev, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     if (arc::prepare(few_kernel<G, NT, P, Z>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
     cfg.blockDim = dim3(kFewThreads, 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
@@ -466,6 +465,24 @@ int start_few(const FewArgs& f, int64_t grid, int smem, int dev, cudaStream_t st
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = f.cluster > 1 ? 1 : 0;
+    // As many clusters as run at once, found out once for each size: a cluster's blocks share a part of the GPU
+    // whose SMs they need not divide evenly, and the 38 clusters of four that 152 SMs would hold took two rounds
+    // (16,384 x 16,384: 60 us)
+    static std::atomic<int> at_once[64][9];
+    int clusters = sms;
+    if (f.cluster > 1) {
+        std::atomic<int>& known = at_once[dev & 63][f.cluster];
+        clusters = known.load(std::memory_order_relaxed);
+        if (clusters == 0) {
+            cfg.gridDim = dim3(static_cast<unsigned>(f.cluster), 1, 1);
+            if (cudaOccupancyMaxActiveClusters(&clusters, few_kernel<G, NT, P, Z>, &cfg) != cudaSuccess || clusters < 1) {
+                (void)cudaGetLastError();
+                clusters = sms / f.cluster;
+            }
+            known.store(clusters, std::memory_order_relaxed);
+        }
+    }
+    cfg.gridDim = dim3(static_cast<unsigned>((clusters < f.tiles ? clusters : f.tiles) * f.cluster), 1, 1);
     if (cudaLaunchKernelEx(&cfg, few_kernel<G, NT, P, Z>, f) != cudaSuccess) {
         (void)cudaGetLastError();
         return ARC_E_CUDA;
@@ -528,12 +545,9 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
     parts = best;
     f.tiles = static_cast<int32_t>(tiles_of(parts));
     f.x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
-    int64_t grid = sms / f.cluster;
-    if (grid > f.tiles) grid = f.tiles;
-    grid *= f.cluster;
     if (f.part > 256)
-        return a.w.zeros ? start_few<G, NT, 512, true>(f, grid, off, dev, st) : start_few<G, NT, 512, false>(f, grid, off, dev, st);
-    return a.w.zeros ? start_few<G, NT, 256, true>(f, grid, off, dev, st) : start_few<G, NT, 256, false>(f, grid, off, dev, st);
+        return a.w.zeros ? start_few<G, NT, 512, true>(f, off, dev, sms, st) : start_few<G, NT, 512, false>(f, off, dev, sms, st);
+    return a.w.zeros ? start_few<G, NT, 256, true>(f, off, dev, sms, st) : start_few<G, NT, 256, false>(f, off, dev, sms, st);
 }
 
 template <int NT>
