@@ -18,8 +18,8 @@
 // number a thread and the running sums are the thread's registers.
 //
 // Roles of a block: one or two groups of four warps add up group sums (and store
-// the output), each its share of the columns; two groups of four copy and unpack
-// weights, taking turns; a warp issues the products and one copies x.  They meet at barriers in shared memory: rings of unpacked A, of x and of group
+// the output), each its share of the columns; two or four groups of four copy and
+// unpack weights, taking turns; a warp issues the products and one copies x.  They meet at barriers in shared memory: rings of unpacked A, of x and of group
 // sums, so that copying, unpacking, multiplying and adding up overlap across
 // groups and tiles.  Few tiles: the inner dimension is split over a cluster
 // whose blocks add each other's sums through distributed shared memory.
@@ -48,7 +48,9 @@ struct Many {
     // 64 columns and more are added up by two groups of warps, each half of the columns: one took 1,100 clocks
     // for the 128 sums of a row, the products 512
     static constexpr int kAdders = N >= 64 ? 2 : 1;
-    static constexpr int kThreads = (kAdders + 3) * 128;
+    // few columns: unpacking is what a block waits for, so four groups of warps do it
+    static constexpr int kUnpackers = N <= 32 ? 4 : 2;
+    static constexpr int kThreads = (kAdders + kUnpackers + 1) * 128;
     static constexpr int kCols = N * H / kAdders;        // columns of a group of warps
     // registers of a thread once the roles part, of 96 at the launch of 640 threads (5 * 96 = 480)
     static constexpr int kAddRegs = H == 2 ? 160 : 128, kUnpackRegs = H == 2 ? 64 : 88, kIssueRegs = H == 2 ? 32 : 40;
@@ -56,10 +58,10 @@ struct Many {
     static constexpr int kSums = H == 2 ? 3 : N == 128 ? 2 : 4;  // ring of group sums, N columns each
     static constexpr int kA = H == 2 ? 2 : 4;            // ring of unpacked A, 64 columns each
     static constexpr int kX = H == 2 ? 2 : N == 128 ? 3 : 4;     // ring of x
-    static constexpr int kRaw = H == 2 ? 2 : N == 128 ? 3 : 4;   // a warp's ring of raw weights
+    static constexpr int kRaw = H == 2 ? 2 : N == 128 || N <= 32 ? 3 : 4;  // a warp's ring of raw weights
     static constexpr int kColumns = 512;                 // tensor memory taken
     static constexpr int kXHalf = N * kInner * 2, kXBytes = H * kXHalf;
-    static constexpr int kRawBytes = 8 * kRaw * kRawStage;
+    static constexpr int kRawBytes = 4 * kUnpackers * kRaw * kRawStage;
     static constexpr int kJoin = H * N * 128 * 4;        // over the rings, at the end
     static constexpr int kRings = kX * kXBytes + kRawBytes;
     static constexpr int kSmem = (kRings > kJoin ? kRings : kJoin) + 1024;
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
     extern __shared__ uint8_t raw_smem[];
     __shared__ Bars bars;
     uint8_t* const dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
-    constexpr int kUnpack = M::kAdders * 4, kIssue = kUnpack + 8;  // first warps of the roles
+    constexpr int kUnpack = M::kAdders * 4, kIssue = kUnpack + 4 * M::kUnpackers;  // first warps of the roles
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x) % a.cluster;
     const int first = static_cast<int>(blockIdx.x) / a.cluster, step = static_cast<int>(gridDim.x) / a.cluster;
@@ -379,9 +381,11 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
     const uint32_t tmem = bars.tmem, tmem_a = tmem + M::kSums * N;
 
     if (warp >= kUnpack && warp < kIssue) {
-        // ---- unpack: a thread for each weight row; the two groups take blocks in turn, counted over all items, so
-        // that neither waits for a buffer more than one use behind the other.  A raw stage holds two of a
-        // group's blocks: 64 bytes of each row, and 64 bytes 128 further on.
+        // ---- unpack: a thread for each weight row; the U groups take blocks in turn, counted over all items, so
+        // that none waits for a buffer more than one use behind another.  A raw stage holds two of a group's
+        // blocks: 64 bytes of each row, and 64 bytes 64 U further on.
+        constexpr int U = M::kUnpackers;
+        static_assert(U <= M::kA, "a group's next block must not be two uses of a buffer past its last");
         if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::kUnpackRegs));
         const int w = warp & 3, turn = (warp - kUnpack) >> 2;
         const uint32_t ring = shared_of(raw_ring) + (warp - kUnpack) * M::kRaw * kRawStage;
@@ -392,13 +396,12 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
         int c_item = first, c_block = turn, c_stage = 0;  // the next raw stage's item and first block
         auto issue = [&]() {
             while (c_block >= nb && c_item < items) {  // the group's next block, of a later item
-                c_block -= nb;
-                c_block &= 1;
+                c_block = (c_block - nb) & (U - 1);
                 c_item += step;
             }
             if (c_item < items) {
                 const int64_t n0 = static_cast<int64_t>(c_item) * 128 + w * 32 + (lane >> 3);
-                const int b = c_block + (cc >> 2) * 2;
+                const int b = c_block + (cc >> 2) * U;
                 const int k = (b0 + b) * kInner + (cc & 3) * 32;  // first inner value of the lane's chunk
                 const bool inner = b < nb && k < end;
                 const char* src = static_cast<const char*>(a.q) + n0 * a.row_bytes + k / 2;
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
                     copy16((to ^ ((i & 1) * 64)) + i * 512, on ? src : static_cast<const char*>(a.q), on);
                     src += 4 * a.row_bytes;
                 }
-                c_block += 4;
+                c_block += 2 * U;
             }
             copies_end();
             c_stage = c_stage + 1 == M::kRaw ? 0 : c_stage + 1;
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
         uint32_t before = 0;  // blocks of the items before
         bool ok = true;
         for (int item = first; ok && item < items; item += step, before += nb) {
-            int block = (turn ^ before) & 1;
+            int block = (turn - before) & (U - 1);
             const int64_t n = static_cast<int64_t>(item) * 128 + w * 32 + lane;
             const uint8_t* zero_at = a.zeros && n < a.outs ? a.zeros + n * a.groups : nullptr;
             // the zero points of a block's groups, one a byte; loaded a raw stage ahead
@@ -437,8 +440,8 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
             };
             uint32_t z_now[2], z_next[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) z_next[h] = zeros_of((b0 + block + 2 * h) * per);
-            for (; ok && block < nb; block += 4) {
+            for (int h = 0; h < 2; ++h) z_next[h] = zeros_of((b0 + block + U * h) * per);
+            for (; ok && block < nb; block += 2 * U) {
                 copies_wait<M::kRaw - 2>();
                 __syncwarp();
                 issue();
@@ -447,11 +450,11 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     z_now[h] = z_next[h];
-                    z_next[h] = zeros_of((b0 + block + 4 + 2 * h) * per);
+                    z_next[h] = zeros_of((b0 + block + 2 * U + U * h) * per);
                 }
 #pragma unroll 1
-                for (int h = 0; h < 2 && block + 2 * h < nb; ++h) {
-                    const uint32_t used = before + block + 2 * h;
+                for (int h = 0; h < 2 && block + U * h < nb; ++h) {
+                    const uint32_t used = before + block + U * h;
                     const int buf = used % M::kA;
                     uint4 q[4];
 #pragma unroll
