@@ -13,6 +13,16 @@
 // where the two ends of that error interval round to different codes (about
 // one value in 10^5) the value is recomputed in fp64, with Taylor sums too.  The same holds for the
 // page's largest magnitude, where the interval's ends give different scales.
+//
+// Bounds and figures.  One token of a sequence: latency, a launch and three
+// dependent loads (position, page, scale): 4.0 us; 256 tokens of 32 + 8 heads
+// of 64: 5.5 us.  Prompts (8,100 tokens of 32 + 8 heads of 128): 73 us against
+// 35 us of memory time; the page blocks wait on their own chain (find the page,
+// load, maximum, round) at 16 warps an SM, which their registers allow.
+// Measured and left: eight values a thread (187 us), one launch for queries and
+// pages (135 us: the queries are held to the pages' registers), no load ahead
+// of the next head (78 us), eight heads a block (80 us), one pass in registers
+// at three blocks an SM (85 us).
 #include <cstring>
 
 #include "kv_host.cuh"

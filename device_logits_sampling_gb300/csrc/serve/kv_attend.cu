@@ -26,6 +26,15 @@
 // p' = 2^(s + ev - m) are at most 1 and small only where their product with
 // the values is, so their fp16 form loses nothing that counts; the sum of the
 // true weights is sum p' 2^-ev, in the same reference.
+//
+// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 277 us,
+// 6.7 TB/s, 98% of the measured copy rate: the 12 warps of an SM need 2,000
+// clocks a step, which is what memory gives them 4 KB in.  One sequence of
+// 200,003: 73 us (83%); 256 of 1 to 4,096: 81 us (54%): the line's ends, about
+// 12,000 clocks to the first step and as many for the joins.  Short calls are
+// those: 13 us.  Measured and left: a block for each (sequence, head) and one
+// token at a time a warp (157 ms for the 200,003), more warps with fewer
+// registers and stages (95 us for it), joins row by row in every thread (84 us).
 #include <atomic>
 
 #include "kv_host.cuh"

@@ -45,6 +45,14 @@ struct W4Args {
 // product is free, x is laid out to match what one shared load of a lane
 // gives.  Inner dimensions over one block's reach are split over a cluster,
 // whose first block adds the others' sums.
+//
+// Bounds and figures.  Instruction issue: about 150 warp instructions for each
+// KB of weights (groups of 64) of the 174 that its share of memory time leaves
+// an SM.  One row by 129,280 x 4,096, groups of 64: 61 us, 4.6 TB/s, 68% of the
+// measured copy rate; 4,096 x 4,096: 5.9 us, most of it a launch and one round
+// trip to memory. Measured and left: 16 rows in two tiles (163 us, shared-memory
+// bound: w4_many.cu takes 83), joining every tile (69 us against 64), a rolled
+// staging loop (19,500 clocks for 7 rows against 10,700).
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kXVecs = 8;               // 16-byte vectors of x a thread stages
@@ -111,7 +119,7 @@ __device__ __forceinline__ uint4 raw8(const void* p, bool vec) {
 // order of the products, and the sums of each group.  All of it is loaded at
 // once (64 KB at most: eight vectors a thread), so the block waits for memory
 // once before its first product.
-template <int DT, int G, int NT, bool Z>
+template <int DT, int G, bool Z>
 __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, int ks) {
     const int tid = threadIdx.x;
     const int rows = f.a.rows, units = ks >> 3, groups = ks / G, all = units * rows;
@@ -135,7 +143,7 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
             }
         }
     }
-    if (tid < 8 * NT) top[tid] = 0;
+    if (tid < 8) top[tid] = 0;
     __syncthreads();
     float v[8];
     auto unpack = [&](const uint4& r) {
@@ -163,7 +171,7 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
         }
     }
     __syncthreads();
-    if (tid < 8 * NT) {
+    if (tid < 8) {
         const float largest = Half<DT>::unpack(top[tid]).x;
         const int ex = static_cast<int>(__float_as_uint(largest) >> 23) - 127;
         const int e = largest == 0.0f ? 0 : (14 - ex > 120 ? 120 : 14 - ex);
@@ -172,8 +180,8 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
     __syncthreads();
     const float* up = reinterpret_cast<const float*>(top);
     float* xs = reinterpret_cast<float*>(dyn + f.xs_off);
-    for (int i = tid; i < groups * 8 * NT; i += kFewThreads)
-        if (i % (8 * NT) >= rows) xs[i] = 0.0f;
+    for (int i = tid; i < groups * 8; i += kFewThreads)
+        if (i % (8) >= rows) xs[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kXVecs; ++j) {
         if (j * kFewThreads >= all) break;
@@ -198,7 +206,7 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
 #pragma unroll
         for (int x = 1; x < G / 8; x <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
         // without zero points the sum comes times the common one, 8 * 2^-24
-        if (on && (u & (G / 8 - 1)) == 0) xs[gi * 8 * NT + m] = Z ? sum : sum * 0x1p-21f;
+        if (on && (u & (G / 8 - 1)) == 0) xs[gi * 8 + m] = Z ? sum : sum * 0x1p-21f;
     }
 }
 
@@ -206,9 +214,9 @@ template <int N>
 struct alignas(4 * N) Words {
     uint32_t w[N];
 };
-// G: group. NT: tiles of 8 rows of x. P: inner values of a part at most (512 or
+// G: group. P: inner values of a part at most (512 or
 // 256). Z: zero points are given.
-template <int G, int NT, int P, bool Z>
+template <int G, int P, bool Z>
 __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_constant__ FewArgs f) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     const W4Args& a = f.a;
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     // [group][row]: the scale, and with Z the zero point times 2^-24
     constexpr int SW = Z ? 2 : 1;
     float* scales = reinterpret_cast<float*>(dyn + f.scale_off) + warp * (16 * PG * SW);
-    const float* xs = reinterpret_cast<const float*>(dyn + f.xs_off) + (p0 / G) * 8 * NT + 2 * t;
+    const float* xs = reinterpret_cast<const float*>(dyn + f.xs_off) + (p0 / G) * 8 + 2 * t;
     const uint8_t* xf = dyn + f.x_off + (static_cast<size_t>(p0 / 32) * a.rows * 4 + g * 4 + t) * 16;
 
     // A lane copies chunk cc of the rows ch, ch + step, ...; the rows' permutation (weight_at) is an
@@ -289,9 +297,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     fetch(first_tile);
 
     if (a.x_bf16)
-        stage_x<ARC_BF16, G, NT, Z>(f, dyn, k0, ks);
+        stage_x<ARC_BF16, G, Z>(f, dyn, k0, ks);
     else
-        stage_x<ARC_F16, G, NT, Z>(f, dyn, k0, ks);
+        stage_x<ARC_F16, G, Z>(f, dyn, k0, ks);
     __syncthreads();
     if (f.cluster > 1) cluster_sync_all();  // every block runs before its memory is written to
 
@@ -317,11 +325,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         fill = fill + 1 == f.stages ? 0 : fill + 1;
         fetch(tile + tile_step);
 
-        float y[NT][4];
+        float y[4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[nt][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) y[e] = 0.0f;
         const uint8_t* st = dyn + (warp * f.stages + stage) * STAGE + read_at;
         stage = stage + 1 == f.stages ? 0 : stage + 1;
         auto one_group = [&](int gi) {
@@ -331,23 +337,17 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             const uint8_t* at = st + ((c * 16) ^ gbits) + o;
             const Words<WG> w0 = *reinterpret_cast<const Words<WG>*>(at);
             const Words<WG> w1 = *reinterpret_cast<const Words<WG>*>(at + 8 * PITCH);
-            float acc[NT][4];
+            float acc[4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) acc[e] = 0.0f;
 #pragma unroll
             for (int w = 0; w < WG; ++w) {
                 constexpr uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u;
                 const uint32_t u0 = w0.w[w] >> 8, u1 = w1.w[w] >> 8;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (8 * nt + g < a.rows)
-                        x = *reinterpret_cast<const uint4*>(xf + ((gi * WG + w) * a.rows + 8 * nt) * 64);
-                    mma16816(acc[nt], w0.w[w] & lo, w1.w[w] & lo, u0 & lo, u1 & lo, x.x, x.y);
-                    mma16816(acc[nt], w0.w[w] & hi, w1.w[w] & hi, u0 & hi, u1 & hi, x.z, x.w);
-                }
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (g < a.rows) x = *reinterpret_cast<const uint4*>(xf + (gi * WG + w) * a.rows * 64);
+                mma16816(acc, w0.w[w] & lo, w1.w[w] & lo, u0 & lo, u1 & lo, x.x, x.y);
+                mma16816(acc, w0.w[w] & hi, w1.w[w] & hi, u0 & hi, u1 & hi, x.z, x.w);
             }
             float s0, s1, z0 = 1.0f, z1 = 1.0f;
             if constexpr (Z) {
@@ -358,14 +358,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
                 s0 = scales[gi * 16 + g];
                 s1 = scales[gi * 16 + g + 8];
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float2 sx = *reinterpret_cast<const float2*>(xs + gi * 8 * NT + 8 * nt);
-                y[nt][0] = fmaf(s0, fmaf(-z0, sx.x, acc[nt][0]), y[nt][0]);
-                y[nt][1] = fmaf(s0, fmaf(-z0, sx.y, acc[nt][1]), y[nt][1]);
-                y[nt][2] = fmaf(s1, fmaf(-z1, sx.x, acc[nt][2]), y[nt][2]);
-                y[nt][3] = fmaf(s1, fmaf(-z1, sx.y, acc[nt][3]), y[nt][3]);
-            }
+            const float2 sx = *reinterpret_cast<const float2*>(xs + gi * 8);
+            y[0] = fmaf(s0, fmaf(-z0, sx.x, acc[0]), y[0]);
+            y[1] = fmaf(s0, fmaf(-z0, sx.y, acc[1]), y[1]);
+            y[2] = fmaf(s1, fmaf(-z1, sx.x, acc[2]), y[2]);
+            y[3] = fmaf(s1, fmaf(-z1, sx.y, acc[3]), y[3]);
         };
         if (whole_part) {
 #pragma unroll
@@ -379,17 +376,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
         // turn: one barrier a period.
         const int vals = 16 * a.rows;
         float* mine = reinterpret_cast<float*>(dyn + f.red_off) + ((turn * f.period + count) * kFewWarps + warp) * vals;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int m = 8 * nt + 2 * t;
-            if (m < a.rows) {
-                mine[m * 16 + g] = y[nt][0];
-                mine[m * 16 + g + 8] = y[nt][2];
-            }
-            if (m + 1 < a.rows) {
-                mine[m * 16 + 16 + g] = y[nt][1];
-                mine[m * 16 + 16 + g + 8] = y[nt][3];
-            }
+        if (2 * t < a.rows) {
+            mine[2 * t * 16 + g] = y[0];
+            mine[2 * t * 16 + g + 8] = y[2];
+        }
+        if (2 * t + 1 < a.rows) {
+            mine[2 * t * 16 + 16 + g] = y[1];
+            mine[2 * t * 16 + 16 + g + 8] = y[3];
         }
         ++count;
         if (count < f.period && tile + tile_step < f.tiles) continue;
@@ -449,10 +442,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
     copies_wait<0>();
 }
 
-template <int G, int NT, int P, bool Z>
+template <int G, int P, bool Z>
 int start_few(const FewArgs& f, int smem, int dev, int sms, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    if (arc::prepare(few_kernel<G, NT, P, Z>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
+    if (arc::prepare(few_kernel<G, P, Z>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.blockDim = dim3(kFewThreads, 1, 1);
@@ -475,7 +468,7 @@ int start_few(const FewArgs& f, int smem, int dev, int sms, cudaStream_t st) {
         clusters = known.load(std::memory_order_relaxed);
         if (clusters == 0) {
             cfg.gridDim = dim3(static_cast<unsigned>(f.cluster), 1, 1);
-            if (cudaOccupancyMaxActiveClusters(&clusters, few_kernel<G, NT, P, Z>, &cfg) != cudaSuccess || clusters < 1) {
+            if (cudaOccupancyMaxActiveClusters(&clusters, few_kernel<G, P, Z>, &cfg) != cudaSuccess || clusters < 1) {
                 (void)cudaGetLastError();
                 clusters = sms / f.cluster;
             }
@@ -483,20 +476,19 @@ int start_few(const FewArgs& f, int smem, int dev, int sms, cudaStream_t st) {
         }
     }
     cfg.gridDim = dim3(static_cast<unsigned>((clusters < f.tiles ? clusters : f.tiles) * f.cluster), 1, 1);
-    if (cudaLaunchKernelEx(&cfg, few_kernel<G, NT, P, Z>, f) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, few_kernel<G, P, Z>, f) != cudaSuccess) {
         (void)cudaGetLastError();
         return ARC_E_CUDA;
     }
     return ARC_OK;
 }
 
-template <int G, int NT>
+template <int G>
 int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
     FewArgs f;
     f.a = a;
     // a block's x stays within 64 KB: 4,096 inner values of 8 rows
     constexpr int reach = kXVecs * kFewThreads;
-    static_assert(NT == 1, "x is staged for one tile of 8 rows");
     int c = 1;
     while (c * reach < a.w.ins) c *= 2;
     f.cluster = c;
@@ -525,11 +517,11 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
             return at;
         };
         f.x_off = take(a.rows * f.slice * 2);
-        f.xs_off = take(groups * 8 * NT * 4);
+        f.xs_off = take(groups * 8 * 4);
         f.scale_off = take(kFewWarps * 16 * (most / G) * (a.w.zeros ? 8 : 4));
         f.red_off = take(2 * f.period * kFewWarps * 16 * a.rows * 4);
         f.join_off = take(f.cluster > 1 ? 2 * f.cluster * (kFewWarps / p) * f.period * 16 * a.rows * 4 : 0);
-        f.up_off = take(8 * NT * 4);
+        f.up_off = take(8 * 4);
         return off;
     };
     f.period = 1;
@@ -546,15 +538,14 @@ int launch_few(const W4Args& a, int dev, int sms, cudaStream_t st) {
     f.tiles = static_cast<int32_t>(tiles_of(parts));
     f.x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
     if (f.part > 256)
-        return a.w.zeros ? start_few<G, NT, 512, true>(f, off, dev, sms, st) : start_few<G, NT, 512, false>(f, off, dev, sms, st);
-    return a.w.zeros ? start_few<G, NT, 256, true>(f, off, dev, sms, st) : start_few<G, NT, 256, false>(f, off, dev, sms, st);
+        return a.w.zeros ? start_few<G, 512, true>(f, off, dev, sms, st) : start_few<G, 512, false>(f, off, dev, sms, st);
+    return a.w.zeros ? start_few<G, 256, true>(f, off, dev, sms, st) : start_few<G, 256, false>(f, off, dev, sms, st);
 }
 
-template <int NT>
 int launch_few_group(const W4Args& a, int dev, int sms, cudaStream_t st) {
-    if (a.w.group == 128) return launch_few<128, NT>(a, dev, sms, st);
-    if (a.w.group == 64) return launch_few<64, NT>(a, dev, sms, st);
-    return launch_few<32, NT>(a, dev, sms, st);
+    if (a.w.group == 128) return launch_few<128>(a, dev, sms, st);
+    if (a.w.group == 64) return launch_few<64>(a, dev, sms, st);
+    return launch_few<32>(a, dev, sms, st);
 }
 
 constexpr int kFewRows = 8;  // more rows take the 5th-generation tensor cores (w4_many.cu)
@@ -603,7 +594,7 @@ int arc_w4_matvec(const arc_w4_weight* weight, const void* x, int64_t rows, int6
         return ARC_E_CUDA;
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (rows <= kFewRows) return launch_few_group<1>(a, dev, sms, st);
+    if (rows <= kFewRows) return launch_few_group(a, dev, sms, st);
     ManyArgs m{};
     m.q = weight->q;
     m.scales = weight->scales;

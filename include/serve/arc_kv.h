@@ -39,8 +39,10 @@ extern "C" {
 #define ARC_SERVE_ABI_VERSION 1
 
 /* device-side error bits, ORed into *err_word (never cleared here) */
-#define ARC_KV_ERR_PAGE 0x1u     /* page id outside [0, pages): token not stored / its row's output is NaN */
-#define ARC_KV_ERR_POSITION 0x2u /* token past max_pages * page_size: as ARC_KV_ERR_PAGE */
+#define ARC_KV_ERR_PAGE 0x1u     /* page id outside [0, pages): tokens not stored; the attention rows of the
+                                    sequence that are computed with such a page are NaN */
+#define ARC_KV_ERR_POSITION 0x2u /* tokens past max_pages * page_size: not stored; attention rows of the
+                                    sequence are NaN */
 #define ARC_KV_ERR_NAN 0x4u      /* a rotated key or a value is NaN: stored as 0 */
 #define ARC_KV_ERR_OFFSETS 0x8u  /* row_offsets does not ascend from 0 to T: the sequence is left out */
 
