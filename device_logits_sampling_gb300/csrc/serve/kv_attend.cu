@@ -30,7 +30,7 @@
 // Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 277 us,
 // 6.7 TB/s, 98% of the measured copy rate: the 12 warps of an SM need 2,000
 // clocks a step, which is what memory gives them 4 KB in.  One sequence of
-// 200,003: 73 us (83%); 256 of 1 to 4,096: 81 us (54%): the line's ends, about
+// 200,003: 73 us (83%); 256 of 1 to 4,096: 63.5 us (69%): the line's ends, about
 // 12,000 clocks to the first step and as many for the joins.  Short calls are
 // those: 13 us.  Measured and left: a block for each (sequence, head) and one
 // token at a time a warp (157 ms for the 200,003), more warps with fewer
@@ -47,7 +47,8 @@ using namespace arcs;
 
 constexpr int kMaxBlocks = 256;  // blocks of a launch: at most one for each SM
 constexpr float kNothing = -3.0e38f;  // maximum of no score: finite, so that differences need no special case
-constexpr int kItemCost = 1;     // an item's fixed cost in steps (query load, output store), for the cut
+constexpr int kItemCost = 3;     // an item's fixed cost in steps (query load, output store), for the cut (256 ragged
+                                 // sequences: 81 us with 1, 67 with 2, 63.5 with 3, 64 with 4)
 constexpr int kStatusBytes = kMaxBlocks * 4;
 
 struct AttendArgs {
