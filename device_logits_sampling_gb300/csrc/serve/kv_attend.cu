@@ -68,11 +68,11 @@ template <int D, int NT>
 struct Shape;
 template <>
 struct Shape<64, 1> {
-    static constexpr int kWarps = 16, kStages = 4;
+    static constexpr int kWarps = 16, kStages = 2;
 };
 template <>
 struct Shape<64, 2> {
-    static constexpr int kWarps = 12, kStages = 4;
+    static constexpr int kWarps = 12, kStages = 3;
 };
 template <>
 struct Shape<128, 1> {
@@ -87,6 +87,15 @@ struct Shape<256, 1> {
     static constexpr int kWarps = 8, kStages = 2;
 };
 
+// A step is 16 tokens; for heads of 64, whose 16 tokens are 2 KB, 32: the work
+// that a step costs whatever its size is shared by two halves, which may lie in
+// different pages.
+template <int D>
+struct Step {
+    static constexpr int kShift = D == 64 ? 5 : 4;
+    static constexpr int kHalves = 1 << (kShift - 4);
+};
+
 struct Part {        // a partial's item
     int64_t from, to;  // the item's units on the line
     int64_t first;     // its sequence's first row
@@ -99,12 +108,14 @@ struct Part {        // a partial's item
 template <int D, int NT>
 struct Smem {
     static constexpr int kW = Shape<D, NT>::kWarps, kS = Shape<D, NT>::kStages, kR = 8 * NT;
-    static constexpr int kStage = 32 * D;  // 16 keys and 16 values
+    static constexpr int kH = Step<D>::kHalves;
+    static constexpr int kHalf = 32 * D;   // 16 keys and 16 values
+    static constexpr int kStage = kH * kHalf;
     static constexpr int kRing = kS * kStage, kHead = kR * D * 4;
     static constexpr int kPerWarp = kRing + kHead;
     static constexpr int kThreads = kW * 32;
     static_assert(kRing >= kHead, "the last partial goes where the ring was");
-    float scales[kW][kS][2];
+    float scales[kW][kS][kH][2];
     float m[2 * kW][kR], l[2 * kW][kR];
     Part part[2 * kW];
     uint32_t run[32];  // partials of the same item, as a mask
@@ -175,7 +186,7 @@ struct Seq {
     bool bad, late;  // offsets are wrong; past the page table
 };
 
-template <int R>
+template <int R, int TS>
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int64_t b) {
     Seq q;
     q.bad = q.late = false;
@@ -201,8 +212,8 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int64_t b) {
         return q;
     }
     const int end = q.pos + q.n;
-    q.step0 = a.q.window > 0 && q.pos + 1 > a.q.window ? (q.pos + 1 - a.q.window) >> 4 : 0;
-    q.cost = ((end + 15) >> 4) - q.step0 + kItemCost;
+    q.step0 = a.q.window > 0 && q.pos + 1 > a.q.window ? (q.pos + 1 - a.q.window) >> TS : 0;
+    q.cost = ((end + (1 << TS) - 1) >> TS) - q.step0 + kItemCost;
     q.tiles = static_cast<int32_t>((n * a.group + R - 1) / R);
     return q;
 }
@@ -212,7 +223,7 @@ __device__ __forceinline__ int64_t units_of(const AttendArgs& a, const Seq& q) {
 }
 
 // A place on the line: an item, and a unit of it.
-template <int R>
+template <int R, int TS>
 struct Cursor {
     Seq q;
     int64_t b;
@@ -232,7 +243,7 @@ struct Cursor {
                 left = 0;
                 return;
             }
-            q = load_seq<R>(a, b);
+            q = load_seq<R, TS>(a, b);
         } while (q.cost == 0);
     }
 };
@@ -241,6 +252,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using S = Smem<D, NT>;
     constexpr int R = S::kR, W = S::kW, ST = S::kS, kThreads = S::kThreads;
+    constexpr int TS = Step<D>::kShift, HV = Step<D>::kHalves;
     constexpr int KS = D / 16;   // 16-value slices of a head
     constexpr int KC = D / 64;   // 16-byte chunks of a key that a lane takes
     constexpr int LB = D / 8;    // values of a head that a lane holds of the output
@@ -254,7 +266,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     int64_t mine = 0;
     uint32_t seen = 0;
     for (int64_t b = run * tid; b < run * (tid + 1) && b < a.s.B; ++b) {
-        const Seq q = load_seq<R>(a, b);
+        const Seq q = load_seq<R, TS>(a, b);
         mine += units_of(a, q);
         if (q.bad) seen |= ARC_KV_ERR_OFFSETS;
         if (q.late) seen |= ARC_KV_ERR_POSITION;
@@ -281,7 +293,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
 
     // rows without work: parked sequences give 0, those past their page table NaN
     for (int64_t b = blockIdx.x; b < a.s.B; b += gridDim.x) {
-        const Seq q = load_seq<R>(a, b);
+        const Seq q = load_seq<R, TS>(a, b);
         if (q.cost != 0 || q.n == 0) continue;
         const uint32_t fill = q.late ? (a.bf16 ? 0x7FC0u : 0x7E00u) : 0u;
         const int64_t vals = int64_t{q.n} * a.q.q_heads * D;
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     float* const tail_store = reinterpret_cast<float*>(dyn + warp * S::kPerWarp);
 
     if (from < to) {
-        Cursor<R> at;  // of the arithmetic; `ahead` of the copies
+        Cursor<R, TS> at;  // of the arithmetic; `ahead` of the copies
         {
             int lo = 0, hi = kThreads;  // the run of sequences that holds `from`
             while (hi - lo > 1) {
@@ -322,10 +334,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             }
             int64_t rest = from - sm.before[lo];
             at.b = run * lo;
-            at.q = load_seq<R>(a, at.b);
+            at.q = load_seq<R, TS>(a, at.b);
             while (rest >= units_of(a, at.q) && at.b + 1 < a.s.B) {
                 rest -= units_of(a, at.q);
-                at.q = load_seq<R>(a, ++at.b);
+                at.q = load_seq<R, TS>(a, ++at.b);
             }
             const int64_t item = at.q.cost <= 0     ? 0
                                  : rest >> 31 == 0 ? static_cast<uint32_t>(rest) / static_cast<uint32_t>(at.q.cost)
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             at.head = static_cast<int32_t>(item - int64_t{at.tile} * a.c.heads);
             at.left = at.q.cost > 0 ? to - from : 0;
         }
-        Cursor<R> ahead = at;
+        Cursor<R, TS> ahead = at;
 
         // ---- copies
         int issued = 0;                 // stage of the next copy
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
         const int32_t* table = nullptr;
         const char *k_head = nullptr, *v_head = nullptr;  // its head, this lane's 16 bytes
         const float *k_scale = nullptr, *v_scale = nullptr;
-        int page = 0, page_of = -1, page_next = 0;  // current page id, its index, the id after it
+        int page = 0, page_of = -1, page_next = 0, page_ahead = -1;  // page id, its index, the id after it, that one's
         int64_t page_at = 0;
         bool ok = true;
         const int ps_shift = 31 - __clz(a.c.page_size), ps_mask = a.c.page_size - 1;
@@ -369,7 +381,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             v_head = static_cast<const char*>(a.c.v) + head;
             k_scale = a.c.k_scale + ahead.head;
             v_scale = a.c.v_scale + ahead.head;
-            page_of = -1;
+            page_of = page_ahead = -1;
         };
         uint32_t to[2];  // a lane's copies alternate between two places of a pattern that moves on by rows
         to[0] = ring + chunk_at<D>(lane / (D / 16), lane % (D / 16));
@@ -377,35 +389,45 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
         auto issue = [&]() {
             if (step == step_end) enter();
             if (step < step_end) {
-                const int tok0 = step << 4, pi = tok0 >> ps_shift;
-                if (pi != page_of) {
-                    page = page_of >= 0 ? page_next : __ldg(table + pi);
-                    page_of = pi;
-                    if (((pi + 1) << ps_shift) >> 4 < step_end) page_next = __ldg(table + pi + 1);
-                    ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
-                    page_at = ok ? page * a.c.page_stride : 0;
-                    if (!ok && lane == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
-                }
-                const int64_t at = page_at + (tok0 & ps_mask) * D;
-                const char *kp = k_head + at, *vp = v_head + at;
-                const uint32_t move = issued * S::kStage;
-                const bool whole = ok && tok0 >= first && tok0 + 15 <= last;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    // D = 256: the pattern of chunk_at has a period of 16 rows, eight copies
-                    const uint32_t dst = (D == 256 ? ring + chunk_at<D>((lane + 32 * i) / 16, (lane + 32 * i) % 16)
-                                                   : to[i & 1] + (i >> 1) * 1024) + move;
-                    const bool on = whole || (ok && tok0 + (lane + 32 * i) / (D / 16) <= last && tok0 + (lane + 32 * i) / (D / 16) >= first);
-                    copy16(dst, kp + i * 512, on);
-                    copy16(dst + 16 * D, vp + i * 512, on);
-                }
-                const int64_t si = static_cast<int64_t>(ok ? page : 0) * a.c.heads;
-                if (ok) {
-                    if (lane < 2)
-                        copy4(static_cast<uint32_t>(__cvta_generic_to_shared(&sm.scales[warp][issued][lane])),
-                              (lane ? v_scale : k_scale) + si);
-                } else if (lane < 2) {
-                    sm.scales[warp][issued][lane] = __int_as_float(0x7FC00000);
+                for (int hv = 0; hv < HV; ++hv) {
+                    const int tok0 = (step << TS) + 16 * hv, pi = tok0 >> ps_shift;
+                    // (a half that no row sees takes no page)
+                    const bool none = HV > 1 && (tok0 > last || tok0 + 15 < first);
+                    if (!none && pi != page_of) {
+                        page = pi == page_ahead ? page_next : __ldg(table + pi);
+                        page_of = pi;
+                        page_ahead = -1;
+                        if (((pi + 1) << ps_shift) <= last && ((pi + 1) << ps_shift) >> TS < step_end) {
+                            page_next = __ldg(table + pi + 1);
+                            page_ahead = pi + 1;
+                        }
+                        ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.c.pages);
+                        page_at = ok ? page * a.c.page_stride : 0;
+                        if (!ok && lane == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
+                    }
+                    const bool here = ok && !none;
+                    const int64_t at = here ? page_at + (tok0 & ps_mask) * D : 0;
+                    const char *kp = k_head + at, *vp = v_head + at;
+                    const uint32_t move = issued * S::kStage + hv * S::kHalf;
+                    const bool whole = here && tok0 >= first && tok0 + 15 <= last;
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        // D = 256: the pattern of chunk_at has a period of 16 rows, eight copies
+                        const uint32_t dst = (D == 256 ? ring + chunk_at<D>((lane + 32 * i) / 16, (lane + 32 * i) % 16)
+                                                       : to[i & 1] + (i >> 1) * 1024) + move;
+                        const int tok = tok0 + (lane + 32 * i) / (D / 16);
+                        const bool on = whole || (here && tok <= last && tok >= first);
+                        copy16(dst, kp + i * 512, on);
+                        copy16(dst + 16 * D, vp + i * 512, on);
+                    }
+                    if (here) {
+                        if (lane < 2)
+                            copy4(static_cast<uint32_t>(__cvta_generic_to_shared(&sm.scales[warp][issued][hv][lane])),
+                                  (lane ? v_scale : k_scale) + static_cast<int64_t>(page) * a.c.heads);
+                    } else if (lane < 2) {
+                        sm.scales[warp][issued][hv][lane] = none ? 1.0f : __int_as_float(0x7FC00000);
+                    }
                 }
                 ++step;
             }
@@ -496,49 +518,61 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 copies_wait<ST - 2>();
                 __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
                 issue();
-                const uint8_t *kst = dyn + warp * S::kPerWarp + stage * S::kStage, *vst = kst + 16 * D;
-                const float ks = sm.scales[warp][stage][0];
-                const uint32_t vb = __float_as_uint(sm.scales[warp][stage][1]);
-                stage = stage + 1 == ST ? 0 : stage + 1;
-                const int tok0 = (at.q.step0 + u - kItemCost) << 4;
-
-                float s[NT][4];
+                const uint8_t* const st = dyn + warp * S::kPerWarp + stage * S::kStage;
+                float ks[HV];
+                uint32_t vb[HV];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
-#pragma unroll
-                for (int i = 0; i < KC; ++i) {
-                    const uint4 k0 = lds16(kst + chunk_at<D>(g, KC * t + i));
-                    const uint4 k1 = lds16(kst + chunk_at<D>(g + 8, KC * t + i));
-                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t a0, a1, a2, a3;
-                        e4m3x4_to_half2(w0[w], a0, a2);
-                        e4m3x4_to_half2(w1[w], a1, a3);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816(s[nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
-                    }
+                for (int hv = 0; hv < HV; ++hv) {
+                    ks[hv] = sm.scales[warp][stage][hv][0];
+                    vb[hv] = __float_as_uint(sm.scales[warp][stage][hv][1]);
                 }
-                const float ev = static_cast<float>(static_cast<int>((vb >> 23) & 0xFF) - 127);
-                const float vm = __uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u);
-                const float vi = __uint_as_float((254u - ((vb >> 23) & 0xFF)) << 23);
-                const bool edge = tok0 + 15 > hi_first || (a.q.window > 0 && tok0 <= hi_last - a.q.window);
-                float top[NT][2];
+                stage = stage + 1 == ST ? 0 : stage + 1;
+                const int tok0 = (at.q.step0 + u - kItemCost) << TS;
+
+                float s[HV][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int hv = 0; hv < HV; ++hv) {
+                    const uint8_t* kst = st + hv * S::kHalf;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s[nt][e] = fmaf(s[nt][e], ks * rf[nt][e & 1], ev);
-                        if (edge) {
-                            const int tok = tok0 + g + (e >> 1) * 8, h = hi[nt][e & 1];
-                            if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) s[nt][e] = -INFINITY;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[hv][nt][e] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < KC; ++i) {
+                        const uint4 k0 = lds16(kst + chunk_at<D>(g, KC * t + i));
+                        const uint4 k1 = lds16(kst + chunk_at<D>(g + 8, KC * t + i));
+                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_to_half2(w0[w], a0, a2);
+                            e4m3x4_to_half2(w1[w], a1, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(s[hv][nt], a0, a1, a2, a3, qf[nt][4 * i + w][0], qf[nt][4 * i + w][1]);
                         }
                     }
+                }
+                const bool edge = tok0 + 16 * HV - 1 > hi_first || (a.q.window > 0 && tok0 <= hi_last - a.q.window);
+                float top[NT][2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(s[nt][e], s[nt][e + 2]);
+                for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = kNothing;
+#pragma unroll
+                for (int hv = 0; hv < HV; ++hv) {
+                    const float ev = static_cast<float>(static_cast<int>((vb[hv] >> 23) & 0xFF) - 127);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s[hv][nt][e] = fmaf(s[hv][nt][e], ks[hv] * rf[nt][e & 1], ev);
+                            if (edge) {
+                                const int tok = tok0 + 16 * hv + g + (e >> 1) * 8, h = hi[nt][e & 1];
+                                if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) s[hv][nt][e] = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[hv][nt][e], s[hv][nt][e + 2]));
+                    }
                 }
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1)
@@ -569,89 +603,95 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                             for (int e = 0; e < 4; ++e) o[nt][i][e] *= f[e & 1];
                     }
                 }
-                uint32_t pf[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
+                for (int hv = 0; hv < HV; ++hv) {
+                    const uint8_t* vst = st + hv * S::kHalf + 16 * D;
+                    const float vm = __uint_as_float((vb[hv] & 0x7FFFFFu) | 0x3F800000u);
+                    const float vi = __uint_as_float((254u - ((vb[hv] >> 23) & 0xFF)) << 23);
+                    uint32_t pf[NT][2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2(s[nt][e] - m[nt][e & 1]);
-                        l[nt][e & 1] = fmaf(p[e], vi, l[nt][e & 1]);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[e] = ex2(s[hv][nt][e] - m[nt][e & 1]);
+                            l[nt][e & 1] = fmaf(p[e], vi, l[nt][e & 1]);
+                        }
+                        // token-major to row-major: what the products take
+                        pf[nt][0] = transpose8x8(pack_f16(p[0] * vm, p[1] * vm));
+                        pf[nt][1] = transpose8x8(pack_f16(p[2] * vm, p[3] * vm));
                     }
-                    // token-major to row-major: what the products take
-                    pf[nt][0] = transpose8x8(pack_f16(p[0] * vm, p[1] * vm));
-                    pf[nt][1] = transpose8x8(pack_f16(p[2] * vm, p[3] * vm));
-                }
 
-                // values: tokens 2t, 2t+1, 2t+8, 2t+9, D / 8 bytes from g * D / 8
-                uint32_t v[4][LB / 4];
+                    // values: tokens 2t, 2t+1, 2t+8, 2t+9, D / 8 bytes from g * D / 8
+                    uint32_t v[4][LB / 4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 2 * t + (i & 1) + (i >> 1) * 8;
-                    if constexpr (D == 64) {
-                        const uint2 x = lds8(vst + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
-                        v[i][0] = x.x;
-                        v[i][1] = x.y;
-                    } else {
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+                        if constexpr (D == 64) {
+                            const uint2 x = lds8(vst + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
+                            v[i][0] = x.x;
+                            v[i][1] = x.y;
+                        } else {
 #pragma unroll
-                        for (int c = 0; c < D / 128; ++c) {
-                            const uint4 x = lds16(vst + chunk_at<D>(r, (D / 128) * g + c));
-                            v[i][4 * c] = x.x;
-                            v[i][4 * c + 1] = x.y;
-                            v[i][4 * c + 2] = x.z;
-                            v[i][4 * c + 3] = x.w;
+                            for (int c = 0; c < D / 128; ++c) {
+                                const uint4 x = lds16(vst + chunk_at<D>(r, (D / 128) * g + c));
+                                v[i][4 * c] = x.x;
+                                v[i][4 * c + 1] = x.y;
+                                v[i][4 * c + 2] = x.z;
+                                v[i][4 * c + 3] = x.w;
+                            }
                         }
                     }
-                }
-                if (edge && hi_first != hi_last) {
-                    // a token that some rows see and others do not: its NaN values must not
-                    // reach the others through 0 * NaN
-                    uint32_t any = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int w = 0; w < LB / 4; ++w) any |= ((v[i][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                    if (__any_sync(0xFFFFFFFFu, any != 0)) {
-                        for (int r = 0; r < R; ++r) {
-                            const int rr = row0 + r, h = at.q.pos + (rr < rows ? rr : rows - 1) / a.group;
-                            uint32_t hit = 0;  // values of this lane's that are NaN in a token row r sees
-                            for (int i = 0; i < 4; ++i) {
-                                const int tok = tok0 + 2 * t + (i & 1) + (i >> 1) * 8;
-                                if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) continue;
-#pragma unroll
-                                for (int k = 0; k < LB; ++k)
-                                    if (((v[i][k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) hit |= 1u << k;
-                            }
-                            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
-                            hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (8 * nt + 2 * t + e == r)
-#pragma unroll
-                                        for (int k = 0; k < LB; ++k)
-                                            if ((hit >> k) & 1) o[nt][k >> 1][2 * (k & 1) + e] = __int_as_float(0x7FC00000);
-                        }
+                    if (edge && hi_first != hi_last) {
+                        // a token that some rows see and others do not: its NaN values must not
+                        // reach the others through 0 * NaN
+                        uint32_t any = 0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int w = 0; w < LB / 4; ++w) {
-                                const uint32_t bad = ((v[i][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                                v[i][w] &= ~((bad >> 7) * 0xFFu);
+                            for (int w = 0; w < LB / 4; ++w) any |= ((v[i][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                        if (__any_sync(0xFFFFFFFFu, any != 0)) {
+                            for (int r = 0; r < R; ++r) {
+                                const int rr = row0 + r, h = at.q.pos + (rr < rows ? rr : rows - 1) / a.group;
+                                uint32_t hit = 0;  // values of this lane's that are NaN in a token row r sees
+                                for (int i = 0; i < 4; ++i) {
+                                    const int tok = tok0 + 16 * hv + 2 * t + (i & 1) + (i >> 1) * 8;
+                                    if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) continue;
+#pragma unroll
+                                    for (int k = 0; k < LB; ++k)
+                                        if (((v[i][k >> 2] >> (8 * (k & 3))) & 0x7Fu) == 0x7Fu) hit |= 1u << k;
+                                }
+                                hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
+                                hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (8 * nt + 2 * t + e == r)
+#pragma unroll
+                                            for (int k = 0; k < LB; ++k)
+                                                if ((hit >> k) & 1) o[nt][k >> 1][2 * (k & 1) + e] = __int_as_float(0x7FC00000);
                             }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int w = 0; w < LB / 4; ++w) {
+                                    const uint32_t bad = ((v[i][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                    v[i][w] &= ~((bad >> 7) * 0xFFu);
+                                }
+                        }
                     }
-                }
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const int w = i >> 1;
-                    const uint32_t x = __byte_perm(v[0][w], v[1][w], (i & 1) ? 0x7362 : 0x5140);
-                    const uint32_t y = __byte_perm(v[2][w], v[3][w], (i & 1) ? 0x7362 : 0x5140);
-                    uint32_t a0, a1, a2, a3;
-                    e4m3x4_to_half2(x, a0, a1);
-                    e4m3x4_to_half2(y, a2, a3);
+                    for (int i = 0; i < KS; ++i) {
+                        const int w = i >> 1;
+                        const uint32_t x = __byte_perm(v[0][w], v[1][w], (i & 1) ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(v[2][w], v[3][w], (i & 1) ? 0x7362 : 0x5140);
+                        uint32_t a0, a1, a2, a3;
+                        e4m3x4_to_half2(x, a0, a1);
+                        e4m3x4_to_half2(y, a2, a3);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                    }
                 }
             }
 
