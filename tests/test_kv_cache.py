@@ -577,6 +577,18 @@ def test_attend_bad_pages_and_positions(cuda_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,page", [(64, 16), (64, 32), (128, 16), (256, 16)])
+def test_attend_window_needs_no_older_pages(cuda_lib, dim, page):
+    """Pages that lie wholly before the first new token's window may be gone from the table."""
+    pos, news, window = [200, 333, 90, 17], [1, 4, 7, 2], 50
+    c = Case(34, dim, page, 1, 6, pos, news, "bf16")
+    put_new(c)
+    for b, p in enumerate(pos):
+        c.table[b, : max(0, p + 1 - window) // page] = -1
+    check_attend(c, window=window)
+
+
+@pytest.mark.gpu
 def test_attend_memory_and_workspace(cuda_lib):
     import torch
 
