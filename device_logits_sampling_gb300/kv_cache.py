@@ -182,7 +182,7 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
         qt, qh, heads = _heads(q, T, None, dim, "q")
         want(q.dtype == dtype and q.get_device() == dev, "q must have k's type and device")
         if q_out is None:
-            q_out = q.new_empty((T, heads, dim))
+            q_out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), dtype)
         elif q_out is not q:
             want(q_out.dtype == dtype and q_out.get_device() == dev, "q_out must have q's type and device")
         ot, oh, _ = _heads(q_out, T, heads, dim, "q_out")
@@ -208,7 +208,7 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
     T, dim, dev = q.shape[0], cache.head_dim, cache.index
     qt, qh, heads = _heads(q, T, None, dim, "q")
     if out is None:
-        out = q.new_empty((T, heads, dim))
+        out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), q.dtype)
         ot, oh = heads * dim, dim
     else:
         ot, oh, _ = _heads(out, T, heads, dim, "out")

@@ -45,7 +45,7 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
         zp = zeros.data_ptr()
     code = serve.dtype_code(x)
     if out is None:
-        out = x.new_empty((rows, outs), dtype=out_dtype)
+        out = serve.new_output(x, (rows, outs), (outs, 1), out_dtype or x.dtype)
         os = outs
     else:
         want(out.shape == (rows, outs) and out.stride(1) == 1, "out must be [rows, outs], rows contiguous")
@@ -58,7 +58,8 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
     wp, wn = 0, 0
     if rows > FEW_ROWS:
         if workspace is None:
-            workspace = x.new_empty(lib.arc_w4_workspace_bytes(w, rows), dtype=torch.uint8)
+            need = lib.arc_w4_workspace_bytes(w, rows)
+            workspace = serve.new_output(x, (need,), (1,), torch.uint8)
         wp, wn = workspace.data_ptr(), workspace.numel()
     rc = lib.arc_w4_matvec(w, x.data_ptr(), rows, xs if rows > 1 else ins, code, out.data_ptr(), os,
                            serve.dtype_code(out, True), wp, wn, serve.stream_of(stream, dev))
