@@ -16,7 +16,7 @@
 //
 // Bounds and figures.  One token of a sequence: latency, a launch and three
 // dependent loads (position, page, scale): 4.0 us; 256 tokens of 32 + 8 heads
-// of 64: 5.5 us.  Prompts (10,472 tokens of 32 + 8 heads of 128): 73 us against
+// of 64: 5.5 us.  Prompts (10,476 tokens of 32 + 8 heads of 128): 73 us against
 // 35 us of memory time; the page blocks wait on their own chain (find the page,
 // load, maximum, round) at 16 warps an SM, which their registers allow.
 // Measured and left: eight values a thread (187 us), one launch for queries and
