@@ -2,7 +2,7 @@
 //
 // Work.  An item is (sequence, tile of up to R query rows, cached head); the
 // rows of an item are the new tokens' query heads that share the cached head.
-// An item is a run of steps of 16 cached tokens.  All items' steps lie one
+// An item is a run of steps of 16 cached tokens (32 for heads of 64).  All items' steps lie one
 // after another on a line (their counts come from the lengths in device
 // memory), the line is cut into equal pieces, one for each warp of the grid,
 // so that ragged lengths, one long sequence and many short ones all fill the
@@ -30,9 +30,10 @@
 // Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 277 us,
 // 6.7 TB/s, 98% of the measured copy rate: the 12 warps of an SM need 2,000
 // clocks a step, which is what memory gives them 4 KB in.  One sequence of
-// 200,003: 73 us (83%); 256 of 1 to 4,096: 63.5 us (69%): the line's ends, about
+// 200,003: 73 us (83%); 256 of 1 to 4,096: 64 us (68%): the line's ends, about
 // 12,000 clocks to the first step and as many for the joins.  Short calls are
-// those: 13 us.  Measured and left: a block for each (sequence, head) and one
+// those: 14 us.  48 sequences of 1 to 5 drafted tokens, heads of 64, a window:
+// 35 us.  Measured and left: a block for each (sequence, head) and one
 // token at a time a warp (157 ms for the 200,003), more warps with fewer
 // registers and stages (95 us for it), joins row by row in every thread (84 us).
 #include <atomic>
@@ -975,10 +976,15 @@ int arc_kv_attend(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
     a.vec = (vectors(query->q, query->q_token_stride, query->q_head_stride) ? 1 : 0) |
             (vectors(query->out, query->out_token_stride, query->out_head_stride) ? 2 : 0);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // rows of a (sequence, cached head) on average: more than 8 take tiles of 16, which read the cache half as often
-    const int64_t rows = (step->T + step->B - 1) / step->B * a.group;
-    if (cache->head_dim == 64) return rows <= 8 ? launch<64, 1>(a, dev, sms, st) : launch<64, 2>(a, dev, sms, st);
-    if (cache->head_dim == 128) return rows <= 8 ? launch<128, 1>(a, dev, sms, st) : launch<128, 2>(a, dev, sms, st);
+    // Rows of a (sequence, cached head) on average.  Tiles of 16 read the cache half as often and pay when they are
+    // full: groups of 10 to 16 heads, one token each, heads of 128: 130 us against 164 with tiles of 8; of 64: 79 to
+    // 81 against 96.  Ragged drafts leave many of them half empty: up to an average of 18 rows tiles of 8 are faster
+    // (heads of 128, 9 rows: 57 us against 71; 12: 63 to 69 against 68 to 78; 18: 80 against 86; heads of 64, 18
+    // rows: 52 against 57), at 20 rows of sequences of one length tiles of 16 (107 against 113).
+    const int64_t small = step->row_offsets != nullptr && a.group <= 8 ? 18 : 8;
+    const bool wide = step->T * a.group > step->B * small;
+    if (cache->head_dim == 64) return wide ? launch<64, 2>(a, dev, sms, st) : launch<64, 1>(a, dev, sms, st);
+    if (cache->head_dim == 128) return wide ? launch<128, 2>(a, dev, sms, st) : launch<128, 1>(a, dev, sms, st);
     return launch<256, 1>(a, dev, sms, st);
 }
 

