@@ -637,7 +637,10 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
                         store_sums<__half, C>(a, bars.back, y, m0, n);
                 }
             } else {
-                // every copy and product of this block is done: the rings give way to the block's sums
+                // Every copy and product of this block is done: the rings give way to the block's sums. With two
+                // products the first group has waited for the last sums of its own alone, and the other's may still
+                // be read from x: the groups meet first.
+                if constexpr (H == 2) asm volatile("bar.sync 1, %0;" ::"n"(M::kAdders * 128) : "memory");
                 float* mine = reinterpret_cast<float*>(dyn);
 #pragma unroll
                 for (int i = 0; i < C; ++i) mine[(c0 + i) * 128 + row] = half_of(y[i / 2], i & 1);
