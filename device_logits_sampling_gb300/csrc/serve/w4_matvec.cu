@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             copies_wait<1>();
         else
             copies_wait<2>();
+        __syncwarp();  // every lane has read the scales of the tile before
 #pragma unroll
         for (int i = 0; i < SC; ++i) {
             const int e = (lane + 32 * i) * SW;
