@@ -397,7 +397,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             const int c = i / vals, m = (i - c * vals) >> 4, r = i & 15;
             const int64_t n = n0 + r - static_cast<int64_t>(count - 1 - c) * tile_step * per_tile;
             if (n >= a.w.outs) return;
-            v = v * 0x1p24f;
             const int64_t at = m * a.y_stride + n;
             if (a.y_f32)
                 static_cast<float*>(a.y)[at] = v;
@@ -413,7 +412,9 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_kernel(const __grid_consta
             const float* p = red + c * kFewWarps * vals + e;
             float v = 0.0f;
             for (int q = 0; q < f.parts; ++q) v += p[q * vals];
-            v = v / up[e >> 4];  // a power of two
+            // the products' unit first: a row of tiny values has a large factor, and dividing by it would leave
+            // fp32's normal range
+            v = v * 0x1p24f / up[e >> 4];  // powers of two
             if (f.cluster == 1) {
                 finish(i, v);
             } else {
