@@ -68,11 +68,12 @@ class PagedCache:
         ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2))
         return cls(k, v, ks, vs)
 
-    def attend_workspace(self):
-        """Zero-filled workspace for `attend` over caches of this shape (one per stream that uses it)."""
+    def attend_workspace(self, stream=None):
+        """Zero-filled workspace for `attend` over caches of this shape (one per stream that uses it),
+        made on the stream given, else on the current one."""
         n = int(serve.load().arc_kv_attend_workspace_bytes(self._ref))
         want(n > 0, "arc_kv_attend_workspace_bytes rejected the cache")
-        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+        return serve.new_workspace(self.k, n, True, stream)
 
 
 class Rope:
@@ -170,7 +171,7 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
     head_dim] into q_out (a new contiguous tensor where None; may be q itself), which is
     returned.  positions int32 [B]: tokens each sequence holds before these (negative:
     parked); page_table int32 [B, pages]; row_offsets int32 [B + 1] or None for one new
-    token each; err_word int32 [1]: ARC_KV_ERR_* bits."""
+    token each; err_word int32 [1]: ARC_KV_ERR_* bits.  stream: as in `attend`."""
     T, dim, dev = k.shape[0], cache.head_dim, cache.index
     kt, kh, _ = _heads(k, T, cache.heads, dim, "k")
     vt, vh, _ = _heads(v, T, cache.heads, dim, "v")
@@ -182,7 +183,7 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
         qt, qh, heads = _heads(q, T, None, dim, "q")
         want(q.dtype == dtype and q.get_device() == dev, "q must have k's type and device")
         if q_out is None:
-            q_out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), dtype)
+            q_out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), dtype, stream)
         elif q_out is not q:
             want(q_out.dtype == dtype and q_out.get_device() == dev, "q_out must have q's type and device")
         ot, oh, _ = _heads(q_out, T, heads, dim, "q_out")
@@ -204,11 +205,14 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
     """arc_kv_attend: attention of the step's tokens, q [T, q_heads, head_dim], over the cache
     that `append` has just extended (the same positions, page_table and row_offsets).  scale:
     head_dim ** -0.5 where None.  window > 0: each token sees its last `window` tokens alone.
-    workspace: cache.attend_workspace(), made for the call where None.  Returns out."""
+    workspace: cache.attend_workspace(), made for the call where None.  Returns out.
+
+    stream: where the call runs, the current stream where None.  What the call makes for itself (out,
+    workspace) is made there; tensors given have to be ready there."""
     T, dim, dev = q.shape[0], cache.head_dim, cache.index
     qt, qh, heads = _heads(q, T, None, dim, "q")
     if out is None:
-        out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), q.dtype)
+        out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), q.dtype, stream)
         ot, oh = heads * dim, dim
     else:
         ot, oh, _ = _heads(out, T, heads, dim, "out")
@@ -216,7 +220,7 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
     want(q.get_device() == dev and out.get_device() == dev, "every tensor must be on the cache's device")
     code = serve.dtype_code(q)
     if workspace is None:
-        workspace = cache.attend_workspace()
+        workspace = cache.attend_workspace(stream)
     query = _QUERY.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, heads, code,
                         cache.default_scale if scale is None else scale, window)
     rc = serve.load().arc_kv_attend(cache._ref, _step(cache, T, positions, page_table, row_offsets), query,

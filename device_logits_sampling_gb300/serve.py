@@ -118,11 +118,37 @@ except ImportError:
     _empty_strided_cuda = None
 
 
-def new_output(like, shape: tuple, strides: tuple, dtype):
-    """An uninitialised contiguous tensor on the device of `like`."""
+def foreign(stream, device: int) -> bool:
+    """Whether a call is to run on a stream that is not the device's current one."""
+    return stream is not None and int(stream.cuda_stream) != stream_of(None, device)
+
+
+def new_output(like, shape: tuple, strides: tuple, dtype, stream=None):
+    """An uninitialised contiguous tensor on the device of `like`, for a call on `stream`.
+
+    Memory is handed out in the order of the stream it is allocated on, so a call on another
+    stream than the current one gets its output from that stream; the current one is recorded
+    as a user too, since that is where the caller goes on."""
+    if foreign(stream, like.get_device()):
+        with torch.cuda.stream(stream):
+            out = like.new_empty(shape, dtype=dtype)
+        out.record_stream(torch.cuda.current_stream(like.device))
+        return out
     if _empty_strided_cuda is not None and like.is_cuda and torch._C._cuda_getDevice() == like.get_device():
         return _empty_strided_cuda(shape, strides, dtype)
     return like.new_empty(shape, dtype=dtype)
+
+
+def new_workspace(like, nbytes: int, zeroed: bool, stream=None):
+    """Memory for one call on `stream`: allocated (and filled) there, so that its fill comes before the
+    call and its next user after it."""
+    make = torch.zeros if zeroed else torch.empty
+    if foreign(stream, like.get_device()):
+        with torch.cuda.stream(stream):
+            return make(nbytes, dtype=torch.uint8, device=like.device)
+    if not zeroed:
+        return new_output(like, (nbytes,), (1,), torch.uint8)
+    return make(nbytes, dtype=torch.uint8, device=like.device)
 
 
 def want(ok: bool, text: str) -> None:

@@ -23,7 +23,8 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
     """arc_w4_matvec: x [rows, ins] (bfloat16 or float16, 1 .. 256 rows) times the transpose of
     (q - zero) * scale, weight uint8 [outs, ins / 2] (see pack), scales [outs, ins / group] of
     x's type with group 32, 64 or 128, zeros uint8 [outs, ins / group] or None for 8.  Returns
-    out [rows, outs] of x's type, or float32 with out_dtype."""
+    out [rows, outs] of x's type, or float32 with out_dtype.  stream: where the call runs, the
+    current stream where None; what the call makes for itself is made there."""
     want(x.dim() == 2 and weight.dim() == 2 and scales.dim() == 2, "x, weight and scales must be matrices")
     rows, ins = x.shape
     outs, groups = scales.shape
@@ -45,7 +46,7 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
         zp = zeros.data_ptr()
     code = serve.dtype_code(x)
     if out is None:
-        out = serve.new_output(x, (rows, outs), (outs, 1), out_dtype or x.dtype)
+        out = serve.new_output(x, (rows, outs), (outs, 1), out_dtype or x.dtype, stream)
         os = outs
     else:
         want(out.shape == (rows, outs) and out.stride(1) == 1, "out must be [rows, outs], rows contiguous")
@@ -59,7 +60,7 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
     if rows > FEW_ROWS:
         if workspace is None:
             need = lib.arc_w4_workspace_bytes(w, rows)
-            workspace = serve.new_output(x, (need,), (1,), torch.uint8)
+            workspace = serve.new_workspace(x, need, False, stream)
         wp, wn = workspace.data_ptr(), workspace.numel()
     rc = lib.arc_w4_matvec(w, x.data_ptr(), rows, xs if rows > 1 else ins, code, out.data_ptr(), os,
                            serve.dtype_code(out, True), wp, wn, serve.stream_of(stream, dev))
