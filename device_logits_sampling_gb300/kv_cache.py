@@ -15,7 +15,7 @@ import struct
 import numpy as np
 import torch
 
-from . import sampler, serve
+from . import serve
 from .serve import want
 
 ARC_KV_ERR_PAGE = 0x1
@@ -175,9 +175,11 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
     T, dim, dev = k.shape[0], cache.head_dim, cache.index
     kt, kh, _ = _heads(k, T, cache.heads, dim, "k")
     vt, vh, _ = _heads(v, T, cache.heads, dim, "v")
-    dtype = k.dtype
+    dtype, code = k.dtype, serve.dtype_code(k)
     want(v.dtype == dtype, "k and v must have one type")
     want(k.get_device() == dev and v.get_device() == dev, "every tensor must be on the cache's device")
+    step = _step(cache, T, positions, page_table, row_offsets)
+    serve.on_current_gpu(dev)
     qp = op = qt = qh = ot = oh = heads = 0
     if q is not None:
         qt, qh, heads = _heads(q, T, None, dim, "q")
@@ -192,10 +194,9 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
         want(q_out is None, "q_out without q")
     if rope is not None:
         want(rope.turns.get_device() == dev, "every tensor must be on the cache's device")
-    rows = _ROWS.pack(qp, k.data_ptr(), v.data_ptr(), op, qt, qh, kt, kh, vt, vh, ot, oh, heads, serve.dtype_code(k))
-    rc = serve.load().arc_kv_append(cache._ref, _step(cache, T, positions, page_table, row_offsets), rows,
-                                    None if rope is None else rope._ref, sampler._ptr(err_word),
-                                    serve.stream_of(stream, dev))
+    rows = _ROWS.pack(qp, k.data_ptr(), v.data_ptr(), op, qt, qh, kt, kh, vt, vh, ot, oh, heads, code)
+    rc = serve.load().arc_kv_append(cache._ref, step, rows, None if rope is None else rope._ref,
+                                    serve.err_word_ptr(err_word, dev), serve.stream_of(stream, dev))
     serve.finish(rc, check)
     return q_out
 
@@ -211,20 +212,22 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
     workspace) is made there; tensors given have to be ready there."""
     T, dim, dev = q.shape[0], cache.head_dim, cache.index
     qt, qh, heads = _heads(q, T, None, dim, "q")
+    code = serve.dtype_code(q)
+    step = _step(cache, T, positions, page_table, row_offsets)
+    want(q.get_device() == dev, "every tensor must be on the cache's device")
+    serve.on_current_gpu(dev)
     if out is None:
         out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), q.dtype, stream)
         ot, oh = heads * dim, dim
     else:
         ot, oh, _ = _heads(out, T, heads, dim, "out")
-        want(out.dtype == q.dtype, "out must have q's type")
-    want(q.get_device() == dev and out.get_device() == dev, "every tensor must be on the cache's device")
-    code = serve.dtype_code(q)
+        want(out.dtype == q.dtype and out.get_device() == dev, "out must have q's type and device")
     if workspace is None:
         workspace = cache.attend_workspace(stream)
+    wp, wn = serve.workspace_of(workspace, dev)
     query = _QUERY.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, heads, code,
                         cache.default_scale if scale is None else scale, window)
-    rc = serve.load().arc_kv_attend(cache._ref, _step(cache, T, positions, page_table, row_offsets), query,
-                                    sampler._ptr(err_word), workspace.data_ptr(), workspace.numel(),
+    rc = serve.load().arc_kv_attend(cache._ref, step, query, serve.err_word_ptr(err_word, dev), wp, wn,
                                     serve.stream_of(stream, dev))
     serve.finish(rc, check)
     return out

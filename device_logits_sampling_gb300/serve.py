@@ -106,10 +106,15 @@ def dtype_code(t, f32: bool = False) -> int:
     raise TypeError(f"must be bfloat16 or float16{' or float32' if f32 else ''}, not {t.dtype}")
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def stream_of(stream, device: int) -> int:
     """The stream's handle; the device's current stream where None (torch.cuda.current_stream()
     builds a Stream object and resolves the device's name, 7 us of a 20 us call on the Arm host)."""
-    return int(stream.cuda_stream) if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    return _raw_stream(device) if _raw_stream is not None else int(torch.cuda.current_stream(device).cuda_stream)
 
 
 try:  # the allocation that compiled graphs of this torch make: 4 us a call less than torch.empty on the Arm host
@@ -149,6 +154,29 @@ def new_workspace(like, nbytes: int, zeroed: bool, stream=None):
     if not zeroed:
         return new_output(like, (nbytes,), (1,), torch.uint8)
     return make(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def on_current_gpu(device: int) -> None:
+    """Refuses host tensors (their device is -1) and those of a GPU that a launch would not go to."""
+    want(device >= 0, "every tensor must be a CUDA tensor")
+    want(torch._C._cuda_getDevice() == device, "every tensor must be on the current CUDA device")
+
+
+def err_word_ptr(err_word, device: int):
+    """Address of a 32-bit error word on the device, or None."""
+    if err_word is None:
+        return None
+    if err_word.dtype != torch.int32 and err_word.dtype != torch.uint32:
+        raise TypeError(f"err_word must be int32 or uint32, not {err_word.dtype}")
+    want(err_word.numel() >= 1 and err_word.get_device() == device, "err_word must be a word on the tensors' device")
+    return err_word.data_ptr()
+
+
+def workspace_of(workspace, device: int):
+    """(address, bytes) of a workspace on the device."""
+    want(workspace.get_device() == device and workspace.is_contiguous(),
+         "workspace must be contiguous, on the tensors' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def want(ok: bool, text: str) -> None:

@@ -45,15 +45,16 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
         want(zeros.get_device() == dev, "every tensor must be on x's device")
         zp = zeros.data_ptr()
     code = serve.dtype_code(x)
+    want(weight.get_device() == dev and scales.get_device() == dev, "every tensor must be on x's device")
+    serve.on_current_gpu(dev)
     if out is None:
         out = serve.new_output(x, (rows, outs), (outs, 1), out_dtype or x.dtype, stream)
         os = outs
     else:
         want(out.shape == (rows, outs) and out.stride(1) == 1, "out must be [rows, outs], rows contiguous")
         want(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+        want(out.get_device() == dev, "every tensor must be on x's device")
         os = out.stride(0) if rows > 1 else outs
-    want(weight.get_device() == dev and scales.get_device() == dev and out.get_device() == dev,
-         "every tensor must be on x's device")
     w = _WEIGHT.pack(weight.data_ptr(), scales.data_ptr(), zp, ws if outs > 1 else ins // 2, outs, ins, ins // groups)
     lib = serve.load()
     wp, wn = 0, 0
@@ -61,7 +62,7 @@ def matvec(x, weight, scales, zeros=None, out=None, out_dtype=None, workspace=No
         if workspace is None:
             need = lib.arc_w4_workspace_bytes(w, rows)
             workspace = serve.new_workspace(x, need, False, stream)
-        wp, wn = workspace.data_ptr(), workspace.numel()
+        wp, wn = serve.workspace_of(workspace, dev)
     rc = lib.arc_w4_matvec(w, x.data_ptr(), rows, xs if rows > 1 else ins, code, out.data_ptr(), os,
                            serve.dtype_code(out, True), wp, wn, serve.stream_of(stream, dev))
     serve.finish(rc, check)
