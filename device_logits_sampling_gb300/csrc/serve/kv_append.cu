@@ -356,12 +356,13 @@ __device__ __forceinline__ bool finish16(Sixteen& v) {
     return true;
 }
 
-// The exact value of element d of a key's head, turned.
+// The exact value of element d of a key's head, turned; NaN counts as 0.
 template <int DT>
 __device__ __noinline__ double exact_value(const AppendArgs& a, const char* head, int64_t pos, int d) {
     const typename Half<DT>::T* e = reinterpret_cast<const typename Half<DT>::T*>(head);
     const float x = Half<DT>::to_float(e[d]);
-    if (d >= a.rot) return x;
+    // (beside a pair that turns it is asked for such a value too, whose slack is the pair's)
+    if (d >= a.rot) return x != x ? 0.0 : x;
     const PairOf p = pair_of(d, a.rot, a.layout);
     const double y = turn64(static_cast<uint64_t>(pos) * __ldg(a.turns + p.pair), x,
                             p.sgn * Half<DT>::to_float(e[p.partner]), a.amp);
