@@ -374,16 +374,17 @@ template <int DT, int TURN, bool EXACT>
 __device__ __forceinline__ void put16(const AppendArgs& a, const Place& p, const char* head, int64_t pos, const Sixteen& v,
                                       int e, char* out) {
     const float inv = exp2i(-e);
-    // values that do not turn are exact, and often lie on a tie: no slack for them
-    const float rel = p.turns ? kTurnedErr * inv : 0.0f;
+    // values that do not turn are exact, and often lie on a tie: no slack for them (nor 0 times an infinity)
+    const float rel = kTurnedErr * inv;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         uint32_t lo[2], hi[2];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             const float* y = v.y + 8 * half + 4 * w;
-            if (EXACT) {
+            if (EXACT || !p.turns) {
                 lo[w] = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
+                hi[w] = lo[w];
             } else {
                 float l[4], h[4];
 #pragma unroll
