@@ -439,11 +439,52 @@ __device__ __forceinline__ bool may_be_largest(const Sixteen& v, int i, float lo
     return !(y + v.err < lo * (1.0f - 4.0f * kTurnedErr));
 }
 
-// Scale exponent of a page that keeps older tokens (`held`): what is stored is
-// a power of two; anything else (never written here) counts as its exponent.
-__device__ __forceinline__ int held_exponent(float scale) {
-    const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 0xFF) - 127;
-    return e < -kScaleExp ? -kScaleExp : (e > kScaleExp ? kScaleExp : e);
+// A page that keeps older tokens under a scale written here: 2^e with e in [-32, 32].
+__device__ __forceinline__ bool plain_scale(float was) {
+    const uint32_t b = __float_as_uint(was);
+    return (b & 0x7FFFFFu) == 0 && (b >> 23) - (127 - kScaleExp) <= 2 * kScaleExp;
+}
+__device__ __forceinline__ int held_exponent(float was) { return static_cast<int>(__float_as_uint(was) >> 23) - 127; }
+
+// Any other one, which another program wrote: the new tokens' slots of a page's head, all in fp64, by the threads
+// `unit` of `units`.  `need` is the least scale for the new tokens; the page's stays where it is as large. Out of
+// range: nothing is stored. One call apart from the rest: its registers cost the prompts 5 us where it was inline.
+struct Held {
+    const char* src;     // the first new token's values
+    char* base;          // the page's head
+    float* scale;
+    int64_t src_stride;  // bytes from token to token
+    int64_t pos;         // of the first new token
+    float was, need;
+    int slot, rows;      // first new slot, new tokens
+    int unit, units;
+    bool turns;
+};
+template <int DT>
+__device__ __noinline__ void store_held(const AppendArgs& a, const Held& h) {
+    if (!(h.was >= exp2i(-kScaleExp) && h.was <= exp2i(kScaleExp))) {
+        if (h.unit == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_SCALE);
+        return;
+    }
+    const int dim = a.c.head_dim;
+    const float now = h.need > h.was ? h.need : h.was;
+    if (now > h.was) {
+        const double f = static_cast<double>(h.was) / static_cast<double>(now);  // exact: now is a power of two
+        for (int i = h.unit; i < h.slot * dim; i += h.units) {
+            uint32_t x, unused;
+            e4m3x4_to_half2(static_cast<uint8_t>(h.base[i]), x, unused);
+            const double y = static_cast<double>(__half2float(__ushort_as_half(static_cast<unsigned short>(x))));
+            h.base[i] = static_cast<char>(e4m3_of_double(y * f));  // a code times a scale: 28 bits
+        }
+        if (h.unit == 0) *h.scale = now;
+    }
+    for (int i = h.unit; i < h.rows * dim; i += h.units) {
+        const int r = i / dim, d = i - r * dim;
+        const char* const head = h.src + r * h.src_stride;
+        const float x = Half<DT>::to_float(reinterpret_cast<const typename Half<DT>::T*>(head)[d]);
+        const double y = h.turns ? exact_value<DT>(a, head, h.pos + r, d) : (x != x ? 0.0 : static_cast<double>(x));
+        h.base[h.slot * dim + i] = static_cast<char>(e4m3_of_double(y / static_cast<double>(now)));
+    }
 }
 
 // One new token of a (sequence, head, key or value): head_dim / 16 lanes.
@@ -520,6 +561,11 @@ __device__ __forceinline__ void store_single(const AppendArgs& a) {
         if (unsure) e = scale_exponent(__double2float_ru(y));
     }
     __syncwarp();  // every lane has read the scale
+    if (on && slot > 0 && !plain_scale(was)) {
+        char* base = static_cast<char*>(is_v ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
+        store_held<DT>(a, Held{head, base, scale, 0, pos, was, exp2i(e), slot, 1, j, L, !is_v});
+        on = false;
+    }
     if (on) {
         char* base = static_cast<char*>(is_v ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
         if (slot > 0) {
@@ -703,6 +749,10 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
             e = scale_exponent(__double2float_ru(y));
         }
         char* base = static_cast<char*>(V ? a.c.v : a.c.k) + page * a.c.page_stride + h * a.c.head_stride;
+        if (slot0 > 0 && !plain_scale(was)) {  // the same in every thread
+            store_held<DT>(a, Held{src, base, scales + h, ts * 2, page0 + slot0, was, exp2i(e), slot0, rows, tid, kThreads, !V});
+            continue;
+        }
         if (slot0 > 0) {
             const int old = held_exponent(was);
             if (e > old) {

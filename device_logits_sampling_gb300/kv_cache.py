@@ -22,6 +22,7 @@ ARC_KV_ERR_PAGE = 0x1
 ARC_KV_ERR_POSITION = 0x2
 ARC_KV_ERR_NAN = 0x4
 ARC_KV_ERR_OFFSETS = 0x8
+ARC_KV_ERR_SCALE = 0x10
 E4M3_MAX = 448.0
 SCALE_EXP = 32  # page scales written by append lie in [2^-32, 2^32]
 LAYOUTS = {"half": 0, "interleaved": 1}

@@ -45,6 +45,8 @@ extern "C" {
                                     sequence are NaN */
 #define ARC_KV_ERR_NAN 0x4u      /* a rotated key or a value is NaN: stored as 0 */
 #define ARC_KV_ERR_OFFSETS 0x8u  /* row_offsets does not ascend from 0 to T: the sequence is left out */
+#define ARC_KV_ERR_SCALE 0x10u   /* a page that holds older tokens has a scale outside [2^-32, 2^32]: the new ones
+                                    are not stored under that head, and the page stays as it is */
 
 /* Host struct.  k and v have the same layout. */
 typedef struct arc_kv_cache {
@@ -105,8 +107,10 @@ typedef struct arc_rope {
  *   rope     NULL: no rotation
  * A page's scale becomes the least 2^e with amax <= 448 * 2^e over its new
  * tokens, e clamped to [-32, 32], or stays where the page already holds tokens
- * and its scale is larger.  Where it grows, the tokens held are rewritten as
- * e4m3(code * 2^(old e - new e)); a NaN code stays one.  A page whose first token is new starts from
+ * and its scale is as large. A scale that stays may be any number of the range
+ * (pages that another program filled): the new codes are the nearest ones under
+ * it, and the older ones stay. Where it grows, the tokens held are rewritten as
+ * e4m3(code * old scale / new scale); a NaN code stays one.  A page whose first token is new starts from
  * nothing: what it held before does not matter.  Infinities and values above
  * 448 * 2^32 saturate.  Pages are written by this call alone: sequences of one
  * call must not share a page that they append to.

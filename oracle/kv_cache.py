@@ -8,7 +8,7 @@ import numpy as np
 
 E4M3_MAX = 448.0
 SCALE_EXP = 32
-ERR_PAGE, ERR_POSITION, ERR_NAN = 1, 2, 4
+ERR_PAGE, ERR_POSITION, ERR_NAN, ERR_SCALE = 1, 2, 4, 16
 
 
 def decode_table() -> np.ndarray:
@@ -91,16 +91,19 @@ def append(k, v, k_scale, v_scale, new_k, new_v, positions, table, offsets, turn
                         if np.isnan(x).any():
                             err |= ERR_NAN
                             x = np.where(np.isnan(x), 0.0, x)
-                        e = scale_exponent(float(np.abs(x).max()))
+                        now = 2.0 ** scale_exponent(float(np.abs(x).max()))
                         if slot:
-                            old = int(round(math.log2(scale[p, h])))
-                            if e > old:
+                            old = float(scale[p, h])
+                            if not 2.0 ** -SCALE_EXP <= old <= 2.0 ** SCALE_EXP:
+                                err |= ERR_SCALE
+                                continue
+                            if now > old:
                                 was = codes[p, h, :slot].copy()  # a NaN code stays one (without its sign)
-                                again = encode(TABLE[was] * 2.0 ** (old - e))
+                                again = encode(TABLE[was] * (old / now))
                                 codes[p, h, :slot] = np.where((was & 0x7F) == 0x7F, 0x7F, again)
-                            e = max(e, old)
-                        scale[p, h] = 2.0 ** e
-                        codes[p, h, slot:slot + take] = encode(x * 2.0 ** -e)
+                            now = max(now, old)
+                        scale[p, h] = now
+                        codes[p, h, slot:slot + take] = encode(x / now)
             at, row = at + take, row + take
     return err
 
