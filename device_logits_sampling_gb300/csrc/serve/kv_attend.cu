@@ -21,21 +21,27 @@
 // e4m3 codes become fp16 pairs by one conversion each, and the two scales
 // enter outside the products.
 //
-// Softmax.  Value scales differ from page to page.  With the value scale
-// 2^ev * vm, the running maximum is that of s + ev (log2 units): weights
-// p' = 2^(s + ev - m) are at most 1 and small only where their product with
-// the values is, so their fp16 form loses nothing that counts; the sum of the
-// true weights is sum p' 2^-ev, in the same reference.
+// Softmax.  A step's weights are taken relative to the step's own largest score
+// of the row, times 2^14, as fp16: half a step of fp16 off where they are
+// within 2^-28 of that, and lost below 2^-39 of it, whatever other steps and
+// their value scales are.  The step's product with the values goes into the
+// running fp32 sums with one factor a row: the page's value scale times
+// 2^(step's largest - running largest).  (For heads of 64 a step's halves, which
+// may lie in two pages, are told apart in all of this.)  Measured and replaced:
+// weights relative to the running maximum of score plus scale exponent, at most
+// 1 and summed up across steps by the matrix instruction, lost what lay below
+// 2^-25 of the largest, which a page of a far larger scale made of all others.
 //
-// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 277 us,
-// 6.7 TB/s, 98% of the measured copy rate: the 12 warps of an SM need 2,000
-// clocks a step, which is what memory gives them 4 KB in.  One sequence of
-// 200,003: 73 us (83%); 256 of 1 to 4,096: 64 us (68%): the line's ends, about
-// 12,000 clocks to the first step and as many for the joins.  Short calls are
-// those: 14 us.  48 sequences of 1 to 5 drafted tokens, heads of 64, a window:
-// 35 us.  Measured and left: a block for each (sequence, head) and one
-// token at a time a warp (157 ms for the 200,003), more warps with fewer
-// registers and stages (95 us for it), joins row by row in every thread (84 us).
+// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 288 us,
+// 6.4 TB/s, 95% of the measured copy rate (278 us, 98%, with the products summed
+// up by the matrix instruction): the 12 warps of an SM need some 2,000 clocks a
+// step, about what memory gives them 4 KB in.  One sequence of 200,003: 75 us
+// (80%); 256 of 1 to 4,096: 66 us (66%): the line's ends, about 12,000 clocks to
+// the first step and as many for the joins.  Short calls are those: 14 us.  48
+// sequences of 1 to 5 drafted tokens, heads of 64, a window: 36 us.  Measured and
+// left: a block for each (sequence, head) and one token at a time a warp (157 ms
+// for the 200,003), more warps with fewer registers and stages (95 us for it),
+// joins row by row in every thread (84 us).
 #include <atomic>
 
 #include "kv_host.cuh"
@@ -50,6 +56,7 @@ constexpr int kMaxBlocks = 256;  // blocks of a launch: at most one for each SM
 constexpr float kNothing = -3.0e38f;  // maximum of no score: finite, so that differences need no special case
 constexpr int kItemCost = 3;     // an item's fixed cost in steps (query load, output store), for the cut (256 ragged
                                  // sequences: 81 us with 1, 67 with 2, 63.5 with 3, 64 with 4)
+constexpr float kLift = 16384.0f;  // of the weights as fp16: 2^14 of its 2^15.99
 constexpr int kStatusBytes = kMaxBlocks * 4;
 
 struct AttendArgs {
@@ -145,6 +152,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The product alone.
+__device__ __forceinline__ void mma16816_only(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -427,7 +441,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                             copy4(static_cast<uint32_t>(__cvta_generic_to_shared(&sm.scales[warp][issued][hv][lane])),
                                   (lane ? v_scale : k_scale) + static_cast<int64_t>(page) * a.c.heads);
                     } else if (lane < 2) {
-                        sm.scales[warp][issued][hv][lane] = none ? 1.0f : __int_as_float(0x7FC00000);
+                        // (a bad page spoils the rows that see its tokens, through their scores)
+                        sm.scales[warp][issued][hv][lane] = none || lane ? 1.0f : __int_as_float(0x7FC00000);
                     }
                 }
                 ++step;
@@ -520,12 +535,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 __syncwarp();  // every lane's copies are in, and every lane is done with the stage before
                 issue();
                 const uint8_t* const st = dyn + warp * S::kPerWarp + stage * S::kStage;
-                float ks[HV];
-                uint32_t vb[HV];
+                float ks[HV], vs[HV];
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
                     ks[hv] = sm.scales[warp][stage][hv][0];
-                    vb[hv] = __float_as_uint(sm.scales[warp][stage][hv][1]);
+                    vs[hv] = sm.scales[warp][stage][hv][1];
                 }
                 stage = stage + 1 == ST ? 0 : stage + 1;
                 const int tok0 = (at.q.step0 + u - kItemCost) << TS;
@@ -555,45 +569,48 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                     }
                 }
                 const bool edge = tok0 + 16 * HV - 1 > hi_first || (a.q.window > 0 && tok0 <= hi_last - a.q.window);
-                float top[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = kNothing;
+                float top[HV][NT][2];  // each row's largest score of the half
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
-                    const float ev = static_cast<float>(static_cast<int>((vb[hv] >> 23) & 0xFF) - 127);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            s[hv][nt][e] = fmaf(s[hv][nt][e], ks[hv] * rf[nt][e & 1], ev);
+                            s[hv][nt][e] *= ks[hv] * rf[nt][e & 1];
                             if (edge) {
                                 const int tok = tok0 + 16 * hv + g + (e >> 1) * 8, h = hi[nt][e & 1];
                                 if (tok > h || (a.q.window > 0 && tok <= h - a.q.window)) s[hv][nt][e] = -INFINITY;
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[hv][nt][e], s[hv][nt][e + 2]));
+                        for (int e = 0; e < 2; ++e) top[hv][nt][e] = fmaxf(kNothing, fmaxf(s[hv][nt][e], s[hv][nt][e + 2]));
                     }
                 }
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int hv = 0; hv < HV; ++hv)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[nt][e], x));
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                top[hv][nt][e] = fmaxf(top[hv][nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[hv][nt][e], x));
                 bool up = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int hv = 0; hv < HV; ++hv)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) up = up || top[nt][e] > m[nt][e];
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) up = up || top[hv][nt][e] > m[nt][e];
                 if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float f[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float mn = fmaxf(m[nt][e], top[nt][e]);
+                            float mn = m[nt][e];
+#pragma unroll
+                            for (int hv = 0; hv < HV; ++hv) mn = fmaxf(mn, top[hv][nt][e]);
                             f[e] = ex2(m[nt][e] - mn);
                             m[nt][e] = mn;
                             l[nt][e] *= f[e];
@@ -607,20 +624,24 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
                     const uint8_t* vst = st + hv * S::kHalf + 16 * D;
-                    const float vm = __uint_as_float((vb[hv] & 0x7FFFFFu) | 0x3F800000u);
-                    const float vi = __uint_as_float((254u - ((vb[hv] >> 23) & 0xFF)) << 23);
                     uint32_t pf[NT][2];
+                    float fv[NT][2];  // what the half's products count in the running sums
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float p[4];
+                        float p[4], f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            f[e] = ex2(top[hv][nt][e] - m[nt][e]);
+                            fv[nt][e] = f[e] * (vs[hv] * (1.0f / kLift));
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            p[e] = ex2(s[hv][nt][e] - m[nt][e & 1]);
-                            l[nt][e & 1] = fmaf(p[e], vi, l[nt][e & 1]);
+                            p[e] = ex2(s[hv][nt][e] - top[hv][nt][e & 1]);
+                            l[nt][e & 1] = fmaf(p[e], f[e & 1], l[nt][e & 1]);
                         }
                         // token-major to row-major: what the products take
-                        pf[nt][0] = transpose8x8(pack_f16(p[0] * vm, p[1] * vm));
-                        pf[nt][1] = transpose8x8(pack_f16(p[2] * vm, p[3] * vm));
+                        pf[nt][0] = transpose8x8(pack_f16(p[0] * kLift, p[1] * kLift));
+                        pf[nt][1] = transpose8x8(pack_f16(p[2] * kLift, p[3] * kLift));
                     }
 
                     // values: tokens 2t, 2t+1, 2t+8, 2t+9, D / 8 bytes from g * D / 8
@@ -691,7 +712,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                         e4m3x4_to_half2(x, a0, a1);
                         e4m3x4_to_half2(y, a2, a3);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float d[4];
+                            mma16816_only(d, a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[nt][i][e] = fmaf(d[e], fv[nt][e & 1], o[nt][i][e]);
+                        }
                     }
                 }
             }

@@ -139,7 +139,9 @@ int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
  *     out = sum_j softmax_j(scale * q . k_j) v_j
  * Scores, the softmax's maximum and sum and the sums over j are fp32; q enters
  * the products as fp16 after a power-of-two scaling of each row (exact but for
- * values below 2^-24 of the row's largest), the weights as fp16.
+ * values below 2^-24 of the row's largest), the weights as fp16 too, relative to
+ * the largest of the 16 tokens they are multiplied with: off by 2^-11 of
+ * themselves at most, 0 below 2^-39 of that one.
  *   out        device, dtype; rows of parked sequences are 0
  *   workspace  device, 16-byte aligned, arc_kv_attend_workspace_bytes(cache)
  *              bytes, zero-filled once before its first use; calls leave it
