@@ -26,8 +26,8 @@
 // within 2^-28 of that, and lost below 2^-39 of it, whatever other steps and
 // their value scales are.  The step's product with the values goes into the
 // running fp32 sums with one factor a row: the page's value scale times
-// 2^(step's largest - running largest).  (For heads of 64 a step's halves, which
-// may lie in two pages, are told apart in all of this.)  Measured and replaced:
+// 2^(step's largest - running largest); for heads of 64 a factor a half, which
+// may lie in two pages.  Measured and replaced:
 // weights relative to the running maximum of score plus scale exponent, at most
 // 1 and summed up across steps by the matrix instruction, lost what lay below
 // 2^-25 of the largest, which a page of a far larger scale made of all others.
@@ -569,7 +569,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                     }
                 }
                 const bool edge = tok0 + 16 * HV - 1 > hi_first || (a.q.window > 0 && tok0 <= hi_last - a.q.window);
-                float top[HV][NT][2];  // each row's largest score of the half
+                float top[NT][2];  // each row's largest score of the step
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = kNothing;
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
 #pragma unroll
@@ -583,34 +585,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) top[hv][nt][e] = fmaxf(kNothing, fmaxf(s[hv][nt][e], s[hv][nt][e + 2]));
+                        for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[hv][nt][e], s[hv][nt][e + 2]));
                     }
                 }
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
-                    for (int hv = 0; hv < HV; ++hv)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                top[hv][nt][e] = fmaxf(top[hv][nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[hv][nt][e], x));
-                bool up = false;
-#pragma unroll
-                for (int hv = 0; hv < HV; ++hv)
-#pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) up = up || top[hv][nt][e] > m[nt][e];
+                        for (int e = 0; e < 2; ++e)
+                            top[nt][e] = fmaxf(top[nt][e], __shfl_xor_sync(0xFFFFFFFFu, top[nt][e], x));
+                bool up = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) up = up || top[nt][e] > m[nt][e];
                 if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float f[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float mn = m[nt][e];
-#pragma unroll
-                            for (int hv = 0; hv < HV; ++hv) mn = fmaxf(mn, top[hv][nt][e]);
+                            const float mn = fmaxf(m[nt][e], top[nt][e]);
                             f[e] = ex2(m[nt][e] - mn);
                             m[nt][e] = mn;
                             l[nt][e] *= f[e];
@@ -621,23 +617,25 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                             for (int e = 0; e < 4; ++e) o[nt][i][e] *= f[e & 1];
                     }
                 }
+                float f[NT][2];  // what the step's weights count in the running sums
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) f[nt][e] = ex2(top[nt][e] - m[nt][e]);
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
                     const uint8_t* vst = st + hv * S::kHalf + 16 * D;
                     uint32_t pf[NT][2];
-                    float fv[NT][2];  // what the half's products count in the running sums
+                    float fv[NT][2];  // and its products, half by half
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float p[4], f[2];
+                        float p[4];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            f[e] = ex2(top[hv][nt][e] - m[nt][e]);
-                            fv[nt][e] = f[e] * (vs[hv] * (1.0f / kLift));
-                        }
+                        for (int e = 0; e < 2; ++e) fv[nt][e] = f[nt][e] * (vs[hv] * (1.0f / kLift));
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            p[e] = ex2(s[hv][nt][e] - top[hv][nt][e & 1]);
-                            l[nt][e & 1] = fmaf(p[e], f[e & 1], l[nt][e & 1]);
+                            p[e] = ex2(s[hv][nt][e] - top[nt][e & 1]);
+                            l[nt][e & 1] = fmaf(p[e], f[nt][e & 1], l[nt][e & 1]);
                         }
                         // token-major to row-major: what the products take
                         pf[nt][0] = transpose8x8(pack_f16(p[0] * kLift, p[1] * kLift));

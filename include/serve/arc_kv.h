@@ -140,8 +140,8 @@ int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
  * Scores, the softmax's maximum and sum and the sums over j are fp32; q enters
  * the products as fp16 after a power-of-two scaling of each row (exact but for
  * values below 2^-24 of the row's largest), the weights as fp16 too, relative to
- * the largest of the 16 tokens they are multiplied with: off by 2^-11 of
- * themselves at most, 0 below 2^-39 of that one.
+ * the largest of the 16 tokens (32 for heads of 64) they are multiplied with: off
+ * by 2^-11 of themselves at most above 2^-28 of that one, 0 below 2^-39.
  *   out        device, dtype; rows of parked sequences are 0
  *   workspace  device, 16-byte aligned, arc_kv_attend_workspace_bytes(cache)
  *              bytes, zero-filled once before its first use; calls leave it

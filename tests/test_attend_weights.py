@@ -2,8 +2,8 @@
 sequences whose weights are all alike, so that every piece of the line and every join counts.
 
 Tolerance: half a step of the output's type, and (2^-11 + 2^-12) sum p |v| (half a step of a weight as fp16, and
-the fp32 scores). There is no absolute term: it holds where the scores of a step of 16 tokens, one page's, lie
-within 28 powers of two of the step's largest, which each case asserts."""
+the fp32 scores). There is no absolute term: it holds where the scores of a step of 16 tokens (32 for heads of 64)
+lie within 28 powers of two of the step's largest, which each case asserts."""
 import math
 
 import numpy as np
@@ -58,7 +58,8 @@ class Cache:
                     lo = max(0, p + 1 - window) if window else 0
                     r, heads = int(self.offsets[b]) + i, slice(h * (self.q_heads // self.heads), (h + 1) * (self.q_heads // self.heads))
                     s = q[r, heads] @ kk[lo:p + 1].T * self.dim ** -0.5
-                    steps = [s[:, j:j + 16] / math.log(2.0) for j in range(0, s.shape[1], 16)]
+                    step = 32 if self.dim == 64 else 16
+                    steps = [s[:, j:j + step] / math.log(2.0) for j in range(0, s.shape[1], step)]
                     assert max(float((x.max(1) - x.min(1)).max()) for x in steps) <= span
                     w = np.exp(s - s.max(1, keepdims=True))
                     w /= w.sum(1, keepdims=True)
