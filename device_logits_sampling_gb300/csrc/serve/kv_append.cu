@@ -25,6 +25,7 @@
 // at three blocks an SM (85 us).
 #include <cstring>
 
+#include "kv_device.cuh"
 #include "kv_host.cuh"
 #include "serve_util.cuh"
 
@@ -227,10 +228,10 @@ __device__ __forceinline__ float turn16(const AppendArgs& a, const Place& p, con
     return most * (kRotErr * a.amp);
 }
 
-// The sequence of row t: the last b with row_offsets[b] <= t.
-__device__ __forceinline__ int64_t sequence_of(const arc_kv_step& s, int64_t t) {
+// The sequence of row t: the last b of `sound` with row_offsets[b] <= t.
+__device__ __forceinline__ int64_t sequence_of(const arc_kv_step& s, int64_t sound, int64_t t) {
     if (s.row_offsets == nullptr) return t;
-    int64_t lo = 0, hi = s.B - 1;
+    int64_t lo = 0, hi = sound - 1;
     while (lo < hi) {
         const int64_t m = (lo + hi + 1) >> 1;
         if (__ldg(s.row_offsets + m) <= t)
@@ -241,21 +242,15 @@ __device__ __forceinline__ int64_t sequence_of(const arc_kv_step& s, int64_t t) 
     return lo;
 }
 
-// Rows of sequence b: first and count; a bad pair of offsets counts as none.
-__device__ __forceinline__ bool rows_of(const arc_kv_step& s, int64_t b, int64_t& first, int64_t& n) {
-    if (s.row_offsets == nullptr) {
-        first = b;
-        n = 1;
-        return true;
+// The place's values of a row that no sequence has: NaN.
+template <int DT>
+__device__ __noinline__ void blank_queries(const AppendArgs& a, const Place& p, int64_t t, int set) {
+    for (int h = set; h < a.r.q_heads; h += a.head_sets) {
+        typename Half<DT>::T* const to =
+            static_cast<typename Half<DT>::T*>(a.r.q_out) + t * a.r.out_token_stride + h * a.r.out_head_stride;
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) to[p.d[i >> 3] + (i & 7)] = Half<DT>::from_float(__uint_as_float(0x7FC00000u));
     }
-    const int64_t lo = __ldg(s.row_offsets + b), hi = __ldg(s.row_offsets + b + 1);
-    first = lo;
-    n = hi - lo;
-    if (lo < 0 || hi < lo || hi > s.T || (b == 0 && lo != 0) || (b == s.B - 1 && hi != s.T)) {
-        n = 0;
-        return false;
-    }
-    return true;
 }
 
 // A thread owns sixteen values of a token's heads set, set + sets, ...: the
@@ -271,16 +266,22 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& a) {
     const int64_t t = g / a.head_sets;
     bool on = t < a.s.T;
     int64_t pos = 0;
-    if (on) {
-        const int64_t b = sequence_of(a.s, t);
-        int64_t first, n;
-        if (!rows_of(a.s, b, first, n) || t < first || t >= first + n) {
-            if (a.err) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
-            on = false;
-        } else {
-            const int at = __ldg(a.s.positions + b);
-            pos = at < 0 ? -1 : at + (t - first);
+    int64_t sound = a.s.B;
+    if (a.s.row_offsets != nullptr) {
+        sound = sound_sequences(a.s);
+        if (sound < a.s.B) {
+            if (threadIdx.x == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
+            if (on && t >= unclaimed_rows(a.s, sound)) {
+                blank_queries<DT>(a, p, t, set);
+                on = false;
+            }
         }
+    }
+    if (on) {
+        const int64_t b = sequence_of(a.s, sound, t);
+        const int64_t first = a.s.row_offsets == nullptr ? b : static_cast<int64_t>(__ldg(a.s.row_offsets + b));
+        const int at = __ldg(a.s.positions + b);
+        pos = at < 0 ? -1 : at + (t - first);
     }
     Turns turns;
     turns_of<TURN>(a, p, pos, turns);
@@ -605,10 +606,11 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ps = a.c.page_size;
     // pages touched by sequence b; the running total finds this block's
+    bool wrong = false;
     auto touched = [&](int64_t b) -> int64_t {
         int64_t first, n;
         if (!rows_of(a.s, b, first, n)) {
-            if (a.err) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
+            wrong = true;
             return 0;
         }
         const int64_t p = __ldg(a.s.positions + b);
@@ -619,13 +621,22 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
     int64_t before = 0;
     for (int64_t b0 = 0; b0 < a.s.B; b0 += kThreads) {
         const int64_t b = b0 + tid;
-        const int64_t mine = b < a.s.B ? touched(b) : 0;
-        int64_t incl = mine;
-        for (int m = 1; m < 32; m <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-            if (lane >= m) incl += o;
+        int64_t mine = b < a.s.B ? touched(b) : 0;
+        auto sums = [&]() {
+            int64_t incl = mine;
+            for (int m = 1; m < 32; m <<= 1) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+                if (lane >= m) incl += o;
+            }
+            return incl;
+        };
+        int64_t incl = sums();
+        const bool stop = __syncthreads_or(wrong);
+        if (stop) {  // the line ends before the first wrong pair of offsets
+            if (tid == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
+            if (b >= sound_sequences(a.s)) mine = 0;
+            incl = sums();
         }
-        __syncthreads();
         if (lane == 31) wsum[warp] = incl;
         __syncthreads();
         int64_t off = before, total = 0;
@@ -639,7 +650,7 @@ __device__ __forceinline__ void store_pages(const AppendArgs& a, int64_t want, i
             found[1] = want - lo;
         }
         before += total;
-        if (before > want) break;
+        if (before > want || stop) break;
     }
     __syncthreads();
     const int64_t b = found[0];
@@ -910,7 +921,8 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
         // a sequence with n tokens touches at most n / page_size + 2 pages, and at most n
         const int64_t seqs = step->B < step->T ? step->B : step->T;
         const int64_t most = step->T / cache->page_size + 2 * seqs;
-        const int64_t pages = most < step->T ? most : step->T;
+        // (and a block more, which finds no page and so sees all offsets)
+        const int64_t pages = (most < step->T ? most : step->T) + 1;
         // many pages: a block stores several heads with one set of angles (prompts of 10,476 tokens: 69 us with four
         // heads, 73 with two, 84 with one)
         while (a.page_heads < 4 && a.page_heads < cache->heads && pages * cache->heads / a.page_heads > 512) a.page_heads *= 2;

@@ -44,6 +44,7 @@
 // joins row by row in every thread (84 us).
 #include <atomic>
 
+#include "kv_device.cuh"
 #include "kv_host.cuh"
 #include "launch_util.cuh"
 #include "serve_util.cuh"
@@ -204,22 +205,13 @@ struct Seq {
 template <int R, int TS>
 __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int64_t b) {
     Seq q;
-    q.bad = q.late = false;
+    q.late = false;
     q.cost = 0;
     q.tiles = 0;
     q.step0 = 0;
     q.pos = __ldg(a.s.positions + b);
-    int64_t n = 1;
-    q.first = b;
-    if (a.s.row_offsets != nullptr) {
-        const int64_t lo = __ldg(a.s.row_offsets + b), hi = __ldg(a.s.row_offsets + b + 1);
-        q.first = lo;
-        n = hi - lo;
-        if (lo < 0 || hi < lo || hi > a.s.T || (b == 0 && lo != 0) || (b == a.s.B - 1 && hi != a.s.T)) {
-            q.bad = true;
-            n = 0;
-        }
-    }
+    int64_t n;
+    q.bad = !rows_of(a.s, b, q.first, n);
     q.n = static_cast<int32_t>(n);
     if (n == 0 || q.pos < 0) return q;
     if (q.pos + n > int64_t{a.s.max_pages} * a.c.page_size) {
@@ -263,6 +255,19 @@ struct Cursor {
     }
 };
 
+// Offsets that do not ascend: the sequences before the first wrong pair; the rows from there on, which are nobody's,
+// become NaN. Called by whole blocks.
+__device__ __forceinline__ int64_t wrong_offsets(const AttendArgs& a) {
+    const int64_t sound = sound_sequences(a.s), row0 = unclaimed_rows(a.s, sound);
+    const int64_t dim = a.c.head_dim, per_row = a.q.q_heads * dim, vals = (a.s.T - row0) * per_row;
+    const int64_t step = int64_t{gridDim.x} * blockDim.x;
+    for (int64_t i = int64_t{blockIdx.x} * blockDim.x + threadIdx.x; i < vals; i += step)
+        static_cast<uint16_t*>(a.q.out)[(row0 + i / per_row) * a.q.out_token_stride + i % per_row / dim * a.q.out_head_stride +
+                                        i % dim] = a.bf16 ? 0x7FC0u : 0x7E00u;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.err) atomicOr(a.err, ARC_KV_ERR_OFFSETS);
+    return sound;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
     using S = Smem<D, NT>;
@@ -278,24 +283,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
 
     // ---- the line: units before each thread's run of sequences
     const int64_t run = (a.s.B + kThreads - 1) / kThreads;
-    int64_t mine = 0;
-    uint32_t seen = 0;
-    for (int64_t b = run * tid; b < run * (tid + 1) && b < a.s.B; ++b) {
-        const Seq q = load_seq<R, TS>(a, b);
-        mine += units_of(a, q);
-        if (q.bad) seen |= ARC_KV_ERR_OFFSETS;
-        if (q.late) seen |= ARC_KV_ERR_POSITION;
+    int64_t mine, incl;
+    uint32_t seen;
+    int64_t sound = a.s.B;
+    for (;; sound = wrong_offsets(a)) {  // (twice where offsets are wrong)
+        mine = 0;
+        seen = 0;
+        for (int64_t b = run * tid; b < run * (tid + 1) && b < sound; ++b) {
+            const Seq q = load_seq<R, TS>(a, b);
+            mine += units_of(a, q);
+            if (q.bad) seen |= ARC_KV_ERR_OFFSETS;
+            if (q.late) seen |= ARC_KV_ERR_POSITION;
+        }
+        incl = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+            if (lane >= m) incl += o;
+        }
+        if (lane == 31) sm.wsum[warp] = incl;
+        if (tid < 2 * W) sm.part[tid].from = -1;
+        if (!__syncthreads_or(seen & ARC_KV_ERR_OFFSETS)) break;
     }
     if (seen && a.err && blockIdx.x == 0) atomicOr(a.err, seen);
-    int64_t incl = mine;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-        if (lane >= m) incl += o;
-    }
-    if (lane == 31) sm.wsum[warp] = incl;
-    if (tid < 2 * W) sm.part[tid].from = -1;
-    __syncthreads();
     int64_t off = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -307,7 +317,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     if (tid == 0) sm.before[kThreads] = total;
 
     // rows without work: parked sequences give 0, those past their page table NaN
-    for (int64_t b = blockIdx.x; b < a.s.B; b += gridDim.x) {
+    for (int64_t b = blockIdx.x; b < sound; b += gridDim.x) {
         const Seq q = load_seq<R, TS>(a, b);
         if (q.cost != 0 || q.n == 0) continue;
         const uint32_t fill = q.late ? (a.bf16 ? 0x7FC0u : 0x7E00u) : 0u;

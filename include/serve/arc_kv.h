@@ -12,7 +12,8 @@
  * device pointers, sizes and a stream; the host arguments are checked before
  * any CUDA call and a negative ARC_E_* code means that nothing was enqueued;
  * nothing is allocated and nothing synchronises; what is found wrong on the
- * device becomes sticky bits in *err_word and leaves the other sequences alone.
+ * device becomes sticky bits in *err_word and leaves the other sequences alone
+ * (but for offsets: where one is wrong, those after it say nothing either).
  * Calls are safe inside stream capture once the first call of their kind on
  * the device has returned (it sets kernel attributes).
  *
@@ -44,7 +45,9 @@ extern "C" {
 #define ARC_KV_ERR_POSITION 0x2u /* tokens past max_pages * page_size: not stored; attention rows of the
                                     sequence are NaN */
 #define ARC_KV_ERR_NAN 0x4u      /* a rotated key or a value is NaN: stored as 0 */
-#define ARC_KV_ERR_OFFSETS 0x8u  /* row_offsets does not ascend from 0 to T: the sequence is left out */
+#define ARC_KV_ERR_OFFSETS 0x8u  /* row_offsets does not ascend from 0 to T: the first sequence where it does not, and
+                                    those after it, are left out; their tokens are not stored, and the rows that
+                                    no sequence before them has are NaN in q_out and in the attention */
 #define ARC_KV_ERR_SCALE 0x10u   /* a page that holds older tokens has a scale outside [2^-32, 2^32]: the new ones
                                     are not stored under that head, and the page stays as it is */
 
