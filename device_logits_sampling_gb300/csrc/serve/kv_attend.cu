@@ -988,6 +988,8 @@ int arc_kv_attend(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
     if (query == nullptr || query->q == nullptr || query->out == nullptr) return ARC_E_NULL;
     if (query->dtype != ARC_BF16 && query->dtype != ARC_F16) return ARC_E_DTYPE;
     if (query->q_heads <= 0 || query->q_heads > (1 << 16) || query->q_heads % cache->heads != 0) return ARC_E_SHAPE;
+    // rows of a (sequence, cached head) are counted in 32 bits
+    if (step->T * (query->q_heads / cache->heads) > (int64_t{1} << 30)) return ARC_E_SHAPE;
     if (query->window < 0 || !(query->scale >= -3.0e38f && query->scale <= 3.0e38f)) return ARC_E_OPTION;
     if (!aligned(query->q, 2) || !aligned(query->out, 2) || !aligned(err_word, 4)) return ARC_E_ALIGN;
     if (workspace == nullptr || workspace_bytes < arc_kv_attend_workspace_bytes(cache)) return ARC_E_WORKSPACE;

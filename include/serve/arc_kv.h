@@ -155,7 +155,7 @@ typedef struct arc_kv_query {
     void* out;
     int64_t q_token_stride, q_head_stride;
     int64_t out_token_stride, out_head_stride;
-    int32_t q_heads;  /* a multiple of cache->heads */
+    int32_t q_heads;  /* a multiple of cache->heads; T * q_heads / heads <= 2^30 */
     int32_t dtype;    /* ARC_BF16 or ARC_F16 */
     float scale;      /* finite */
     int32_t window;   /* 0: off */
