@@ -81,6 +81,7 @@ struct Bars {
     uint64_t a_full[4], a_empty[4];
     uint64_t x_full[4], x_empty[4];
     uint64_t s_full[4], s_empty[4];
+    uint64_t drained;  // the products issued before a wait ran out
     uint32_t tmem;
     uint32_t failed;
     float back[256];  // each row of x's factor
@@ -244,9 +245,9 @@ __device__ __forceinline__ void store_sums(const ManyArgs& a, const float* back,
 }
 
 // The products of all items, by one thread: for each block of 128 inner values
-// its groups, each into the next slot of the ring of sums.
+// its groups, each into the next slot of the ring of sums. False where a wait ran out.
 template <int N, int H, int G>
-__device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint32_t tmem, uint32_t tmem_a, int first, int step,
+__device__ __forceinline__ bool issue_products(Bars& bars, uint32_t x_ring, uint32_t tmem, uint32_t tmem_a, int first, int step,
                                                int items, int nb) {
     using M = Many<N, H>;
     constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (8u << 24);
@@ -258,15 +259,15 @@ __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint
     uint32_t a_ready = 0, x_ready = 0, s_ready = 0;
     for (int item = first; item < items; item += step)
         for (int b = 0; b < nb; ++b) {
-            if (!a_ready && !bar_wait(&bars.a_full[buf], buf_phase, &bars.failed)) return;
-            if (!x_ready && !bar_wait(&bars.x_full[xs], xs_phase, &bars.failed)) return;
+            if (!a_ready && !bar_wait(&bars.a_full[buf], buf_phase, &bars.failed)) return false;
+            if (!x_ready && !bar_wait(&bars.x_full[xs], xs_phase, &bars.failed)) return false;
             // addresses count 16 bytes
             const uint64_t x_at = x0 + xs * (M::kXBytes / 16);
             const uint32_t a_at = tmem_a + buf * 64;
 #pragma unroll
             for (int gh = 0; gh < kInner / G * H; ++gh) {
                 const int g = gh / H, h = gh % H;
-                if (!s_ready && !bar_wait(&bars.s_empty[slot], slot_phase, &bars.failed)) return;
+                if (!s_ready && !bar_wait(&bars.s_empty[slot], slot_phase, &bars.failed)) return false;
                 fence_after();
                 const uint32_t d = tmem + slot * N;
 #pragma unroll
@@ -294,6 +295,7 @@ __device__ __forceinline__ void issue_products(Bars& bars, uint32_t x_ring, uint
             a_ready = bar_done(&bars.a_full[buf], buf_phase);
             x_ready = bar_done(&bars.x_full[xs], xs_phase);
         }
+    return true;
 }
 
 // ------------------------------------------------------------------ x
@@ -375,6 +377,7 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
             bar_init(&bars.s_full[i], 1);
             bar_init(&bars.s_empty[i], H == 2 ? 4 : 4 * M::kAdders);
         }
+        bar_init(&bars.drained, 1);
         bars.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -504,12 +507,15 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
         if constexpr (M::kAdders == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(M::kIssueRegs));
         if (warp == kIssue && elect_one()) {
             // ---- products
-            if (a.group == 128)
-                issue_products<N, H, 128>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
-            else if (a.group == 64)
-                issue_products<N, H, 64>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
-            else
-                issue_products<N, H, 32>(bars, shared_of(x_ring), tmem, tmem_a, first, step, items, nb);
+            const uint32_t x_at = shared_of(x_ring);
+            const bool ok = a.group == 128  ? issue_products<N, H, 128>(bars, x_at, tmem, tmem_a, first, step, items, nb)
+                            : a.group == 64 ? issue_products<N, H, 64>(bars, x_at, tmem, tmem_a, first, step, items, nb)
+                                            : issue_products<N, H, 32>(bars, x_at, tmem, tmem_a, first, step, items, nb);
+            if (!ok) {  // a failed block's products end before its memory goes away
+                commit_to(&bars.drained);
+                uint32_t quiet = 0;
+                bar_wait(&bars.drained, 0, &quiet);
+            }
         }
         if (warp == kIssue + 1 && elect_one()) {
             // ---- x
@@ -649,6 +655,9 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
     }
     __syncthreads();
     if (a.cluster > 1) {
+        if (bars.failed) {  // copies that were under way may have landed on the sums: they are NaN again
+            for (int i = tid; i < H * N * 128; i += M::kThreads) reinterpret_cast<float*>(dyn)[i] = __uint_as_float(0x7FC00000u);
+        }
         // one item a cluster: each block adds up its share of the rows of x
         cluster_sync_all();
         const int item = first;
