@@ -12,7 +12,6 @@
 
 namespace arcs {
 
-constexpr float kE4m3Max = 448.0f;
 constexpr int kScaleExp = 32;  // page scales written here lie in [2^-32, 2^32]
 
 template <int DT>
@@ -92,16 +91,8 @@ __device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& lo, uint32
 
 // Least e in [-32, 32] with amax <= 448 * 2^e; 448 = 1.75 * 2^8, so the
 // exponent of amax counts one more when its mantissa passes 1.75.
-__host__ __device__ __forceinline__ int scale_exponent(float amax) {
-#ifdef __CUDA_ARCH__
+__device__ __forceinline__ int scale_exponent(float amax) {
     const uint32_t b = __float_as_uint(amax);
-#else
-    union {
-        float f;
-        uint32_t u;
-    } v = {amax};
-    const uint32_t b = v.u;
-#endif
     const int e = static_cast<int>((b + 0x1FFFFFu) >> 23) - 127 - 8;
     return e < -kScaleExp ? -kScaleExp : (e > kScaleExp ? kScaleExp : e);
 }

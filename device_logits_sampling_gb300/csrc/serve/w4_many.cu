@@ -161,13 +161,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&x)[32]) {
         : "r"(at)
         : "memory");
 }
-__device__ __forceinline__ void tmem_load64(uint32_t at, uint32_t (&x)[64]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
-        : ARC_OUT8(x, 0), ARC_OUT8(x, 8), ARC_OUT8(x, 16), ARC_OUT8(x, 24), ARC_OUT8(x, 32), ARC_OUT8(x, 40), ARC_OUT8(x, 48), ARC_OUT8(x, 56)
-        : "r"(at)
-        : "memory");
-}
 #undef ARC_OUT8
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -611,9 +604,7 @@ __global__ void __launch_bounds__(Many<N, H>::kThreads, 1) many_kernel(const __g
 #pragma unroll
                 for (int c = 0; c < C; c += L) {
                     uint32_t d[L];
-                    if constexpr (L == 64)
-                        tmem_load64(at + c, d);
-                    else if constexpr (L == 32)
+                    if constexpr (L == 32)
                         tmem_load32(at + c, d);
                     else
                         tmem_load16(at + c, d);

@@ -180,7 +180,7 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
     const float* up = reinterpret_cast<const float*>(top);
     float* xs = reinterpret_cast<float*>(dyn + f.xs_off);
     for (int i = tid; i < groups * 8; i += kFewThreads)
-        if (i % (8) >= rows) xs[i] = 0.0f;
+        if (i % 8 >= rows) xs[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < kXVecs; ++j) {
         if (j * kFewThreads >= all) break;
