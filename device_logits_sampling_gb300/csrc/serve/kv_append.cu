@@ -16,9 +16,12 @@
 //
 // Bounds and figures.  One token of a sequence: latency, a launch and three
 // dependent loads (position, page, scale): 4.0 us; 256 tokens of 32 + 8 heads
-// of 64: 5.5 us.  Prompts (10,476 tokens of 32 + 8 heads of 128): 69 us against
+// of 64: 5.7 us.  Prompts (10,476 tokens of 32 + 8 heads of 128): 72 us against
 // 35 us of memory time; the page blocks wait on their own chain (find the page,
-// load, maximum, round) at 16 warps an SM, which their registers allow.
+// load, maximum, round) at 16 warps an SM, which their registers allow (the half
+// layout spills 312 to 384 bytes a thread).  300 sequences of 1 to 5 drafted tokens:
+// 50 us, a block a page and four heads.  2 us of these are the look at all offsets
+// by every block, 1 us the care for infinities.
 // Measured and left: eight values a thread (187 us), one launch for queries and
 // pages (135 us: the queries are held to the pages' registers), no load ahead
 // of the next head (78 us), eight heads a block (80 us), one pass in registers
@@ -908,7 +911,8 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
     a.q_blocks = 0;
     if (rows->q_heads > 0) {
         // few tokens: each head its own threads; many: a thread turns several heads of its sixteen values with one
-        // set of angles (10,476 tokens of 32 heads: 69 us with sets for 155,000 threads, 72 for 620,000)
+        // set of angles.  Sets for 155,000 threads against 620,000: 10,476 tokens of 32 heads of 128 73 us against 77,
+        // of 64 38 against 46; 5,400 in 16 pieces 47 against 57; 700 16.6 either way
         const int64_t units = step->T * L;
         while (a.head_sets < rows->q_heads && units * a.head_sets < 152 * 1024) a.head_sets *= 2;
         if (a.head_sets > rows->q_heads) a.head_sets = rows->q_heads;
@@ -923,8 +927,8 @@ extern "C" int arc_kv_append(const arc_kv_cache* cache, const arc_kv_step* step,
         const int64_t most = step->T / cache->page_size + 2 * seqs;
         // (and a block more, which finds no page and so sees all offsets)
         const int64_t pages = (most < step->T ? most : step->T) + 1;
-        // many pages: a block stores several heads with one set of angles (prompts of 10,476 tokens: 69 us with four
-        // heads, 73 with two, 84 with one)
+        // many pages: a block stores several heads with one set of angles.  Four, two and one: 10,476 tokens 73, 76
+        // and 90 us; 300 sequences of drafts 50, 71 and 111; 16 pieces 47, 47 and 52
         while (a.page_heads < 4 && a.page_heads < cache->heads && pages * cache->heads / a.page_heads > 512) a.page_heads *= 2;
         kv_blocks = pages * 2 * ((cache->heads + a.page_heads - 1) / a.page_heads);
     }

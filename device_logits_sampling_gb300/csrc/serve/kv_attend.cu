@@ -32,16 +32,16 @@
 // 1 and summed up across steps by the matrix instruction, lost what lay below
 // 2^-25 of the largest, which a page of a far larger scale made of all others.
 //
-// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 288 us,
-// 6.4 TB/s, 95% of the measured copy rate (278 us, 98%, with the products summed
-// up by the matrix instruction): the 12 warps of an SM need some 2,000 clocks a
-// step, about what memory gives them 4 KB in.  One sequence of 200,003: 75 us
-// (80%); 256 of 1 to 4,096: 66 us (66%): the line's ends, about 12,000 clocks to
-// the first step and as many for the joins.  Short calls are those: 14 us.  48
-// sequences of 1 to 5 drafted tokens, heads of 64, a window: 36 us.  Measured and
-// left: a block for each (sequence, head) and one token at a time a warp (157 ms
-// for the 200,003), more warps with fewer registers and stages (95 us for it),
-// joins row by row in every thread (84 us).
+// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 282 us,
+// 6.6 TB/s, 97% of the measured copy rate (278 us with the products summed up by
+// the matrix instruction): the 12 warps of an SM need some 2,000 clocks a step,
+// which is what memory gives them 4 KB in.  One sequence of 200,003: 74 us (81%);
+// 256 of 1 to 4,096: 65 us (67%): the line's ends, about 12,000 clocks to the first
+// step and as many for the joins.  Short calls are those: 14 us.  48 sequences of 1
+// to 5 drafted tokens, heads of 64, a window: 36 us.  Measured and left: a block for
+// each (sequence, head) and one token at a time a warp (157 ms for the 200,003),
+// more warps with fewer registers and stages (95 us for it), joins row by row in
+// every thread (84 us).
 #include <atomic>
 
 #include "kv_device.cuh"
@@ -55,8 +55,10 @@ using namespace arcs;
 
 constexpr int kMaxBlocks = 256;  // blocks of a launch: at most one for each SM
 constexpr float kNothing = -3.0e38f;  // maximum of no score: finite, so that differences need no special case
-constexpr int kItemCost = 3;     // an item's fixed cost in steps (query load, output store), for the cut (256 ragged
-                                 // sequences: 81 us with 1, 67 with 2, 63.5 with 3, 64 with 4)
+// An item's fixed cost in steps (query load, output store), for the cut.  With 1, 2, 3 and 4: 256 ragged sequences
+// 82, 68, 65 and 65 us, heads of 64 50, 46, 48 and 49, heads of 256 69, 62, 60 and 60; 500 short ones 37, 35, 36 and 37;
+// drafts 37, 36, 36 and 35; sequences of one length 69 to 70 with any.
+constexpr int kItemCost = 3;
 constexpr float kLift = 16384.0f;  // of the weights as fp16: 2^14 of its 2^15.99
 constexpr int kStatusBytes = kMaxBlocks * 4;
 
@@ -1013,10 +1015,12 @@ int arc_kv_attend(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
             (vectors(query->out, query->out_token_stride, query->out_head_stride) ? 2 : 0);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // Rows of a (sequence, cached head) on average.  Tiles of 16 read the cache half as often and pay when they are
-    // full: groups of 10 to 16 heads, one token each, heads of 128: 130 us against 164 with tiles of 8; of 64: 79 to
-    // 81 against 96.  Ragged drafts leave many of them half empty: up to an average of 18 rows tiles of 8 are faster
-    // (heads of 128, 9 rows: 57 us against 71; 12: 63 to 69 against 68 to 78; 18: 80 against 86; heads of 64, 18
-    // rows: 52 against 57), at 20 rows of sequences of one length tiles of 16 (107 against 113).
+    // full: groups of 10 to 16 heads, one token each, heads of 128: 136 us against 168 with tiles of 8; of 64: 88 to
+    // 91 against 100; pieces of 30 to 90 tokens 449 against 566 and 266 against 317.  Ragged drafts leave many of them
+    // half empty: 1 to 5 tokens at 9 rows on average 64 us against 72, at 15 87 against 93, at 18 to 24 still 91 to 103
+    // against 100 to 110; sequences of one length, at 16 rows 132 against 139, at 20 163 against 155 (heads of 64: 45
+    // against 50, 57 against 62, 60 to 67 against 67 to 73, 83 against 93, 99 against 102).  The lengths are on the
+    // device, so the border lies between the ragged and the even ones.
     const int64_t small = step->row_offsets != nullptr && a.group <= 8 ? 18 : 8;
     const bool wide = step->T * a.group > step->B * small;
     if (cache->head_dim == 64) return wide ? launch<64, 2>(a, dev, sms, st) : launch<64, 1>(a, dev, sms, st);

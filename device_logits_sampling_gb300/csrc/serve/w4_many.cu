@@ -26,10 +26,10 @@
 //
 // Every wait has a limit; a block whose wait runs out writes NaN.
 //
-// Bounds and figures (129,280 x 4,096, groups of 128).  256 rows: 186 us, 1,450
-// TFLOP/s, 77% of the measured bf16 rate; what is left is the round from a
+// Bounds and figures (129,280 x 4,096, groups of 128).  256 rows: 184 us, 1,470
+// TFLOP/s, 78% of the measured bf16 rate; what is left is the round from a
 // group's sums back to the product that takes their place, about 1,600 clocks
-// over three slots.  128 rows: 121 us, the adders' share.  16 rows: 83 us, 3.2
+// over three slots.  128 rows: 118 us, the adders' share.  16 rows: 82 us, 3.4
 // TB/s; a block of 128 x 128 takes 700 clocks of adding and unpacking against
 // 350 of memory time.  Measured and left: products predicated on the thread's
 // index rather than elect.sync (222 us at 16 rows), one lane polling for a warp

@@ -51,7 +51,7 @@ struct W4Args {
 // an SM.  One row by 129,280 x 4,096, groups of 64: 61 us, 4.6 TB/s, 68% of the
 // measured copy rate; 4,096 x 4,096: 5.9 us, most of it a launch and one round
 // trip to memory. Measured and left: 16 rows in two tiles (163 us, shared-memory
-// bound: w4_many.cu takes 83), joining every tile (69 us against 64), a rolled
+// bound: w4_many.cu takes 82), joining every tile (69 us against 64), a rolled
 // staging loop (19,500 clocks for 7 rows against 10,700).
 constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -550,7 +550,7 @@ int launch_few_group(const W4Args& a, int dev, int sms, cudaStream_t st) {
 }
 
 // More rows take the 5th-generation tensor cores (w4_many.cu).  129,280 x 4,096, groups of 128: 8 rows 65 us here
-// and 83 to 88 there; 9 rows, which do not fit one tile here, 84 there.
+// and 82 to 88 there; 9 rows, which do not fit one tile here, 84 there.
 constexpr int kFewRows = 8;
 
 int check_weight(const arc_w4_weight* w) {

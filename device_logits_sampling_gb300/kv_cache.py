@@ -35,7 +35,7 @@ _I32 = torch.int32
 
 
 class PagedCache:
-    """Keys and values as e4m3 codes [pages, heads, page_size, head_dim] (float8_e4m3fn or
+    """CUDA tensors as a cache: keys and values as e4m3 codes [pages, heads, page_size, head_dim] (float8_e4m3fn or
     uint8; the last two dimensions contiguous) with fp32 scales [pages, heads]:
     value = code * scale.  page_size 16, 32, 64, 128 or 256; head_dim 64, 128 or 256."""
 
@@ -103,7 +103,10 @@ def rope_turns(rot_dim: int, base: float = 10000.0, scaling: str | None = None, 
       "base"    the base raised so that the slowest pair turns `factor` times slower
       "parts"   pairs that turn less than `slow` times over original_length are
                 interpolated, those that turn more than `fast` times are left alone, with a
-                linear ramp between; amplitude 0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN")
+                linear ramp between; amplitude 0.1 ln(factor) + 1 (Peng et al. 2023, "YaRN").  The
+                ramp runs over the number of turns, as in the paper; where a model's own code ramps
+                over the index of the pair instead, the pairs between turn differently: give that
+                model's `turns` to Rope
     """
     want(rot_dim >= 0 and rot_dim % 2 == 0, "rot_dim must be even")
     want(scaling in (None, "linear", "base", "parts"), "scaling must be None, 'linear', 'base' or 'parts'")

@@ -133,7 +133,8 @@ def new_output(like, shape: tuple, strides: tuple, dtype, stream=None):
 
     Memory is handed out in the order of the stream it is allocated on, so a call on another
     stream than the current one gets its output from that stream; the current one is recorded
-    as a user too, since that is where the caller goes on."""
+    as a user too, since that is where the caller goes on.  On the current stream the short
+    allocation is taken, which no dispatch mode of torch sees."""
     if foreign(stream, like.get_device()):
         with torch.cuda.stream(stream):
             out = like.new_empty(shape, dtype=dtype)

@@ -7,7 +7,12 @@
  *
  * q is unsigned, 0 .. 15, two to a byte: byte i of row n holds q[n][2 i] in
  * its low half and q[n][2 i + 1] in its high half.  z is 8 where `zeros` is
- * NULL.  Products are exact, sums are fp32, y is rounded once.
+ * NULL.  x enters the products as fp16 after a power-of-two scaling of each row
+ * (exact but for values below 2^-25 of the row's largest), codes less zero
+ * points are exact, and so are products.  Sums are fp32; within a group they are
+ * the tensor cores', which cut off where a rounding would be to nearest (one
+ * part in 2^23 for 16 products).  y is rounded once.  An infinite or NaN value of
+ * x makes its own row infinite or NaN.
  *
  * Library: libarcserve.so; conventions as in arc_kv.h.
  */
