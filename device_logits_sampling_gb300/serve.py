@@ -128,6 +128,13 @@ def foreign(stream, device: int) -> bool:
     return stream is not None and int(stream.cuda_stream) != stream_of(None, device)
 
 
+def on_stream(stream, device: int):
+    """Context whose allocations are the stream's; any object that has the handle of one as cuda_stream will do."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 def new_output(like, shape: tuple, strides: tuple, dtype, stream=None):
     """An uninitialised contiguous tensor on the device of `like`, for a call on `stream`.
 
@@ -136,7 +143,7 @@ def new_output(like, shape: tuple, strides: tuple, dtype, stream=None):
     as a user too, since that is where the caller goes on.  On the current stream the short
     allocation is taken, which no dispatch mode of torch sees."""
     if foreign(stream, like.get_device()):
-        with torch.cuda.stream(stream):
+        with on_stream(stream, like.get_device()):
             out = like.new_empty(shape, dtype=dtype)
         out.record_stream(torch.cuda.current_stream(like.device))
         return out
@@ -150,7 +157,7 @@ def new_workspace(like, nbytes: int, zeroed: bool, stream=None):
     call and its next user after it."""
     make = torch.zeros if zeroed else torch.empty
     if foreign(stream, like.get_device()):
-        with torch.cuda.stream(stream):
+        with on_stream(stream, like.get_device()):
             return make(nbytes, dtype=torch.uint8, device=like.device)
     if not zeroed:
         return new_output(like, (nbytes,), (1,), torch.uint8)

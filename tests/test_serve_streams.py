@@ -118,3 +118,25 @@ def test_a_stream_that_is_current_already(cuda_lib):
             got = call(stream=side)
         side.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", range(4))
+def test_another_library_s_stream(cuda_lib, which):
+    """A call asks no more of a stream than its handle."""
+    import torch
+
+    class Handle:
+        def __init__(self, stream):
+            self.cuda_stream = stream.cuda_stream
+
+    _, call, made = calls()[which]
+    want = call()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    del poison(made)[:]
+    torch.cuda._sleep(BUSY)
+    got = call(stream=Handle(side))
+    side.synchronize()
+    assert torch.equal(got.cpu(), want.cpu())
+    torch.cuda.synchronize()
