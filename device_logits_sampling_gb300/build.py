@@ -24,7 +24,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("kernels_bf16.cu", "kernels_bf16_hist
                                             "arc_sample.cu", "arc_decode.cu")]
 SERVE_LIB = os.path.join(LIBDIR, "libarcserve.so")
 SERVE_SOURCES = [os.path.join(CSRC, "serve", f) for f in ("kv_append.cu", "kv_attend.cu", "w4_matvec.cu",
-                                                           "w4_many.cu",
+                                                           "w4_many.cu", "norm_join.cu", "logit_edit.cu",
                                                            "arc_serve.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,285 @@
+// arc_edit_logits: penalties, biases and a mask of allowed ids on a step's logits, in one pass.
+//
+// A block has a slice of a row.  It reads the row's lists once, keeps those of its ids in two tables in shared memory
+// (how often the history has the id; the last bias entry for it, so that the order in which entries arrive does not
+// matter) and marks each group of eight ids that has one.  Then it streams: eight ids are one byte of the mask, one
+// byte of marks and 16 bytes of 16-bit logits.  Eight disallowed ids are written without being read; in place, eight
+// that are allowed and unmarked are not touched at all.
+//
+// Rows of an odd vocabulary begin anywhere: the groups of eight are laid on the 16-byte boundaries of the output, the
+// mask's byte is cut out of two, and logits that are not aligned alike are read one by one.
+#include <atomic>
+#include <climits>
+#include <cstdint>
+
+#include "launch_util.cuh"
+#include "serve/arc_edit.h"
+#include "serve_util.cuh"
+
+namespace {
+
+using namespace arcs;
+
+constexpr int kThreads = 256;
+constexpr int kGroups = 4;                          // groups of eight a thread has
+constexpr int kSlice = kThreads * kGroups;          // groups of a block
+constexpr int kIds = kSlice * 8;
+
+struct EditArgs {
+    arc_logit_edits e;
+    const void* logits;
+    void* out;
+    int64_t B, V, ld, out_ld;
+    uint32_t* err;
+    int32_t in_place;
+};
+
+struct Tables {
+    uint32_t count[kIds];  // of the history
+    uint32_t entry[kIds];  // 1 + the last bias entry
+    uint8_t marks[kSlice];
+};
+
+template <int DT>
+struct Type {
+    using T = typename Half<DT>::T;
+};
+template <>
+struct Type<ARC_F32> {
+    using T = float;
+};
+template <int DT>
+__device__ __forceinline__ float widen(typename Type<DT>::T x) {
+    if constexpr (DT == ARC_F32)
+        return x;
+    else
+        return Half<DT>::to_float(x);
+}
+template <int DT>
+__device__ __forceinline__ typename Type<DT>::T narrow(float x) {
+    if constexpr (DT == ARC_F32)
+        return x;
+    else
+        return Half<DT>::from_float(x);
+}
+
+// A row's part of a list; false where its offsets are wrong.
+__device__ __forceinline__ bool part_of(const int32_t* offsets, int64_t row, int64_t len, int64_t& lo, int64_t& hi) {
+    lo = __ldg(offsets + row);
+    hi = __ldg(offsets + row + 1);
+    if (lo >= 0 && lo <= hi && hi <= len) return true;
+    lo = hi = 0;
+    return false;
+}
+
+__device__ __forceinline__ bool in_range(float x) { return fabsf(x) <= 3.4028235e38f; }
+
+template <int DT, int OT, bool LISTS>
+__global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ EditArgs a) {
+    using T = typename Type<DT>::T;
+    using O = typename Type<OT>::T;
+    extern __shared__ __align__(16) uint8_t dyn[];
+    Tables& tab = *reinterpret_cast<Tables*>(dyn);
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.y + static_cast<int64_t>(gridDim.y) * blockIdx.z;
+    if (row >= a.B) return;
+    const T* const in = static_cast<const T*>(a.logits) + row * a.ld;
+    O* const out = static_cast<O*>(a.out) + row * a.out_ld;
+    // ids of the first, short group: those before the output's first 16-byte boundary
+    const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out) & 15)) & 15) / static_cast<int>(sizeof(O));
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kIds + (head ? head - 8 : 0);  // first id, maybe below 0
+    if (base >= a.V) return;
+    const bool first = blockIdx.x == 0;
+    uint32_t err = 0;
+
+    int64_t h0 = 0, h1 = 0, b0 = 0, b1 = 0;
+    float rep = 1.0f, freq = 0.0f, pres = 0.0f;
+    if (a.e.hist_offsets) {
+        if (!part_of(a.e.hist_offsets, row, a.e.hist_len, h0, h1)) err |= ARC_EDIT_ERR_HIST;
+        const arc_row_params* p = a.e.params + row;
+        rep = p->repetition_penalty;
+        freq = p->frequency_penalty;
+        pres = p->presence_penalty;
+        if (!(rep > 0.0f) || !in_range(rep) || !in_range(freq) || !in_range(pres)) {
+            err |= ARC_EDIT_ERR_PARAM;
+            h1 = h0;
+        }
+    }
+    if (a.e.bias_offsets && !part_of(a.e.bias_offsets, row, a.e.bias_len, b0, b1)) err |= ARC_EDIT_ERR_BIAS;
+    const uint32_t* mask = nullptr;
+    bool nothing = false;
+    if (a.e.allowed) {
+        const int64_t m = a.e.allowed_rows ? __ldg(a.e.allowed_rows + row) : row;
+        if (m >= a.e.allowed_count) {
+            err |= ARC_EDIT_ERR_MASK;
+            nothing = true;
+        } else if (m >= 0) {
+            mask = a.e.allowed + m * a.e.allowed_stride;
+        }
+    }
+
+    const bool lists = LISTS && !nothing && (h1 > h0 || b1 > b0);
+    if (lists) {
+        uint4* z = reinterpret_cast<uint4*>(dyn);
+        for (int i = tid; i < static_cast<int>(sizeof(Tables) / 16); i += kThreads) z[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        for (int64_t i = h0 + tid; i < h1; i += kThreads) {
+            const int64_t id = __ldg(a.e.hist_ids + i);
+            if (id < 0 || id >= a.V) {
+                err |= ARC_EDIT_ERR_HIST;
+            } else if (static_cast<uint64_t>(id - base) < kIds) {
+                atomicAdd(&tab.count[id - base], 1u);
+                tab.marks[(id - base) >> 3] = 1;
+            }
+        }
+        for (int64_t i = b0 + tid; i < b1; i += kThreads) {
+            const int64_t id = __ldg(a.e.bias_ids + i);
+            if (id < 0 || id >= a.V) {
+                err |= ARC_EDIT_ERR_BIAS;
+            } else if (static_cast<uint64_t>(id - base) < kIds) {
+                atomicMax(&tab.entry[id - base], static_cast<uint32_t>(i - b0 + 1));
+                tab.marks[(id - base) >> 3] = 1;
+            }
+        }
+        __syncthreads();
+    }
+    if (err && first && a.err) atomicOr(a.err, err);
+
+    // the mask's eight bits of ids i .. i + 7 (i may lie below 0; no bit from V on is used)
+    const int64_t words = (a.V + 31) >> 5;
+    auto bits_of = [&](int64_t i) -> uint32_t {
+        if (nothing) return 0;
+        if (mask == nullptr) return 0xFFu;
+        const int64_t w = i >> 5;
+        const int s = static_cast<int>(i & 31);
+        uint32_t lo = w >= 0 ? __ldg(mask + w) : 0, hi = 0;
+        if (s > 24 && w + 1 < words) hi = __ldg(mask + w + 1);
+        return __funnelshift_r(lo, hi, s) & 0xFFu;
+    };
+    auto edited = [&](float z, int64_t id) {
+        const int at = static_cast<int>(id - base);
+        const uint32_t c = tab.count[at], e = tab.entry[at];
+        if (c) {
+            z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+            z = __fsub_rn(z, __fmul_rn(static_cast<float>(c), freq));
+            z = __fsub_rn(z, pres);
+        }
+        if (e) z = __fadd_rn(z, __ldg(a.e.bias + b0 + (e - 1)));
+        return z;
+    };
+    const float none = -__int_as_float(0x7F800000);
+    const bool in_vec = ((reinterpret_cast<uintptr_t>(in) + base * static_cast<int64_t>(sizeof(T))) & 15) == 0;
+    uint32_t bits[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int64_t i = base + (g * kThreads + tid) * 8;
+        bits[g] = i < a.V ? bits_of(i) : 0;
+    }
+    T x[kGroups][8];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int64_t i = base + (g * kThreads + tid) * 8;
+        const bool marked = lists && tab.marks[g * kThreads + tid];
+        if (i >= a.V || bits[g] == 0 || (a.in_place && bits[g] == 0xFFu && !marked)) continue;
+        if (in_vec && i >= 0 && i + 8 <= a.V) {
+            const uint4* p = reinterpret_cast<const uint4*>(in + i);
+            uint4* q = reinterpret_cast<uint4*>(x[g]);
+#pragma unroll
+            for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) q[k] = p[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k >= 0 && i + k < a.V) x[g][k] = in[i + k];
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const int64_t i = base + (g * kThreads + tid) * 8;
+        const bool marked = lists && tab.marks[g * kThreads + tid];
+        if (i >= a.V || (a.in_place && bits[g] == 0xFFu && !marked)) continue;
+        O y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (bits[g] >> k & 1) {
+                if constexpr (DT == OT)
+                    y[k] = x[g][k];
+                else
+                    y[k] = narrow<OT>(widen<DT>(x[g][k]));
+                if (marked && i + k >= 0 && i + k < a.V) {
+                    const int at = static_cast<int>(i + k - base);
+                    if (tab.count[at] | tab.entry[at]) y[k] = narrow<OT>(edited(widen<DT>(x[g][k]), i + k));
+                }
+            } else {
+                y[k] = narrow<OT>(none);
+            }
+        }
+        if (i >= 0 && i + 8 <= a.V) {
+            const uint4* q = reinterpret_cast<const uint4*>(y);
+            uint4* p = reinterpret_cast<uint4*>(out + i);
+#pragma unroll
+            for (int k = 0; k < static_cast<int>(sizeof(O)) / 2; ++k) p[k] = q[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k >= 0 && i + k < a.V) out[i + k] = y[k];
+        }
+    }
+}
+
+template <int DT, int OT, bool LISTS>
+int launch(const EditArgs& a, int dev, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    // without tables the whole of an SM's storage holds loads in flight
+    if (arc::prepare(edit_kernel<DT, OT, LISTS>, dev, done, LISTS ? 100 : 0) != cudaSuccess) return ARC_E_CUDA;
+    // the short first group shifts the slices by less than one group
+    const int64_t slices = (a.V + 7 + kIds - 1) / kIds;
+    const int64_t ys = a.B < 65535 ? a.B : 65535, zs = (a.B + ys - 1) / ys;
+    const dim3 grid(static_cast<unsigned>(slices), static_cast<unsigned>(ys), static_cast<unsigned>(zs));
+    edit_kernel<DT, OT, LISTS><<<grid, kThreads, LISTS ? sizeof(Tables) : 0, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
+}
+
+template <int DT, int OT>
+int launch(const EditArgs& a, int dev, cudaStream_t st) {
+    return a.e.hist_offsets || a.e.bias_offsets ? launch<DT, OT, true>(a, dev, st) : launch<DT, OT, false>(a, dev, st);
+}
+
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+}  // namespace
+
+extern "C" int arc_edit_logits(const void* logits, int64_t B, int64_t V, int64_t ld, int32_t dtype, void* out,
+                               int64_t out_ld, int32_t out_dtype, const arc_logit_edits* edits, uint32_t* err_word,
+                               void* stream) {
+    if (logits == nullptr || out == nullptr || edits == nullptr) return ARC_E_NULL;
+    const arc_logit_edits& e = *edits;
+    if ((e.hist_offsets == nullptr) != (e.hist_ids == nullptr)) return ARC_E_NULL;
+    if (e.hist_offsets != nullptr && e.params == nullptr) return ARC_E_NULL;
+    if ((e.bias_offsets == nullptr) != (e.bias_ids == nullptr) || (e.bias_offsets == nullptr) != (e.bias == nullptr))
+        return ARC_E_NULL;
+    if (e.allowed == nullptr && e.allowed_rows != nullptr) return ARC_E_NULL;
+    if (dtype != ARC_F32 && dtype != ARC_BF16 && dtype != ARC_F16) return ARC_E_DTYPE;
+    if (out_dtype != dtype && out_dtype != ARC_F32) return ARC_E_DTYPE;
+    if (B <= 0 || B > INT_MAX || V <= 0 || V > INT_MAX || ld < V || out_ld < V) return ARC_E_SHAPE;
+    if (e.hist_offsets && (e.hist_len < 0 || e.hist_len > INT_MAX)) return ARC_E_SHAPE;
+    if (e.bias_offsets && (e.bias_len < 0 || e.bias_len > INT_MAX)) return ARC_E_SHAPE;
+    if (e.allowed && (e.allowed_stride < (V + 31) / 32 || e.allowed_count <= 0 ||
+                      (e.allowed_rows == nullptr && e.allowed_count < B)))
+        return ARC_E_SHAPE;
+    if (out == logits && (out_dtype != dtype || (B > 1 && out_ld != ld))) return ARC_E_OPTION;
+    const uintptr_t in_size = dtype == ARC_F32 ? 4 : 2, out_size = out_dtype == ARC_F32 ? 4 : 2;
+    if (!aligned(logits, in_size) || !aligned(out, out_size) || !aligned(err_word, 4) || !aligned(e.hist_offsets, 4) ||
+        !aligned(e.hist_ids, 4) || !aligned(e.bias_offsets, 4) || !aligned(e.bias_ids, 4) || !aligned(e.bias, 4) ||
+        !aligned(e.allowed, 4) || !aligned(e.allowed_rows, 4) || !aligned(e.params, 8))
+        return ARC_E_ALIGN;
+    EditArgs a{e, logits, out, B, V, ld, out_ld, err_word, out == logits};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == ARC_F32) return launch<ARC_F32, ARC_F32>(a, dev, st);
+    if (dtype == ARC_BF16) return out_dtype == ARC_F32 ? launch<ARC_BF16, ARC_F32>(a, dev, st) : launch<ARC_BF16, ARC_BF16>(a, dev, st);
+    return out_dtype == ARC_F32 ? launch<ARC_F16, ARC_F32>(a, dev, st) : launch<ARC_F16, ARC_F16>(a, dev, st);
+}

@@ -49,6 +49,21 @@ class KvQuery(ctypes.Structure):
                 ("out_head_stride", I64), ("q_heads", I32), ("dtype", I32), ("scale", ctypes.c_float), ("window", I32)]
 
 
+class NormRows(ctypes.Structure):
+    """arc_norm_rows, 136 bytes."""
+    _fields_ = [("x", P), ("y", P), ("gate", P), ("post_weight", P), ("weight", P), ("h", P), ("n", P), ("x_stride", I64),
+                ("y_stride", I64), ("gate_stride", I64), ("h_stride", I64), ("n_stride", I64), ("rows", I64), ("dim", I32),
+                ("stream_dtype", I32), ("dtype", I32), ("weight_dtype", I32), ("activation", I32),
+                ("alpha", ctypes.c_float), ("offset", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class LogitEdits(ctypes.Structure):
+    """arc_logit_edits, 96 bytes."""
+    _fields_ = [("params", P), ("hist_offsets", P), ("hist_ids", P), ("hist_len", I64), ("bias_offsets", P),
+                ("bias_ids", P), ("bias", P), ("bias_len", I64), ("allowed", P), ("allowed_stride", I64),
+                ("allowed_count", I64), ("allowed_rows", P)]
+
+
 class W4Weight(ctypes.Structure):
     """arc_w4_weight, 48 bytes."""
     _fields_ = [("q", P), ("scales", P), ("zeros", P), ("row_bytes", I64), ("outs", I64), ("ins", I32), ("group", I32)]
@@ -61,6 +76,8 @@ SIGNATURES = {
     "arc_kv_attend_workspace_bytes": (SIZE, [P]),
     "arc_w4_matvec": (ctypes.c_int, [P, P, I64, I64, I32, P, I64, I32, P, SIZE, P]),
     "arc_w4_workspace_bytes": (SIZE, [P, I64]),
+    "arc_norm_join": (ctypes.c_int, [P, P]),
+    "arc_edit_logits": (ctypes.c_int, [P, I64, I64, I64, I32, P, I64, I32, P, P, P]),
     "arc_serve_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     "arc_serve_abi_version": (ctypes.c_int, []),
 }
