@@ -206,10 +206,11 @@ def append(cache: PagedCache, k, v, positions, page_table, q=None, q_out=None, r
 
 
 def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=None, scale: float | None = None,
-           window: int = 0, err_word=None, workspace=None, stream=None, check: bool = True):
+           window: int = 0, err_word=None, workspace=None, stream=None, check: bool = True, sinks: int = 0):
     """arc_kv_attend: attention of the step's tokens, q [T, q_heads, head_dim], over the cache
     that `append` has just extended (the same positions, page_table and row_offsets).  scale:
-    head_dim ** -0.5 where None.  window > 0: each token sees its last `window` tokens alone.
+    head_dim ** -0.5 where None.  window > 0: each token sees its last `window` tokens, and the
+    first `sinks` of its sequence (arc_kv_attend_sinks), alone.
     workspace: cache.attend_workspace(), made for the call where None.  Returns out.
 
     stream: where the call runs, the current stream where None.  What the call makes for itself (out,
@@ -231,7 +232,10 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
     wp, wn = serve.workspace_of(workspace, dev)
     query = _QUERY.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, heads, code,
                         cache.default_scale if scale is None else scale, window)
-    rc = serve.load().arc_kv_attend(cache._ref, step, query, serve.err_word_ptr(err_word, dev), wp, wn,
-                                    serve.stream_of(stream, dev))
+    err, handle = serve.err_word_ptr(err_word, dev), serve.stream_of(stream, dev)
+    if sinks:
+        rc = serve.load().arc_kv_attend_sinks(cache._ref, step, query, sinks, err, wp, wn, handle)
+    else:
+        rc = serve.load().arc_kv_attend(cache._ref, step, query, err, wp, wn, handle)
     serve.finish(rc, check)
     return out

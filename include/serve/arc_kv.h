@@ -167,6 +167,16 @@ int arc_kv_attend(const arc_kv_cache* cache, const arc_kv_step* step, const arc_
 /* Host only; 0 for a cache that arc_kv_attend would refuse. */
 size_t arc_kv_attend_workspace_bytes(const arc_kv_cache* cache);
 
+/*
+ * The same with a sequence's first `sinks` tokens visible whatever the window:
+ * the token at position p sees j <= p with j > p - window or j < sinks.  Pages
+ * that hold neither are not read, nor are their entries of the page table, so
+ * they may have been given to other sequences.  Without a window, or with 0
+ * sinks, this is arc_kv_attend.
+ */
+int arc_kv_attend_sinks(const arc_kv_cache* cache, const arc_kv_step* step, const arc_kv_query* query, int32_t sinks,
+                        uint32_t* err_word, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Text for an ARC_E_* code of this library's calls (static storage). */
 const char* arc_serve_strerror(int code);
 

@@ -115,7 +115,7 @@ def gather(codes, scale, table_row, length: int, head: int) -> np.ndarray:
     return np.concatenate(rows)[:length] if rows else np.zeros((0, codes.shape[3]))
 
 
-def attend(k, v, k_scale, v_scale, q, positions, table, offsets, scale=None, window=0):
+def attend(k, v, k_scale, v_scale, q, positions, table, offsets, scale=None, window=0, sinks=0):
     """(out, spread) [T, q_heads, dim]: the attention, and sum_j p_j |v_j|, which bounds its rounding errors."""
     T, hq, d = q.shape
     heads, ps = k.shape[1], k.shape[2]
@@ -128,20 +128,24 @@ def attend(k, v, k_scale, v_scale, q, positions, table, offsets, scale=None, win
         length = int(positions[b]) + n
         first = max(0, int(positions[b]) + 1 - window) if window else 0
         need = table[b, first // ps: -(-length // ps)]
+        front = min(-(-sinks // ps), first // ps) if window else 0  # pages of first tokens before the window's
+        need = np.concatenate([table[b, :front], need])
         if -(-length // ps) > table.shape[1] or (need < 0).any() or (need >= k.shape[0]).any():
             out[offsets[b]:offsets[b + 1]] = np.nan
             continue
-        skip = first // ps * ps
+        skip = (first // ps - front) * ps  # tokens between them that nobody sees
         for h in range(heads):
             kk = gather(k, k_scale, need, length - skip, h)
             vv = gather(v, v_scale, need, length - skip, h)
             for i in range(n):
                 p = int(positions[b]) + i
-                lo = (max(0, p + 1 - window) if window else 0) - skip
+                lo = max(0, p + 1 - window) if window else 0
+                at = np.concatenate([np.arange(min(sinks, lo)), np.arange(lo, p + 1)])
+                at = np.where(at < front * ps, at, at - skip)  # a window's token behind the front pages
                 t = int(offsets[b]) + i
                 grp = slice(h * (hq // heads), (h + 1) * (hq // heads))
-                s = q[t, grp].astype(np.float64) @ kk[lo:p + 1 - skip].T * scale
+                s = q[t, grp].astype(np.float64) @ kk[at].T * scale
                 w = np.exp(s - s.max(-1, keepdims=True))
                 w /= w.sum(-1, keepdims=True)
-                out[t, grp], spread[t, grp] = w @ vv[lo:p + 1 - skip], w @ np.abs(vv[lo:p + 1 - skip])
+                out[t, grp], spread[t, grp] = w @ vv[at], w @ np.abs(vv[at])
     return out, spread
