@@ -97,6 +97,12 @@ __device__ __forceinline__ int scale_exponent(float amax) {
     return e < -kScaleExp ? -kScaleExp : (e > kScaleExp ? kScaleExp : e);
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 2^e for |e| <= 126.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 

@@ -77,6 +77,14 @@ class PagedCache:
         return serve.new_workspace(self.k, n, True, stream)
 
 
+    def shared_workspace(self, tokens: int, q_heads: int, stream=None):
+        """Zero-filled workspace for `attend_shared` of up to so many new tokens over caches of this shape (one per
+        stream that uses it), made on the stream given, else on the current one."""
+        n = int(serve.load().arc_kv_attend_shared_workspace_bytes(self._ref, tokens, q_heads))
+        want(n > 0, "arc_kv_attend_shared_workspace_bytes rejected the cache, the tokens or the heads")
+        return serve.new_workspace(self.k, n, True, stream)
+
+
 class Rope:
     """A position rotation: `turns` int64 [rot_dim / 2] on the device (64-bit fixed-point
     fractions of a turn per position, see rope_turns), the layout of the pairs ("half" or
@@ -237,5 +245,38 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
         rc = serve.load().arc_kv_attend_sinks(cache._ref, step, query, sinks, err, wp, wn, handle)
     else:
         rc = serve.load().arc_kv_attend(cache._ref, step, query, err, wp, wn, handle)
+    serve.finish(rc, check)
+    return out
+
+
+def attend_shared(cache: PagedCache, q, positions, page_table, prefix, out=None, row_offsets=None,
+                  scale: float | None = None, err_word=None, workspace=None, stream=None, check: bool = True):
+    """arc_kv_attend_shared: `attend` for sequences that all begin with the same tokens, whose whole pages `prefix`
+    int32 [pages] names: they are read once for the batch.  page_table keeps a sequence's pages in their places; the
+    entries under the prefix are not read.  Every sequence's position lies at or past the prefix's end.  workspace:
+    cache.shared_workspace(tokens, q_heads), made for the call where None.  Returns out.  stream: as in `attend`."""
+    T, dim, dev = q.shape[0], cache.head_dim, cache.index
+    qt, qh, heads = _heads(q, T, None, dim, "q")
+    code = serve.dtype_code(q)
+    step = _step(cache, T, positions, page_table, row_offsets)
+    want(q.get_device() == dev, "every tensor must be on the cache's device")
+    want(prefix.dim() == 1 and prefix.is_contiguous(), "prefix must be contiguous [pages]")
+    if prefix.dtype != _I32:
+        raise TypeError("prefix must be int32")
+    want(prefix.get_device() == dev, "every tensor must be on the cache's device")
+    serve.on_current_gpu(dev)
+    if out is None:
+        out = serve.new_output(q, (T, heads, dim), (heads * dim, dim, 1), q.dtype, stream)
+        ot, oh = heads * dim, dim
+    else:
+        ot, oh, _ = _heads(out, T, heads, dim, "out")
+        want(out.dtype == q.dtype and out.get_device() == dev, "out must have q's type and device")
+    if workspace is None:
+        workspace = cache.shared_workspace(T, heads, stream)
+    wp, wn = serve.workspace_of(workspace, dev)
+    query = _QUERY.pack(q.data_ptr(), out.data_ptr(), qt, qh, ot, oh, heads, code,
+                        cache.default_scale if scale is None else scale, 0)
+    rc = serve.load().arc_kv_attend_shared(cache._ref, step, query, prefix.data_ptr(), prefix.numel(),
+                                           serve.err_word_ptr(err_word, dev), wp, wn, serve.stream_of(stream, dev))
     serve.finish(rc, check)
     return out

@@ -74,6 +74,8 @@ SIGNATURES = {
     "arc_kv_append": (ctypes.c_int, [P, P, P, P, P, P]),
     "arc_kv_attend": (ctypes.c_int, [P, P, P, P, P, SIZE, P]),
     "arc_kv_attend_sinks": (ctypes.c_int, [P, P, P, I32, P, P, SIZE, P]),
+    "arc_kv_attend_shared": (ctypes.c_int, [P, P, P, P, I32, P, P, SIZE, P]),
+    "arc_kv_attend_shared_workspace_bytes": (SIZE, [P, I64, I32]),
     "arc_kv_attend_workspace_bytes": (SIZE, [P]),
     "arc_w4_matvec": (ctypes.c_int, [P, P, I64, I64, I32, P, I64, I32, P, SIZE, P]),
     "arc_w4_workspace_bytes": (SIZE, [P, I64]),

@@ -177,6 +177,32 @@ size_t arc_kv_attend_workspace_bytes(const arc_kv_cache* cache);
 int arc_kv_attend_sinks(const arc_kv_cache* cache, const arc_kv_step* step, const arc_kv_query* query, int32_t sinks,
                         uint32_t* err_word, void* workspace, size_t workspace_bytes, void* stream);
 
+#define ARC_KV_SHARED_MAX_ROWS (1 << 22) /* T * q_heads */
+
+/*
+ * The same, without a window, for sequences that all begin with one prefix of
+ * whole pages, whose keys and values are read once for all of them:
+ *   prefix        device [prefix_pages]: the page of each of the prefix's parts
+ *   prefix_pages  1 .. step->max_pages
+ * step->page_table keeps a sequence's pages in their places: its first
+ * prefix_pages entries are not read here.  Every sequence holds the whole
+ * prefix: one whose position lies before the prefix's end sets
+ * ARC_KV_ERR_POSITION and its rows are NaN.  A page outside [0, pages) in the
+ * prefix makes every row NaN.
+ * Weights enter the products with the prefix as fp16, relative to the largest
+ * of the 128 tokens (64 for heads of 256) they are multiplied with, all of
+ * pages whose value scales lie within a factor of 64: off by 2^-11 of
+ * themselves at most above 2^-22 of that one, 0 below 2^-33.
+ *   workspace  arc_kv_attend_shared_workspace_bytes(cache, T, q_heads) bytes,
+ *              as for arc_kv_attend
+ */
+int arc_kv_attend_shared(const arc_kv_cache* cache, const arc_kv_step* step, const arc_kv_query* query,
+                         const int32_t* prefix, int32_t prefix_pages, uint32_t* err_word, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Host only; 0 for arguments that arc_kv_attend_shared would refuse. */
+size_t arc_kv_attend_shared_workspace_bytes(const arc_kv_cache* cache, int64_t T, int32_t q_heads);
+
 /* Text for an ARC_E_* code of this library's calls (static storage). */
 const char* arc_serve_strerror(int code);
 
