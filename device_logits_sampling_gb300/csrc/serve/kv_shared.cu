@@ -9,18 +9,22 @@
 // of 256) of the prefix; all units' chunks lie on a line that is cut into one piece a block.  A block runs through its
 // piece tile by tile, and leaves a partial for each unit that it has met.
 //
-// A tile is a chunk, or the part of one whose pages' value scales lie within a factor of 64: the weights enter the
-// second product as fp16, 2^14 times themselves relative to the tile's largest and times their page's scale over the
-// tile's largest scale, so no page's own scale pushes its weights out of fp16.
+// Products.  Codes are loaded a tile ahead into registers and become fp16 in shared memory, exactly.  S = Q K^T and
+// O += P V run on the 5th-generation tensor cores, M = 128 rows: Q and K from shared memory, P from tensor memory, where
+// the softmax has put it over S, V as it lies, tokens as rows, read across.
 //
-// Products.  Codes come in by bulk copies, page by page, and become fp16 in shared memory, exactly.  S = Q K^T and
-// O = P V run on the 5th-generation tensor cores, M = 128 rows: Q and K from shared memory, P from tensor memory, where
-// the softmax has put it over S, V as it lies, tokens as rows, read across.  A tile's O is read back and added up in
-// registers with a factor a row, so weights are relative to their own tile's largest score, whatever came before.
+// Softmax.  P holds the weights relative to a reference of the row and the value scales relative to a reference of the
+// tiles, 2^12 times, as fp16, and O is summed up in tensor memory in their units.  The references stay while the
+// largest score of a tile lies at most 3 above the row's (as a power of two) or 6 below, and its pages' value scales
+// within 1/16 of theirs; a tile is a chunk, or the part of one whose pages agree.  Else the row takes the tile's own
+// largest score, and the sums so far are multiplied by what that changes, in fp32: a weight keeps its bits beside those
+// of its own tile, whatever scores and scales came before.  (A reference lies at most 2^60 below the largest weight
+// times scale so far, so that the sums stay in fp32's range.)  The sum of the weights is kept apart, relative to the
+// largest score.
 //
-// Roles of a block: two groups of four warps take softmax and sums, a thread a row (two groups of 128 rows, or for heads
-// of 256 one, half of the output each), one group makes fp16 of codes, a warp issues the products and a warp the copies.
-// While one group of rows is at its softmax the products of the other run.
+// Roles of a block: two groups of four warps take the softmax, a thread a row (two groups of 128 rows, or for heads of
+// 256 one, half of the output each), a group makes fp16 of codes, a warp issues the products and a warp looks up pages
+// and scales.  While one group of rows is at its softmax the products of the other run.
 //
 // Every wait has a limit; a block whose wait runs out leaves NaN.
 #include "kv_shared.cuh"
@@ -36,25 +40,31 @@
 namespace arcs {
 namespace {
 
-constexpr float kSpread = 64.0f;  // of the value scales of a tile's pages
-constexpr int kInfos = 8;         // ring of tiles' descriptions: the copies are at most seven tiles ahead
-constexpr int kLiftLog = 14;
+constexpr float kSpread = 16.0f;  // of the value scales that share a reference
+constexpr int kInfos = 8;         // ring of tiles' descriptions
+// A new reference lies kRoom above the tile's largest score; it stays while that is at most kAbove above it (2^(12 + 3)
+// is the largest weight as fp16) and kBelow below.
+constexpr float kLift = 12.0f, kRoom = 4.0f, kAbove = 3.0f, kBelow = 10.0f;
+constexpr float kSpan = 60.0f;
 
 template <int D>
 struct Prefix {
-    static constexpr int kTokens = D == 256 ? 64 : 128;  // of a tile
+    static constexpr int kStep = 64;                     // tokens of a step
+    static constexpr int kSteps = D == 256 ? 1 : 2;      // of a tile
+    static constexpr int kTokens = kStep * kSteps;       // of a tile
     static constexpr int kTiles = D == 256 ? 1 : 2;      // tiles of 128 rows
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kOut = D == 256 ? 128 : D;      // values of the output that a thread adds up
     static constexpr int kGranules = kTokens / 16;
     static constexpr int kThreads = 512;
     static constexpr int kQ = 128 * D * 2;
-    static constexpr int kOp = kTokens * D * 2, kOps = D == 64 ? 6 : 3;   // ring of fp16 tiles, K and V in turn
-    static constexpr int kRaw = kTokens * D, kRaws = D == 64 ? 8 : 4;     // ring of codes, likewise
-    static constexpr int kSmem = kTiles * kQ + kOps * kOp + kRaws * kRaw + 1024;
-    static constexpr int kS = 0, kP = D == 256 ? 128 : 0, kO = 256;       // columns of tensor memory
+    static constexpr int kOp = kTokens * D * 2, kOps = D == 64 ? 8 : 5;  // ring of fp16 tiles, K and V in turn
+    static constexpr int kSmem = kTiles * kQ + kOps * kOp + 1024;
+    static constexpr int kEach = kTokens * D / 16 / 128;  // 16 codes each, of K or V, that a converting thread has
+    // columns of tensor memory: two steps' scores of each tile of rows, weights over them (heads of 256: beside), output
+    static constexpr int kS = 0, kP = D == 256 ? 128 : 0, kPStep = D == 256 ? 32 : 64, kO = 256;
     // registers of a thread once the roles part, of 128 at the launch of 512 threads (4 * 128 = 512)
-    static constexpr int kSoftmaxRegs = 200, kConvertRegs = 72, kIssueRegs = 40;
+    static constexpr int kSoftmaxRegs = 176, kConvertRegs = 104, kIssueRegs = 56;
     static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs <= 512, "registers of the launch");
     static_assert(kO + kTiles * D <= 512, "tensor memory");
 };
@@ -80,87 +90,112 @@ struct PrefixArgs {
 
 __host__ __device__ inline int64_t cut_of(int64_t total, int64_t i, int64_t of) { return total / of * i + total % of * i / of; }
 
-struct Info {  // a tile
+struct __align__(16) Info {  // a tile
     int32_t tokens;
-    int32_t flags;    // 1: the last of its unit's, 2: the last of all
-    float value;      // the tile's largest value scale, times 2^-14
+    int32_t flags;    // 1: the last of its unit's, 2: the last of all, 4: another reference than the tile before's
+    float value;      // the reference of the value scales,
+    float value_log;  // its logarithm
     float key[8];     // of each 16 tokens: key scale,
-    float lift[8];    // 14 + the logarithm of the value scale over the largest
+    float lift[8];    // 12 + the logarithm of the value scale over the reference,
+    float back[8];    // 2^-lift; where there are no tokens key and back are 0 and the lift takes every weight to 0
+    int64_t at[8];    // bytes from the cache's beginning to each page's part; -1: a bad page
 };
 
 struct PrefixBars {
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-    uint64_t raw_full[8], raw_empty[8];
-    uint64_t op_full[6], op_empty[6];
-    uint64_t info_full[kInfos];
-    uint64_t drained;
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2];  // [tile of rows][step's parity]
+    uint64_t op_full[8], op_empty[8];
+    uint64_t info_full[kInfos], info_empty[kInfos];
+    uint64_t drained[2];
     uint32_t tmem, failed;
     Info info[kInfos];
-    float top[2][128];  // heads of 256: the largest of each half of a query row
 };
 
-// One thread issues all products: for each tile S of every tile of rows, a tile ahead, and O behind the softmax.
+// One thread issues the products of tile w of the rows.  The scores are two steps ahead of the output, whose weights the
+// softmax makes meanwhile: where a step's output is issued its scores' place is free, and the step after next's follow at
+// once.  At a unit's end they wait for the next unit's queries.
 template <int D>
-__device__ __forceinline__ bool issue_prefix(PrefixBars& bars, uint32_t q_at, uint32_t ops, uint32_t tmem, int tiles) {
+__device__ __forceinline__ bool issue_prefix(PrefixBars& bars, uint32_t q_at, uint32_t ops, uint32_t tmem, int w) {
     using X = Prefix<D>;
-    constexpr uint32_t s_desc = (1u << 4) | (static_cast<uint32_t>(X::kTokens / 8) << 17) | (8u << 24);
+    constexpr uint32_t s_desc = (1u << 4) | (static_cast<uint32_t>(X::kStep / 8) << 17) | (8u << 24);
     constexpr uint32_t o_desc = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D / 8) << 17) | (8u << 24);
     constexpr uint32_t kBlock = X::kTokens * 128;  // 64 values of all tokens
-    uint32_t q_phase[2] = {0, 0};
-    int flags = 0;
-    bool fresh = true;  // the next tile begins a unit
-    uint32_t op = 0, op_phase = 0;
-    auto next_op = [&]() {
-        if (++op == X::kOps) {
-            op = 0;
-            op_phase ^= 1;
-        }
-    };
-    auto scores = [&](int w, uint32_t stage) {
-        const uint64_t a = operand_at(q_at + w * X::kQ), b = operand_at(ops + stage * X::kOp);
+    auto op_of = [](uint32_t u) { return u % X::kOps; };
+    auto op_phase = [](uint32_t u) { return (u / X::kOps) & 1; };
+    const uint64_t queries = operand_at(q_at + w * X::kQ);
+    uint32_t q_phase = 0;
+    uint32_t ahead = 0;  // the next step whose scores are to be issued, of tile ahead / kSteps
+    int ahead_flags = 0;
+    bool unit_done = false;  // the scores of this unit's last step are out
+    auto scores = [&]() {
+        const uint32_t t = ahead / X::kSteps, half = ahead % X::kSteps;
+        const uint64_t b = operand_at(ops + op_of(2 * t) * X::kOp + half * (X::kStep * 128));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-            mma_f16_shared(tmem + X::kS + w * 128, a + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
+            mma_f16_shared(tmem + X::kS + w * 128 + (ahead & 1) * 64, queries + (k >> 2) * (128 * 128 / 16) + (k & 3) * 2,
                            b + (k >> 2) * (kBlock / 16) + (k & 3) * 2, s_desc, k != 0);
-        commit_to(&bars.s_full[w]);
+        commit_to(&bars.s_full[w][ahead & 1]);
+        if (half == X::kSteps - 1) {
+            commit_to(&bars.op_empty[op_of(2 * t)]);
+            unit_done = ahead_flags & 1;
+        }
+        ++ahead;
     };
-    for (uint32_t t = 0;; ++t) {  // tile t's scores, then tile t - 1's output; past the last tile its output alone
-        const bool more = t == 0 || !(flags & 2);
-        uint32_t k_stage = 0;
-        const uint32_t v_stage = op, v_phase = op_phase;  // of tile t - 1
-        if (t) next_op();
-        if (more) {
-            k_stage = op;
-            if (!bar_wait(&bars.info_full[t % kInfos], (t / kInfos) & 1, &bars.failed)) return false;
-            if (!bar_wait(&bars.op_full[k_stage], op_phase, &bars.failed)) return false;
-            next_op();
+    // What the coming steps wait for but their weights: keys of the step `ahead` where it begins a tile, values of step n
+    // where it does.  It is looked at while the softmax is at work, and together: a look at a barrier takes 150 clocks even
+    // at a finished phase, 400 beside the other warps.
+    auto look = [&](bool keys, bool values, uint32_t n) {
+        keys = keys && ahead % X::kSteps == 0;
+        values = values && n % X::kSteps == 0;
+        const uint32_t t = ahead / X::kSteps, u = 2 * (n / X::kSteps) + 1;
+        uint64_t* const info_bar = &bars.info_full[t % kInfos];
+        uint64_t* const k_bar = &bars.op_full[op_of(2 * t)];
+        uint64_t* const v_bar = &bars.op_full[op_of(u)];
+        uint32_t info_done = 1, k_done = 1, v_done = 1;
+        if (keys) {
+            info_done = bar_done(info_bar, (t / kInfos) & 1);
+            k_done = bar_done(k_bar, op_phase(2 * t));
         }
-        if (t && !bar_wait(&bars.op_full[v_stage], v_phase, &bars.failed)) return false;
-        for (int w = 0; w < tiles; ++w) {
-            if (t) {
-                if (!bar_wait(&bars.p_full[w], (t - 1) & 1, &bars.failed)) return false;
-                fence_after();
-                const uint64_t b = operand_across(ops + v_stage * X::kOp, kBlock);
+        if (values) v_done = bar_done(v_bar, op_phase(u));
+        if (!info_done && !bar_wait(info_bar, (t / kInfos) & 1, &bars.failed)) return false;
+        if (keys) ahead_flags = bars.info[t % kInfos].flags;
+        if (!k_done && !bar_wait(k_bar, op_phase(2 * t), &bars.failed)) return false;
+        return v_done || bar_wait(v_bar, op_phase(u), &bars.failed);
+    };
+    uint32_t n = 0;  // the step whose output comes next
+    for (bool all = false; !all;) {
+        // ---- a unit: its first two steps' scores
+        unit_done = false;
+        if (!look(true, true, n) || !bar_wait(&bars.q_full[w], q_phase, &bars.failed)) return false;
+        q_phase ^= 1;
+        fence_after();
+        scores();
+        if (!unit_done) {
+            if (!look(true, false, n)) return false;
+            fence_after();
+            scores();
+        }
+        const uint32_t first = n;
+        bool more = !unit_done;
+        if (more && !look(true, false, n)) return false;
+        for (;;) {
+            const uint32_t u = 2 * (n / X::kSteps) + 1, half = n % X::kSteps;
+            if (!bar_wait(&bars.p_full[w][n & 1], (n >> 1) & 1, &bars.failed)) return false;
+            fence_after();
+            const uint64_t b = operand_across(ops + op_of(u) * X::kOp + half * (X::kStep * 128), kBlock);
 #pragma unroll
-                for (int k = 0; k < X::kTokens / 16; ++k)
-                    mma_f16(tmem + X::kO + w * D, tmem + X::kP + w * 128 + k * 8, b + k * (2048 / 16), o_desc, k != 0);
-                commit_to(&bars.o_full[w]);
-            }
-            if (more) {
-                if (fresh) {
-                    if (!bar_wait(&bars.q_full[w], q_phase[w], &bars.failed)) return false;
-                    q_phase[w] ^= 1;
-                }
-                fence_after();
-                scores(w, k_stage);
-            }
+            for (int k = 0; k < X::kStep / 16; ++k)
+                mma_f16(tmem + X::kO + w * D, tmem + X::kP + w * 128 + (n & 1) * X::kPStep + k * 8, b + k * (2048 / 16), o_desc,
+                        k != 0 || n != first);
+            commit_to(&bars.o_full[w][n & 1]);
+            if (half == X::kSteps - 1) commit_to(&bars.op_empty[op_of(u)]);
+            if (more) scores();
+            if (++n == ahead) break;
+            more = !unit_done;
+            if (!look(more, true, n)) return false;
         }
-        if (t) commit_to(&bars.op_empty[v_stage]);
-        if (!more) return true;
-        commit_to(&bars.op_empty[k_stage]);
-        flags = bars.info[t % kInfos].flags;
-        fresh = flags & 1;
+        all = ahead_flags & 2;
     }
+    return true;
 }
 
 template <int D>
@@ -171,7 +206,6 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     uint8_t* const dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
     uint8_t* const q_tiles = dyn;
     uint8_t* const ops = dyn + X::kTiles * X::kQ;
-    uint8_t* const raws = ops + X::kOps * X::kOp;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t from = cut_of(a.total, blockIdx.x, a.pieces), to = cut_of(a.total, blockIdx.x + 1, a.pieces);
     const int tiles = X::kTiles == 2 && a.rows > 128 ? 2 : 1;  // of rows
@@ -179,20 +213,21 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             bar_init(&bars.q_full[i], D == 256 ? 8 : 4);
-            bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.p_full[i], D == 256 ? 8 : 4);
-            bar_init(&bars.o_full[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                bar_init(&bars.s_full[i][b], 1);
+                bar_init(&bars.o_full[i][b], 1);
+                bar_init(&bars.p_full[i][b], D == 256 ? 8 : 4);
+            }
         }
         for (int i = 0; i < 8; ++i) {
-            bar_init(&bars.raw_full[i], 1);
-            bar_init(&bars.raw_empty[i], 4);
-        }
-        for (int i = 0; i < 6; ++i) {
             bar_init(&bars.op_full[i], 4);
-            bar_init(&bars.op_empty[i], 1);
+            bar_init(&bars.op_empty[i], tiles);
         }
-        for (int i = 0; i < kInfos; ++i) bar_init(&bars.info_full[i], 1);
-        bar_init(&bars.drained, 1);
+        for (int i = 0; i < kInfos; ++i) {
+            bar_init(&bars.info_full[i], 1);
+            bar_init(&bars.info_empty[i], D == 256 ? 8 : 4 * tiles);
+        }
+        for (int i = 0; i < 2; ++i) bar_init(&bars.drained[i], 1);
         bars.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_operands();
@@ -209,160 +244,195 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
 
     if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kIssueRegs));
-        if (warp == 12 && elect_one()) {
-            // ---- products
-            if (!issue_prefix<D>(bars, shared_of(q_tiles), shared_of(ops), tmem, tiles)) {
-                commit_to(&bars.drained);
+        if (warp - 12 < tiles && elect_one()) {
+            // ---- products: a thread for each tile of rows, in warps that wait for nobody
+            if (!issue_prefix<D>(bars, shared_of(q_tiles), shared_of(ops), tmem, warp - 12)) {
+                commit_to(&bars.drained[warp - 12]);
                 uint32_t quiet = 0;
-                bar_wait(&bars.drained, 0, &quiet);
+                bar_wait(&bars.drained[warp - 12], 0, &quiet);
             }
         }
-        if (warp == 13) {
-            // ---- copies: a lane for each page of a chunk, whose number and scales are loaded ahead
+        if (warp == 14) {
+            // ---- tiles: a lane for each page of a chunk, whose number and scales are loaded ahead
             const int ps = a.c.page_size, span = ps < X::kTokens ? ps : X::kTokens, per = X::kTokens / span;
-            int id[2] = {-1, -1};  // of this chunk and the next
-            float key = 0.0f, val = 0.0f;
-            auto pages_of = [&](int64_t c, int64_t& head, int& first, int& offset, int& n) {
-                const int64_t unit = c / a.chunks;
-                const int64_t token = (c - unit * a.chunks) * X::kTokens;
-                head = unit / a.row_groups;
-                first = static_cast<int>(token / ps);
-                offset = static_cast<int>(token - int64_t{first} * ps);
-                n = a.prefix_pages - first < per ? a.prefix_pages - first : per;
+            const int ps_shift = 31 - __clz(ps), span_shift = 31 - __clz(span);
+            struct Place {  // of a chunk; stepped on, since its divisions take longer than a tile
+                int64_t c;
+                int head, group, chunk;
             };
-            auto load_id = [&](int64_t c) {
-                int64_t head;
-                int first, offset, n;
-                if (c >= to) return -1;
-                pages_of(c, head, first, offset, n);
-                return lane < n ? __ldg(a.pages + first + lane) : -1;
+            Place now;
+            now.c = from;
+            now.chunk = static_cast<int>(from % a.chunks);
+            now.head = static_cast<int>(from / a.chunks / a.row_groups);
+            now.group = static_cast<int>(from / a.chunks % a.row_groups);
+            auto step = [&](Place p) {
+                ++p.c;
+                if (++p.chunk == a.chunks) {
+                    p.chunk = 0;
+                    if (++p.group == a.row_groups) {
+                        p.group = 0;
+                        ++p.head;
+                    }
+                }
+                return p;
             };
-            auto load_scales = [&](int64_t c, int page, float& k, float& v) {
+            auto first_of = [&](const Place& p) { return static_cast<int>((int64_t{p.chunk} * X::kTokens) >> ps_shift); };
+            auto count_of = [&](int first) { return a.prefix_pages - first < per ? a.prefix_pages - first : per; };
+            auto load_id = [&](const Place& p) {
+                const int first = first_of(p);
+                return p.c < to && lane < count_of(first) ? __ldg(a.pages + first + lane) : -1;
+            };
+            auto load_scales = [&](const Place& p, int page, float& k, float& v) {
                 k = __int_as_float(0x7FC00000);  // a bad page spoils every row, through its scores
                 v = 1.0f;
-                if (c >= to || static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.c.pages)) return;
-                const int64_t at = static_cast<int64_t>(page) * a.c.heads + c / a.chunks / a.row_groups;
+                if (p.c >= to || static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.c.pages)) return;
+                const int64_t at = static_cast<int64_t>(page) * a.c.heads + p.head;
                 k = __ldg(a.c.k_scale + at);
                 v = __ldg(a.c.v_scale + at);
             };
-            id[0] = load_id(from);
-            id[1] = load_id(from + 1);
-            load_scales(from, id[0], key, val);
+            // the page of this chunk, of the next and of the one after it; this one's scales
+            Place next = step(now), after = step(next);
+            int id = load_id(now), id_next = load_id(next);
+            float key = 0.0f, val = 0.0f;
+            load_scales(now, id, key, val);
             uint32_t t = 0;
             bool ok = true;
-            for (int64_t c = from; ok && c < to; ++c) {
+            float value = 0.0f;  // the reference of the value scales; 0: none yet
+            while (ok && now.c < to) {
+                if (now.chunk == 0) value = 0.0f;
                 float key_next, val_next;
-                load_scales(c + 1, id[1], key_next, val_next);
-                const int id_next = load_id(c + 2);
-                int64_t head;
-                int first, offset, n;
-                pages_of(c, head, first, offset, n);
-                const bool good = lane < n && static_cast<uint32_t>(id[0]) < static_cast<uint32_t>(a.c.pages);
+                load_scales(next, id_next, key_next, val_next);
+                const int id_after = load_id(after);
+                const int first = first_of(now), n = count_of(first);
+                const int offset = (now.chunk * X::kTokens) & (ps - 1);  // where pages are larger than a tile
+                const bool good = lane < n && static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.pages);
                 if (lane < n && !good && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
-                const int64_t at = (good ? id[0] : 0) * a.c.page_stride + head * a.c.head_stride + int64_t{offset} * D;
-                const bool unit_ends = (c + 1) % a.chunks == 0 || c + 1 == to;
+                const int64_t at = (good ? id : 0) * a.c.page_stride + now.head * a.c.head_stride + int64_t{offset} * D;
+                const bool ends_all = next.c == to, unit_ends = next.chunk == 0 || ends_all;
                 for (int start = 0; ok && start < n; ++t) {
-                    // the pages from `start` on whose scales go together
-                    float hi = lane >= start && lane < n ? val : 0.0f, lo = hi;
+                    // the pages from `start` on whose scales go with the reference, or with one another
+                    bool apart = lane > start && lane < n;
+                    const float v0 = __shfl_sync(0xFFFFFFFFu, val, start);
+                    const bool stays = v0 <= value && v0 * kSpread >= value;
+                    if (stays) {
+                        apart = apart && !(val <= value && val * kSpread >= value);
+                    } else {
+                        float hi = lane >= start && lane < n ? val : 0.0f, lo = hi;
 #pragma unroll
-                    for (int m = 1; m < 8; m <<= 1) {
-                        const float h = __shfl_up_sync(0xFFFFFFFFu, hi, m), l = __shfl_up_sync(0xFFFFFFFFu, lo, m);
-                        if (lane - m >= start) {
-                            hi = fmaxf(hi, h);
-                            lo = fminf(lo, l);
+                        for (int m = 1; m < 8; m <<= 1) {
+                            const float h = __shfl_up_sync(0xFFFFFFFFu, hi, m), l = __shfl_up_sync(0xFFFFFFFFu, lo, m);
+                            if (lane - m >= start) {
+                                hi = fmaxf(hi, h);
+                                lo = fminf(lo, l);
+                            }
                         }
+                        apart = apart && hi > kSpread * lo;
+                        const uint32_t ends = __ballot_sync(0xFFFFFFFFu, apart);
+                        value = __shfl_sync(0xFFFFFFFFu, hi, ends ? __ffs(ends) - 2 : n - 1);
                     }
-                    const uint32_t apart = __ballot_sync(0xFFFFFFFFu, lane > start && lane < n && hi > kSpread * lo);
-                    const int end = apart ? __ffs(apart) - 1 : n;
-                    const float top = __shfl_sync(0xFFFFFFFFu, hi, end - 1);
-                    const uint32_t ks = 2 * t % X::kRaws, vs = (2 * t + 1) % X::kRaws, phase = (2 * t / X::kRaws & 1) ^ 1;
-                    ok = warp_wait(&bars.raw_empty[ks], phase, &bars.failed) && warp_wait(&bars.raw_empty[vs], phase, &bars.failed);
+                    const uint32_t ends = __ballot_sync(0xFFFFFFFFu, apart);
+                    const int end = ends ? __ffs(ends) - 1 : n;
+                    ok = warp_wait(&bars.info_empty[t % kInfos], (t / kInfos & 1) ^ 1, &bars.failed);
                     if (!ok) break;
                     Info& info = bars.info[t % kInfos];
-                    const int page = start + lane * 16 / span;  // of the lane's 16 tokens
+                    const int page = start + (lane * 16 >> span_shift);  // of the lane's 16 tokens
                     const float k16 = __shfl_sync(0xFFFFFFFFu, key, page & 31), v16 = __shfl_sync(0xFFFFFFFFu, val, page & 31);
                     if (lane < X::kGranules) {
-                        const float lift = kLiftLog + (v16 == top ? 0.0f : __log2f(v16 / top));
-                        info.key[lane] = k16;
-                        info.lift[lane] = lift;
+                        const bool there = page < end;
+                        const float lift = kLift + (v16 == value ? 0.0f : __log2f(v16 / value));
+                        info.key[lane] = there ? k16 : 0.0f;
+                        info.lift[lane] = there ? lift : -kAlone;
+                        info.back[lane] = there ? ex2(-lift) : 0.0f;
                     }
                     if (lane == 0) {
-                        info.tokens = (end - start) * span;
-                        info.flags = end == n && unit_ends ? (c + 1 == to ? 3 : 1) : 0;
-                        info.value = top * (1.0f / (1 << kLiftLog));
+                        info.tokens = (end - start) << span_shift;
+                        info.flags = (end == n && unit_ends ? (ends_all ? 3 : 1) : 0) | (stays ? 0 : 4);
+                        info.value = value;
+                        info.value_log = __log2f(value);
                     }
-                    const bool mine = good && lane >= start && lane < end;
-                    const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, mine)) * span * D;
+                    if (lane >= start && lane < end) info.at[lane - start] = good ? at : -1;
                     __syncwarp();
-                    if (lane == 0) {
-                        bar_arrive(&bars.info_full[t % kInfos]);
-                        bar_expect(&bars.raw_full[ks], bytes);
-                        bar_expect(&bars.raw_full[vs], bytes);
-                    }
-                    __syncwarp();
-                    if (mine) {
-                        const uint32_t dst = shared_of(raws) + (lane - start) * span * D;
-                        bulk_copy(dst + ks * X::kRaw, static_cast<const char*>(a.c.k) + at, span * D, &bars.raw_full[ks]);
-                        bulk_copy(dst + vs * X::kRaw, static_cast<const char*>(a.c.v) + at, span * D, &bars.raw_full[vs]);
-                    }
+                    if (lane == 0) bar_arrive(&bars.info_full[t % kInfos]);
                     start = end;
                 }
-                id[0] = id[1];
-                id[1] = id_next;
+                id = id_next;
+                id_next = id_after;
                 key = key_next;
                 val = val_next;
+                now = next;
+                next = after;
+                after = step(after);
             }
-            // a failed block still waits for its copies in flight before its memory goes away
-            if (!ok)
-                for (uint32_t i = 0; i < X::kRaws && i < 2 * t; ++i) {
-                    const uint32_t u = 2 * t - 1 - i;
-                    uint32_t quiet = 0;
-                    bar_wait(&bars.raw_full[u % X::kRaws], (u / X::kRaws) & 1, &quiet);
-                }
         }
         __syncwarp();
     } else if (warp >= 8) {
         // ---- codes to fp16: 64 values a row of 128 bytes, its 16-byte chunks permuted by the token
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(X::kConvertRegs));
         const int me = tid - 256;
-        constexpr int kChunks = D / 16;  // 16 codes each, of a token
-        bool ok = true, last = false;
-        for (uint32_t t = 0; ok && !last; ++t) {
-            ok = warp_wait(&bars.info_full[t % kInfos], (t / kInfos) & 1, &bars.failed);
-            if (!ok) break;
-            const int tokens = bars.info[t % kInfos].tokens;
-            last = bars.info[t % kInfos].flags & 2;
-#pragma unroll 1
-            for (uint32_t u = 2 * t; u < 2 * t + 2; ++u) {
-                const uint32_t rs = u % X::kRaws, os = u % X::kOps;
-                ok = warp_wait(&bars.raw_full[rs], (u / X::kRaws) & 1, &bars.failed);
-                if (ok) ok = warp_wait(&bars.op_empty[os], ((u / X::kOps) & 1) ^ 1, &bars.failed);
-                if (!ok) break;
-                const uint8_t* src = raws + rs * X::kRaw;
-                uint8_t* dst = ops + os * X::kOp;
-#pragma unroll 4
-                for (int j = 0; j < X::kTokens * kChunks / 128; ++j) {
-                    const int i = j * 128 + me, token = i / kChunks, chunk = i % kChunks;
-                    uint4 x = *reinterpret_cast<const uint4*>(src + i * 16);
-                    if (token >= tokens) x = make_uint4(0, 0, 0, 0);
-                    uint32_t h[8];
-                    e4m3x4_to_half2(x.x, h[0], h[1]);
-                    e4m3x4_to_half2(x.y, h[2], h[3]);
-                    e4m3x4_to_half2(x.z, h[4], h[5]);
-                    e4m3x4_to_half2(x.w, h[6], h[7]);
-                    uint8_t* row = dst + (chunk >> 2) * (X::kTokens * 128) + token * 128;
-                    const int c0 = (chunk & 3) * 2, odd = (chunk >> 2) & 1;  // lanes of two blocks meet in no bank
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    *reinterpret_cast<uint4*>(row + (((c0 + odd) ^ (token & 7)) * 16)) = odd ? hi : lo;
-                    *reinterpret_cast<uint4*>(row + (((c0 + (odd ^ 1)) ^ (token & 7)) * 16)) = odd ? lo : hi;
-                }
-                fence_operands();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(&bars.op_full[os]);
-                    bar_arrive(&bars.raw_empty[rs]);
-                }
+        constexpr int N = X::kEach;
+        // Four lanes take 64 values of a token and a warp eight tokens at a time, so that eight lanes' stores, of an even
+        // and an odd token, meet in no bank; the blocks of 64 values one after another.
+        constexpr int kTurns = X::kTokens / 32;  // of the 128 threads through a block's tokens
+        auto token_of = [&](int j) { return (j % kTurns) * 32 + (me >> 2); };
+        auto chunk_of = [&](int j) { return (j / kTurns) * 4 + (me & 3); };
+        const int ps = a.c.page_size, span = ps < X::kTokens ? ps : X::kTokens, shift = 31 - __clz(span);
+        uint4 k[N], v[N];
+        auto load = [&](uint32_t t, const void* from, uint4 (&x)[N]) {
+            const Info& info = bars.info[t % kInfos];
+            const int tokens = info.tokens;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int token = token_of(j), chunk = chunk_of(j);
+                const int64_t at = token < tokens ? info.at[token >> shift] : -1;
+                x[j] = at < 0 ? make_uint4(0, 0, 0, 0)
+                              : load_past_l1(static_cast<const char*>(from) + at + (token & (span - 1)) * D + chunk * 16);
             }
+        };
+        uint32_t os = 0, phase = 1;
+        auto convert = [&](const uint4 (&x)[N]) {
+            if (!warp_wait(&bars.op_empty[os], phase, &bars.failed)) return false;
+            uint8_t* dst = ops + os * X::kOp;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int token = token_of(j), chunk = chunk_of(j);
+                uint32_t h[8];
+                e4m3x4_to_half2(x[j].x, h[0], h[1]);
+                e4m3x4_to_half2(x[j].y, h[2], h[3]);
+                e4m3x4_to_half2(x[j].z, h[4], h[5]);
+                e4m3x4_to_half2(x[j].w, h[6], h[7]);
+                uint8_t* row = dst + (chunk >> 2) * (X::kTokens * 128) + token * 128;
+                const int at = (((chunk & 3) * 2) ^ (token & 7)) * 16;
+                *reinterpret_cast<uint4*>(row + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(row + (at ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            fence_operands();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bars.op_full[os]);
+            if (++os == X::kOps) {
+                os = 0;
+                phase ^= 1;
+            }
+            return true;
+        };
+        bool ok = warp_wait(&bars.info_full[0], 0, &bars.failed), last = !ok;
+        if (ok) {
+            load(0, a.c.k, k);
+            load(0, a.c.v, v);
+            last = bars.info[0].flags & 2;
+        }
+#pragma unroll 1
+        for (uint32_t t = 1; ok; ++t) {  // tile t - 1 is converted while tile t is loaded
+            const bool more = !last;
+            if (more) {
+                ok = warp_wait(&bars.info_full[t % kInfos], (t / kInfos) & 1, &bars.failed);
+                if (!ok) break;
+                last = bars.info[t % kInfos].flags & 2;
+            }
+            ok = convert(k);
+            if (ok && more) load(t, a.c.k, k);
+            if (ok) ok = convert(v);
+            if (!more) break;
+            if (ok) load(t, a.c.v, v);
         }
     } else {
         // ---- softmax and sums: a thread a row
@@ -411,16 +481,18 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                     top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                 }
                 if constexpr (D == 256) {
-                    bars.top[who][r] = top;
+                    // (the halves of a row meet where the last unit's queries were)
+                    float* const tops = reinterpret_cast<float*>(q_tiles);
+                    tops[who * 128 + r] = top;
                     asm volatile("bar.sync 1, 256;" ::: "memory");
-                    top = fmaxf(top, bars.top[who ^ 1][r]);
+                    top = fmaxf(top, tops[(who ^ 1) * 128 + r]);
                     asm volatile("bar.sync 1, 256;" ::: "memory");
                 }
                 // 2^(14 - exponent), kept inside fp32's normal range
                 const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
                 const int up = top == 0.0f ? 0 : (14 - ex > 126 ? 126 : (14 - ex < -113 ? -113 : 14 - ex));
-                const float f = exp2i(up);
-                back = exp2i(-up) * a.scale;
+                const float f = a.scale < 0.0f ? -exp2i(up) : exp2i(up);  // the scale's sign goes with the queries
+                back = exp2i(-up) * fabsf(a.scale);
 #pragma unroll
                 for (int i = 0; i < C / 8; ++i) {
                     uint32_t h[4];
@@ -437,106 +509,130 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) bar_arrive(&bars.q_full[w]);
             }
-            uint64_t o[C / 2];
-#pragma unroll
-            for (int i = 0; i < C / 2; ++i) o[i] = 0;
-            float m = kNothing, l = 0.0f;
-            for (bool unit_ends = false; ok && !unit_ends; ++t) {
-                ok = warp_wait(&bars.info_full[t % kInfos], (t / kInfos) & 1, &bars.failed);
-                if (!ok) break;
+            // the row's reference, its largest score, the largest of score and value scale, the sum relative to m
+            float ref = 0.0f, m = kNothing, peak = kNothing, l = 0.0f, value = 1.0f, value_log = 0.0f;
+            bool fresh = true;
+            ok = ok && warp_wait(&bars.info_full[t % kInfos], (t / kInfos) & 1, &bars.failed);
+            while (ok) {
                 const Info& info = bars.info[t % kInfos];
-                const int granules = info.tokens >> 4;
-                const float value = info.value;
-                unit_ends = info.flags & 1;
-                ok = warp_wait(&bars.s_full[w], t & 1, &bars.failed);
-                if (!ok) break;
-                fence_after();
-                float top = kNothing;
+                const int granules = info.tokens >> 4, flags = info.flags;
+#pragma unroll 1
+                for (int half = 0; half < X::kSteps; ++half) {
+                    const uint32_t n = t * X::kSteps + half;
+                    const uint32_t s_now = s_at + (n & 1) * 64, p_now = p_at + (n & 1) * X::kPStep;
+                    const float4 key = *reinterpret_cast<const float4*>(&info.key[4 * half]);
+                    const float4 lift = *reinterpret_cast<const float4*>(&info.lift[4 * half]);
+                    const float keys[4] = {key.x * back, key.y * back, key.z * back, key.w * back};
+                    const float4 unlift = *reinterpret_cast<const float4*>(&info.back[4 * half]);
+                    const float lifts[4] = {lift.x, lift.y, lift.z, lift.w};
+                    const float unlifts[4] = {unlift.x, unlift.y, unlift.z, unlift.w};
+                    const int left = granules - 4 * half;  // groups of 16 tokens that there are
+                    ok = warp_wait(&bars.s_full[w][n & 1], (n >> 1) & 1, &bars.failed);
+                    if (!ok) break;
+                    fence_after();
+                    uint32_t s[2][32];
+                    tmem_load32(s_now, s[0]);
+                    tmem_load32(s_now + 32, s[1]);
+                    tmem_wait_load32(s[0]);
+                    tmem_wait_load32(s[1]);
+                    float hi[4] = {kNothing, kNothing, kNothing, kNothing}, top = kNothing;
 #pragma unroll
-                for (int b = 0; b < X::kTokens / 32; ++b) {
-                    if (2 * b >= granules) break;
-                    uint32_t s[32];
-                    tmem_load32(s_at + 32 * b, s);
-                    tmem_wait_load32(s);
-                    // (the key scale is positive, the row's factor has the sign of the call's)
+                    for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (2 * b + h >= granules) break;
-                        const float f = info.key[2 * b + h] * back;
-                        float hi = __uint_as_float(s[16 * h]) * f;
+                        for (int g = 0; g < 4; ++g)
+                            hi[g] = max3(hi[g], __uint_as_float(s[g >> 1][16 * (g & 1) + 2 * i]),
+                                         __uint_as_float(s[g >> 1][16 * (g & 1) + 2 * i + 1]));
 #pragma unroll
-                        for (int i = 1; i < 16; ++i) hi = fmaxf(hi, __uint_as_float(s[16 * h + i]) * f);
-                        top = fmaxf(top, hi);
-                    }
-                }
-                float sum = 0.0f;
-#pragma unroll
-                for (int b = 0; b < X::kTokens / 32; ++b) {
-                    uint32_t p[16];
-                    if (2 * b < granules) {
-                        uint32_t s[32];
-                        tmem_load32(s_at + 32 * b, s);
-                        tmem_wait_load32(s);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (2 * b + h < granules) {
-                                const float f = info.key[2 * b + h] * back, add = info.lift[2 * b + h] - top;
-                                float part = 0.0f;
+                    for (int g = 0; g < 4; ++g) top = fmaxf(top, g < left ? hi[g] * keys[g] : kNothing);
+                    const bool move = left > 0 && (((flags & 4) && half == 0) || top > ref + kAbove || top < ref - kBelow);
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+                        const float old = ref, old_value = value_log;
+                        value = info.value;
+                        value_log = info.value_log;
+                        if (fresh) {
+                            ref = top + kRoom;
+                        } else {
+                            if (move) ref = fmaxf(top + kRoom, peak - kSpan - value_log);
+                            ok = warp_wait(&bars.o_full[w][(n - 1) & 1], ((n - 1) >> 1) & 1, &bars.failed);
+                            if (!ok) break;
+                            fence_after();
+                            const float f = ex2((old - ref) + (old_value - value_log));
+                            const uint64_t f2 = pack2(f, f);
+#pragma unroll 1
+                            for (int b = 0; b < C / 16; ++b) {
+                                uint32_t y[16];
+                                tmem_load16(o_at + 16 * b, y);
+                                tmem_wait_load16(y);
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
-                                    const float e0 = ex2(fmaf(__uint_as_float(s[16 * h + 2 * i]), f, add));
-                                    const float e1 = ex2(fmaf(__uint_as_float(s[16 * h + 2 * i + 1]), f, add));
-                                    part += e0 + e1;
-                                    p[8 * h + i] = Half<ARC_F16>::pack(e0, e1);
+                                    const uint64_t z = mul2(pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), f2);
+                                    y[2 * i] = static_cast<uint32_t>(z);
+                                    y[2 * i + 1] = static_cast<uint32_t>(z >> 32);
                                 }
-                                sum = fmaf(part, ex2(-info.lift[2 * b + h]), sum);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) p[8 * h + i] = 0;
+                                tmem_store16(o_at + 16 * b, y);
                             }
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) p[i] = 0;
                     }
-                    if (D != 256 || b == who) tmem_store16(p_at + 16 * b, p);
+                    fresh = false;
+                    if (left > 0) peak = fmaxf(peak, top + value_log);
+                    const float now = fmaxf(m, top);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int g = 2 * b + h;
+                            const float add = lifts[g] - ref;
+                            const uint64_t f2 = pack2(keys[g], keys[g]), add2 = pack2(add, add);
+                            float part[2] = {0.0f, 0.0f};
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const uint64_t z = fma2(pack2(__uint_as_float(s[b][16 * h + 2 * i]),
+                                                              __uint_as_float(s[b][16 * h + 2 * i + 1])), f2, add2);
+                                const float e0 = ex2(half_of(z, 0)), e1 = ex2(half_of(z, 1));
+                                part[0] += e0;
+                                part[1] += e1;
+                                p[8 * h + i] = Half<ARC_F16>::pack(e0, e1);
+                            }
+                            sum = fmaf(part[0] + part[1], unlifts[g], sum);
+                        }
+                        if (D != 256 || b == who) tmem_store16(p_now + 16 * b, p);
+                    }
+                    tmem_wait_store();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&bars.p_full[w][n & 1]);
+                        if (half + 1 == X::kSteps) bar_arrive(&bars.info_empty[t % kInfos]);
+                    }
+                    l = fmaf(l, ex2(m - now), sum * ex2(ref - now));
+                    m = now;
                 }
-                tmem_wait_store();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&bars.p_full[w]);
-                // what the sums so far and this tile's count from here on
-                const float now = fmaxf(m, top), old = ex2(m - now), add = ex2(top - now);
-                m = now;
-                l = fmaf(l, old, sum * add);
-                ok = warp_wait(&bars.o_full[w], t & 1, &bars.failed);
                 if (!ok) break;
+                ++t;
+                if (flags & 1) break;
+                ok = warp_wait(&bars.info_full[t % kInfos], (t / kInfos) & 1, &bars.failed);
+            }
+            // ---- the unit's partial
+            const uint32_t last = t * X::kSteps - 1;
+            if (ok) ok = warp_wait(&bars.o_full[w][last & 1], (last >> 1) & 1, &bars.failed);
+            if (ok) {
                 fence_after();
-                const uint64_t f2 = pack2(add * value, add * value);
-                const bool grown = __any_sync(0xFFFFFFFFu, old != 1.0f);
-                const uint64_t old2 = pack2(old, old);
+                const float f = ex2(ref - m) * (value * (1.0f / 4096.0f)) / l;  // (the weights have 2^kLift)
+                float4* out = reinterpret_cast<float4*>(a.slots) + ((slot * X::kTiles + w) * (D / 4) + o0 / 4) * 128 + r;
 #pragma unroll
                 for (int b = 0; b < C / 32; ++b) {
                     uint32_t y[32];
                     tmem_load32(o_at + 32 * b, y);
                     tmem_wait_load32(y);
-                    if (grown) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[16 * b + i] = mul2(o[16 * b + i], old2);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[16 * b + i] = fma2(pack2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), f2, o[16 * b + i]);
+                    for (int i = 0; i < 8; ++i)
+                        out[(8 * b + i) * 128] = make_float4(__uint_as_float(y[4 * i]) * f, __uint_as_float(y[4 * i + 1]) * f,
+                                                             __uint_as_float(y[4 * i + 2]) * f, __uint_as_float(y[4 * i + 3]) * f);
                 }
                 fence_before();
             }
-            // ---- the unit's partial
-            const float inv = 1.0f / l;
-            float4* out = reinterpret_cast<float4*>(a.slots) + ((slot * X::kTiles + w) * (D / 4) + o0 / 4) * 128 + r;
-#pragma unroll
-            for (int i = 0; i < C / 4; ++i)
-                out[i * 128] = make_float4(half_of(o[2 * i], 0) * inv, half_of(o[2 * i], 1) * inv, half_of(o[2 * i + 1], 0) * inv,
-                                           half_of(o[2 * i + 1], 1) * inv);
             if (D != 256 || who == 0)
                 a.slot_logs[slot * X::kRows + w * 128 + r] = ok ? m + __log2f(l) : __int_as_float(0x7FC00000);
         }

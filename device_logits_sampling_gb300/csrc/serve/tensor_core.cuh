@@ -73,6 +73,12 @@ __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_
                  "r"(bytes), "r"(shared_of(bar))
                  : "memory");
 }
+// Read-only bytes that are used once: nothing of them stays in L1, which is what shared memory leaves of it.
+__device__ __forceinline__ uint4 load_past_l1(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
 // Plain stores to shared memory before what the tensor cores read.
 __device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 #define ARC_REGS8(x, o) "r"(x[o]), "r"(x[o + 1]), "r"(x[o + 2]), "r"(x[o + 3]), "r"(x[o + 4]), "r"(x[o + 5]), "r"(x[o + 6]), "r"(x[o + 7])
@@ -107,10 +113,18 @@ __device__ __forceinline__ void tmem_wait_load32(uint32_t (&x)[32]) {
                  :
                  : "memory");
 }
+__device__ __forceinline__ void tmem_wait_load16(uint32_t (&x)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : ARC_BOTH8(x, 0), ARC_BOTH8(x, 8) : : "memory");
+}
 #undef ARC_BOTH8
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
