@@ -2,9 +2,16 @@
 //
 // A block has a slice of a row.  It reads the row's lists once, keeps those of its ids in two tables in shared memory
 // (how often the history has the id; the last bias entry for it, so that the order in which entries arrive does not
-// matter) and marks each group of eight ids that has one.  Then it streams: eight ids are one byte of the mask, one
-// byte of marks and 16 bytes of 16-bit logits.  Eight disallowed ids are written without being read; in place, eight
-// that are allowed and unmarked are not touched at all.
+// matter) and marks each group of eight ids that has one; the slice's logits and mask are under way meanwhile.  Eight ids
+// are one byte of the mask, one byte of marks and 16 bytes of 16-bit logits.  Eight disallowed ids are written without
+// being read; in place, eight that are allowed and unmarked are not touched at all.
+//
+// Bounds and figures.  A mask alone, in place, 100 x 100,003 fp32: 10.0 us, faster than its 81 MB at the measured copy
+// rate (12.1), since what it takes out is not read.  256 rows x 129,280 with histories of up to 4,096 ids, up to 300
+// biases and masks: 56 us (20.5 of traffic): every block of a row goes through the row's lists, and six blocks an SM, whose
+// tables fill its shared memory, hide no more of that than they do.  One row 5.8 us: four loads that wait for one another.
+// Measured and left: a second kernel with a hash table a row that edits behind the stream (54 us for the batch, 12 for the
+// row), edits from the lists instead of marks (66 to 80), one table of counts and entries in one word (73).
 //
 // Rows of an odd vocabulary begin anywhere: the groups of eight are laid on the 16-byte boundaries of the output, the
 // mask's byte is cut out of two, and logits that are not aligned alike are read one by one.
@@ -21,9 +28,17 @@ namespace {
 using namespace arcs;
 
 constexpr int kThreads = 256;
-constexpr int kGroups = 4;                          // groups of eight a thread has
-constexpr int kSlice = kThreads * kGroups;          // groups of a block
-constexpr int kIds = kSlice * 8;
+
+// G: groups of eight ids a thread has.
+template <int G>
+struct Slice {
+    static constexpr int kSlice = kThreads * G, kIds = kSlice * 8;  // groups and ids of a block
+    struct Tables {
+        uint32_t count[kIds];  // of the history
+        uint32_t entry[kIds];  // 1 + the last bias entry
+        uint8_t marks[kSlice];
+    };
+};
 
 struct EditArgs {
     arc_logit_edits e;
@@ -32,12 +47,6 @@ struct EditArgs {
     int64_t B, V, ld, out_ld;
     uint32_t* err;
     int32_t in_place;
-};
-
-struct Tables {
-    uint32_t count[kIds];  // of the history
-    uint32_t entry[kIds];  // 1 + the last bias entry
-    uint8_t marks[kSlice];
 };
 
 template <int DT>
@@ -74,10 +83,12 @@ __device__ __forceinline__ bool part_of(const int32_t* offsets, int64_t row, int
 
 __device__ __forceinline__ bool in_range(float x) { return fabsf(x) <= 3.4028235e38f; }
 
-template <int DT, int OT, bool LISTS>
+template <int DT, int OT, bool LISTS, int G>
 __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ EditArgs a) {
     using T = typename Type<DT>::T;
     using O = typename Type<OT>::T;
+    using Tables = typename Slice<G>::Tables;
+    constexpr int kIds = Slice<G>::kIds;
     extern __shared__ __align__(16) uint8_t dyn[];
     Tables& tab = *reinterpret_cast<Tables*>(dyn);
     const int tid = threadIdx.x;
@@ -118,33 +129,6 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         }
     }
 
-    const bool lists = LISTS && !nothing && (h1 > h0 || b1 > b0);
-    if (lists) {
-        uint4* z = reinterpret_cast<uint4*>(dyn);
-        for (int i = tid; i < static_cast<int>(sizeof(Tables) / 16); i += kThreads) z[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-        for (int64_t i = h0 + tid; i < h1; i += kThreads) {
-            const int64_t id = __ldg(a.e.hist_ids + i);
-            if (id < 0 || id >= a.V) {
-                err |= ARC_EDIT_ERR_HIST;
-            } else if (static_cast<uint64_t>(id - base) < kIds) {
-                atomicAdd(&tab.count[id - base], 1u);
-                tab.marks[(id - base) >> 3] = 1;
-            }
-        }
-        for (int64_t i = b0 + tid; i < b1; i += kThreads) {
-            const int64_t id = __ldg(a.e.bias_ids + i);
-            if (id < 0 || id >= a.V) {
-                err |= ARC_EDIT_ERR_BIAS;
-            } else if (static_cast<uint64_t>(id - base) < kIds) {
-                atomicMax(&tab.entry[id - base], static_cast<uint32_t>(i - b0 + 1));
-                tab.marks[(id - base) >> 3] = 1;
-            }
-        }
-        __syncthreads();
-    }
-    if (err && first && a.err) atomicOr(a.err, err);
-
     // the mask's eight bits of ids i .. i + 7 (i may lie below 0; no bit from V on is used)
     const int64_t words = (a.V + 31) >> 5;
     auto bits_of = [&](int64_t i) -> uint32_t {
@@ -156,6 +140,76 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         if (s > 24 && w + 1 < words) hi = __ldg(mask + w + 1);
         return __funnelshift_r(lo, hi, s) & 0xFFu;
     };
+    const bool lists = LISTS && !nothing && (h1 > h0 || b1 > b0);
+    // the history's first ids, the mask and the logits are on their way together
+    int32_t early[4] = {0, 0, 0, 0};
+    if (lists) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (h0 + tid + k * kThreads < h1) early[k] = __ldg(a.e.hist_ids + h0 + tid + k * kThreads);
+    }
+    const float none = -__int_as_float(0x7F800000);
+    const bool in_vec = ((reinterpret_cast<uintptr_t>(in) + base * static_cast<int64_t>(sizeof(T))) & 15) == 0;
+    uint32_t bits[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const int64_t i = base + (g * kThreads + tid) * 8;
+        bits[g] = i < a.V ? bits_of(i) : 0;
+    }
+    T x[G][8];
+    auto load = [&](bool late) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int64_t i = base + (g * kThreads + tid) * 8;
+            // (in place, eight that are allowed are read once a list is known to have one of them)
+            if (i >= a.V || bits[g] == 0 || (a.in_place && !late && bits[g] == 0xFFu)) continue;
+            if (late && !(bits[g] == 0xFFu && tab.marks[g * kThreads + tid])) continue;
+            if (in_vec && i >= 0 && i + 8 <= a.V) {
+                const uint4* p = reinterpret_cast<const uint4*>(in + i);
+                uint4* q = reinterpret_cast<uint4*>(x[g]);
+#pragma unroll
+                for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) q[k] = p[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i + k >= 0 && i + k < a.V) x[g][k] = in[i + k];
+            }
+        }
+    };
+    load(false);
+
+    if (lists) {
+        uint4* z = reinterpret_cast<uint4*>(dyn);
+        for (int i = tid; i < static_cast<int>(sizeof(Tables) / 16); i += kThreads) z[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        // a list's ids, four loads of a thread under way at a time
+        auto each = [&](const int32_t* ids, int64_t lo, int64_t hi, uint32_t bit, bool loaded, auto take) {
+            for (int64_t i = lo + tid; i < hi; i += 4 * kThreads) {
+                int32_t id[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    id[k] = loaded ? early[k] : i + k * kThreads < hi ? __ldg(ids + i + k * kThreads) : 0;
+                loaded = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (i + k * kThreads >= hi) break;
+                    if (id[k] < 0 || id[k] >= a.V) {
+                        err |= bit;
+                    } else if (static_cast<uint64_t>(id[k] - base) < kIds) {
+                        const int at = static_cast<int>(id[k] - base);
+                        take(at, static_cast<uint32_t>(i + k * kThreads - lo + 1));
+                        tab.marks[at >> 3] = 1;
+                    }
+                }
+            }
+        };
+        each(a.e.hist_ids, h0, h1, ARC_EDIT_ERR_HIST, true, [&](int at, uint32_t) { atomicAdd(&tab.count[at], 1u); });
+        each(a.e.bias_ids, b0, b1, ARC_EDIT_ERR_BIAS, false, [&](int at, uint32_t e) { atomicMax(&tab.entry[at], e); });
+        __syncthreads();
+    }
+    if (lists && a.in_place) load(true);
+    if (err && first && a.err) atomicOr(a.err, err);
+
     auto edited = [&](float z, int64_t id) {
         const int at = static_cast<int>(id - base);
         const uint32_t c = tab.count[at], e = tab.entry[at];
@@ -167,33 +221,8 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         if (e) z = __fadd_rn(z, __ldg(a.e.bias + b0 + (e - 1)));
         return z;
     };
-    const float none = -__int_as_float(0x7F800000);
-    const bool in_vec = ((reinterpret_cast<uintptr_t>(in) + base * static_cast<int64_t>(sizeof(T))) & 15) == 0;
-    uint32_t bits[kGroups];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        const int64_t i = base + (g * kThreads + tid) * 8;
-        bits[g] = i < a.V ? bits_of(i) : 0;
-    }
-    T x[kGroups][8];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        const int64_t i = base + (g * kThreads + tid) * 8;
-        const bool marked = lists && tab.marks[g * kThreads + tid];
-        if (i >= a.V || bits[g] == 0 || (a.in_place && bits[g] == 0xFFu && !marked)) continue;
-        if (in_vec && i >= 0 && i + 8 <= a.V) {
-            const uint4* p = reinterpret_cast<const uint4*>(in + i);
-            uint4* q = reinterpret_cast<uint4*>(x[g]);
-#pragma unroll
-            for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) q[k] = p[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (i + k >= 0 && i + k < a.V) x[g][k] = in[i + k];
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
+    for (int g = 0; g < G; ++g) {
         const int64_t i = base + (g * kThreads + tid) * 8;
         const bool marked = lists && tab.marks[g * kThreads + tid];
         if (i >= a.V || (a.in_place && bits[g] == 0xFFu && !marked)) continue;
@@ -226,22 +255,27 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
     }
 }
 
-template <int DT, int OT, bool LISTS>
+template <int DT, int OT, bool LISTS, int G>
 int launch(const EditArgs& a, int dev, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     // without tables the whole of an SM's storage holds loads in flight
-    if (arc::prepare(edit_kernel<DT, OT, LISTS>, dev, done, LISTS ? 100 : 0) != cudaSuccess) return ARC_E_CUDA;
+    if (arc::prepare(edit_kernel<DT, OT, LISTS, G>, dev, done, LISTS ? 100 : 0) != cudaSuccess) return ARC_E_CUDA;
     // the short first group shifts the slices by less than one group
-    const int64_t slices = (a.V + 7 + kIds - 1) / kIds;
+    const int64_t slices = (a.V + 7 + Slice<G>::kIds - 1) / Slice<G>::kIds;
     const int64_t ys = a.B < 65535 ? a.B : 65535, zs = (a.B + ys - 1) / ys;
     const dim3 grid(static_cast<unsigned>(slices), static_cast<unsigned>(ys), static_cast<unsigned>(zs));
-    edit_kernel<DT, OT, LISTS><<<grid, kThreads, LISTS ? sizeof(Tables) : 0, st>>>(a);
+    edit_kernel<DT, OT, LISTS, G><<<grid, kThreads, LISTS ? sizeof(typename Slice<G>::Tables) : 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
 }
 
 template <int DT, int OT>
 int launch(const EditArgs& a, int dev, cudaStream_t st) {
-    return a.e.hist_offsets || a.e.bias_offsets ? launch<DT, OT, true>(a, dev, st) : launch<DT, OT, false>(a, dev, st);
+    // Two groups a thread where there are lists: 256 rows x 129,280 55.9 us, 68.1 with one, 76.8 with four; 32 rows 11.7,
+    // 13.1, 15.4; 512 rows 96, 115, 137.  Few rows want more blocks: one row 5.8 us with one, 7.5 with two; 8 rows 7.8 and
+    // 9.5; 16 rows 7.5 and 7.8.  Without lists the numbers lie within 4%.
+    if (a.e.hist_offsets || a.e.bias_offsets)
+        return a.B * a.V <= (5 << 19) ? launch<DT, OT, true, 1>(a, dev, st) : launch<DT, OT, true, 2>(a, dev, st);
+    return launch<DT, OT, false, 1>(a, dev, st);
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }

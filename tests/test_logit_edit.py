@@ -318,3 +318,29 @@ def test_another_stream(cuda_lib):
     got = edit.edit_logits(c.logits, **c.kw, stream=side)
     side.synchronize()
     assert torch.equal(got.cpu().view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,V", [(1, 5001), (3, 40000)])
+def test_long_lists(cuda_lib, rows, V):
+    """A history of a million ids, most of them one id, and thousands of biases that name one id over and over, beside
+    short rows."""
+    import torch
+
+    rng = np.random.default_rng(8)
+    c = Case(rows, V, "float32", mask="most", seed=8)
+    long_hist = np.where(rng.random((1 << 20) + 77) < 0.7, 4321, rng.integers(0, V, (1 << 20) + 77)).astype(np.int32)
+    long_bias = rng.integers(0, 700, 9001).astype(np.int32)
+    hist = [long_hist] + [rng.integers(0, V, 50).astype(np.int32) for _ in range(rows - 1)]
+    bias = [rng.integers(0, V, 3).astype(np.int32) for _ in range(rows - 1)] + [long_bias]
+    for name, lists in (("hist", hist), ("bias", bias)):
+        c.host[name + "_offsets"] = np.concatenate([[0], np.cumsum([len(x) for x in lists])]).astype(np.int32)
+        c.host[name + "_ids"] = np.concatenate(lists)
+    c.host["bias"] = rng.normal(0, 4, len(c.host["bias_ids"])).astype(np.float32)
+    c.host["penalties"] = [(1.1, float(np.float32(1e-5)), 0.25)] * rows
+    kw = {k: torch.from_numpy(c.host[k]).cuda() for k in ("hist_offsets", "hist_ids", "bias_offsets", "bias_ids", "bias")}
+    kw.update(c.kw, params=records(c.host["penalties"]))
+    c.check(edit.edit_logits(c.logits, **kw))
+    want = c.want()[0]
+    edit.edit_logits(c.logits, out=c.logits, **kw)
+    assert np.array_equal(c.logits.cpu().numpy(), want)
