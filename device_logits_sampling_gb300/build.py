@@ -25,7 +25,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("kernels_bf16.cu", "kernels_bf16_hist
 SERVE_LIB = os.path.join(LIBDIR, "libarcserve.so")
 SERVE_SOURCES = [os.path.join(CSRC, "serve", f) for f in ("kv_append.cu", "kv_attend.cu", "kv_sinks.cu", "kv_behind.cu",
                                                            "kv_shared.cu", "w4_matvec.cu",
-                                                           "w4_many.cu", "norm_join.cu", "logit_edit.cu",
+                                                           "w4_many.cu", "norm_join.cu", "norm_bf16.cu", "norm_f16.cu", "logit_edit.cu",
                                                            "arc_serve.cu")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,5 @@
+#include "norm_join.cuh"
+
+int arcs::launch_join_bf16(const JoinArgs& a, Moves moves, int dev, int sms, cudaStream_t st) {
+    return launch_join<ARC_BF16>(a, moves, dev, sms, st);
+}
