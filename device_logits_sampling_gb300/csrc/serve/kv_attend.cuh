@@ -267,10 +267,17 @@ struct Cursor {
     // under the call, the piece ends at the last sequence.
     __device__ __forceinline__ void next_item(const AttendArgs& a) {
         unit = 0;
-        if (++head < a.c.heads) return;
-        head = 0;
-        if (++tile < q.tiles) return;
-        tile = 0;
+        if constexpr (MODE == kSinks) {  // a head's tiles one after another: the later ones find its cache in L2
+            if (++tile < q.tiles) return;
+            tile = 0;
+            if (++head < a.c.heads) return;
+            head = 0;
+        } else {
+            if (++head < a.c.heads) return;
+            head = 0;
+            if (++tile < q.tiles) return;
+            tile = 0;
+        }
         do {
             if (++b >= a.s.B) {
                 left = 0;
@@ -402,9 +409,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                                  : rest >> 31 == 0 ? static_cast<uint32_t>(rest) / static_cast<uint32_t>(at.q.cost)
                                                    : rest / at.q.cost;
             at.unit = static_cast<int32_t>(rest - item * at.q.cost);
-            at.tile = static_cast<int32_t>(item >> 31 == 0 ? static_cast<uint32_t>(item) / static_cast<uint32_t>(a.c.heads)
-                                                           : item / a.c.heads);
-            at.head = static_cast<int32_t>(item - int64_t{at.tile} * a.c.heads);
+            // (an item's number counts heads, or for kSinks tiles, first)
+            const int32_t inner = MODE == kSinks ? (at.q.tiles > 0 ? at.q.tiles : 1) : a.c.heads;
+            const int32_t outer_at = static_cast<int32_t>(
+                item >> 31 == 0 ? static_cast<uint32_t>(item) / static_cast<uint32_t>(inner) : item / inner);
+            const int32_t inner_at = static_cast<int32_t>(item - int64_t{outer_at} * inner);
+            at.tile = MODE == kSinks ? inner_at : outer_at;
+            at.head = MODE == kSinks ? outer_at : inner_at;
             at.left = at.q.cost > 0 ? to - from : 0;
         }
         Cursor<R, TS, MODE> ahead = at;

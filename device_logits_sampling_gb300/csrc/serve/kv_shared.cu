@@ -27,6 +27,14 @@
 // and scales.  While one group of rows is at its softmax the products of the other run.
 //
 // Every wait has a limit; a block whose wait runs out leaves NaN.
+//
+// Bounds and figures.  256 sequences behind 16,384 tokens, 64 + 8 heads of 128 (137 GFLOP): the prefix 142 us, 970
+// TFLOP/s, 51% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what is
+// left are the latencies of the softmax's steps (barrier, scores, maximum, exponentials, barrier), which two warps a
+// scheduler do not hide.  64 behind 32,768, 32 + 8 heads: 45 us of 78 in all.  Few rows: latency, 28 us for the three
+// kernels.  Measured and left, the prefix of the first case: output read back and added up in registers each tile 252 us;
+// steps of 128 tokens, one ahead 169; weights made before the maximum is known and again where the reference moves 186 to
+// 255; one thread for all products 161; loops over a step's scores unrolled further 10% to 30% slower each time.
 #include "kv_shared.cuh"
 
 #include <atomic>
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                 load_scales(next, id_next, key_next, val_next);
                 const int id_after = load_id(after);
                 const int first = first_of(now), n = count_of(first);
-                const int offset = (now.chunk * X::kTokens) & (ps - 1);  // where pages are larger than a tile
+                const int offset = ((now.chunk & 3) * X::kTokens) & (ps - 1);  // where pages are larger than a tile (at most four)
                 const bool good = lane < n && static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.pages);
                 if (lane < n && !good && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
                 const int64_t at = (good ? id : 0) * a.c.page_stride + now.head * a.c.head_stride + int64_t{offset} * D;
@@ -656,7 +664,7 @@ struct JoinArgs {
     int32_t chunks, pieces, group, q_heads, bf16, vec;
 };
 
-// 32 rows of a cached head, a lane each; the warps share the output's values.
+// 32 rows of a cached head, a lane each, and 32 of the output's values, four a warp.
 template <int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ JoinArgs a) {
     using X = Prefix<D>;
@@ -680,41 +688,30 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
     __syncthreads();
     for (int i = warp; i <= n; i += 8) weight[i][lane] = ex2(weight[i][lane] - top) / total;
     __syncthreads();
-    constexpr int Q = D / 32;  // four values each
-    float4 x[Q];
+    const int quad = blockIdx.z * 8 + warp;  // the warp's four values
     const float f0 = weight[n][lane];
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(a.rows)[own * (D / 4) + warp * Q + i];
-        x[i] = make_float4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
-    }
-    const float4* part = reinterpret_cast<const float4*>(a.slots) + ((slot0 * X::kTiles + in / 128) * (D / 4) + warp * Q) * 128 + in % 128;
-#pragma unroll 4
+    float4 x = reinterpret_cast<const float4*>(a.rows)[own * (D / 4) + quad];
+    x = make_float4(x.x * f0, x.y * f0, x.z * f0, x.w * f0);
+    const float4* part = reinterpret_cast<const float4*>(a.slots) + ((slot0 * X::kTiles + in / 128) * (D / 4) + quad) * 128 + in % 128;
+#pragma unroll 8
     for (int s = 0; s < n; ++s) {
         const float f = weight[s][lane];
-        const float4* p = part + static_cast<int64_t>(s) * X::kTiles * (D / 4) * 128;
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            const float4 v = p[i * 128];
-            if (f != 0.0f)  // (rows that nothing is joined to)
-                x[i] = make_float4(fmaf(v.x, f, x[i].x), fmaf(v.y, f, x[i].y), fmaf(v.z, f, x[i].z), fmaf(v.w, f, x[i].w));
-        }
+        const float4 v = part[static_cast<int64_t>(s) * X::kTiles * (D / 4) * 128];
+        if (f != 0.0f)  // (rows that nothing is joined to)
+            x = make_float4(fmaf(v.x, f, x.x), fmaf(v.y, f, x.y), fmaf(v.z, f, x.z), fmaf(v.w, f, x.w));
     }
     if (!real) return;
     uint16_t* out = static_cast<uint16_t*>(a.out) + tok * a.out_token_stride +
-                    (head * a.group + row - tok * a.group) * a.out_head_stride + warp * Q * 4;
-#pragma unroll
-    for (int i = 0; i < Q; ++i) {
-        const uint32_t lo = a.bf16 ? Half<ARC_BF16>::pack(x[i].x, x[i].y) : Half<ARC_F16>::pack(x[i].x, x[i].y);
-        const uint32_t hi = a.bf16 ? Half<ARC_BF16>::pack(x[i].z, x[i].w) : Half<ARC_F16>::pack(x[i].z, x[i].w);
-        if (a.vec) {
-            *reinterpret_cast<uint2*>(out + 4 * i) = make_uint2(lo, hi);
-        } else {
-            out[4 * i] = static_cast<uint16_t>(lo);
-            out[4 * i + 1] = static_cast<uint16_t>(lo >> 16);
-            out[4 * i + 2] = static_cast<uint16_t>(hi);
-            out[4 * i + 3] = static_cast<uint16_t>(hi >> 16);
-        }
+                    (head * a.group + row - tok * a.group) * a.out_head_stride + quad * 4;
+    const uint32_t lo = a.bf16 ? Half<ARC_BF16>::pack(x.x, x.y) : Half<ARC_F16>::pack(x.x, x.y);
+    const uint32_t hi = a.bf16 ? Half<ARC_BF16>::pack(x.z, x.w) : Half<ARC_F16>::pack(x.z, x.w);
+    if (a.vec) {
+        *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+    } else {
+        out[0] = static_cast<uint16_t>(lo);
+        out[1] = static_cast<uint16_t>(lo >> 16);
+        out[2] = static_cast<uint16_t>(hi);
+        out[3] = static_cast<uint16_t>(hi >> 16);
     }
 }
 
@@ -730,7 +727,7 @@ int launch_prefix(const PrefixArgs& p, const JoinArgs& j, const arc_kv_cache& ca
     if (cudaGetLastError() != cudaSuccess) return ARC_E_CUDA;
     const int rc = launch_behind(cache, step, query, err_word, workspace, at, prefix_tokens, dev, sms, st);
     if (rc != ARC_OK) return rc;
-    const dim3 grid(static_cast<unsigned>((p.rows + 31) / 32), static_cast<unsigned>(cache.heads));
+    const dim3 grid(static_cast<unsigned>((p.rows + 31) / 32), static_cast<unsigned>(cache.heads), D / 32);
     shared_join_kernel<D><<<grid, 256, 0, st>>>(j);
     return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
 }

@@ -8,10 +8,10 @@
 //
 // Bounds and figures.  A mask alone, in place, 100 x 100,003 fp32: 10.0 us, faster than its 81 MB at the measured copy
 // rate (12.1), since what it takes out is not read.  256 rows x 129,280 with histories of up to 4,096 ids, up to 300
-// biases and masks: 56 us (20.5 of traffic): every block of a row goes through the row's lists, and six blocks an SM, whose
-// tables fill its shared memory, hide no more of that than they do.  One row 5.8 us: four loads that wait for one another.
-// Measured and left: a second kernel with a hash table a row that edits behind the stream (54 us for the batch, 12 for the
-// row), edits from the lists instead of marks (66 to 80), one table of counts and entries in one word (73).
+// biases and masks: 47 us (20.5 of traffic): instructions, 70% of the issue slots; every block of a row goes through the
+// row's lists.  One row 5.0 us: four loads that wait for one another.  Measured and left: all eight ids of a marked group
+// looked up with its store (56 us), a second kernel with a hash table a row that edits behind the stream (54, and 12 for
+// one row), edits by whoever takes an id's word out of the table (66 to 80), counts and entries in one word (73).
 //
 // Rows of an odd vocabulary begin anywhere: the groups of eight are laid on the 16-byte boundaries of the output, the
 // mask's byte is cut out of two, and logits that are not aligned alike are read one by one.
@@ -157,26 +157,21 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         bits[g] = i < a.V ? bits_of(i) : 0;
     }
     T x[G][8];
-    auto load = [&](bool late) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const int64_t i = base + (g * kThreads + tid) * 8;
-            // (in place, eight that are allowed are read once a list is known to have one of them)
-            if (i >= a.V || bits[g] == 0 || (a.in_place && !late && bits[g] == 0xFFu)) continue;
-            if (late && !(bits[g] == 0xFFu && tab.marks[g * kThreads + tid])) continue;
-            if (in_vec && i >= 0 && i + 8 <= a.V) {
-                const uint4* p = reinterpret_cast<const uint4*>(in + i);
-                uint4* q = reinterpret_cast<uint4*>(x[g]);
+    for (int g = 0; g < G; ++g) {
+        const int64_t i = base + (g * kThreads + tid) * 8;
+        if (i >= a.V || bits[g] == 0 || (a.in_place && bits[g] == 0xFFu)) continue;
+        if (in_vec && i >= 0 && i + 8 <= a.V) {
+            const uint4* p = reinterpret_cast<const uint4*>(in + i);
+            uint4* q = reinterpret_cast<uint4*>(x[g]);
 #pragma unroll
-                for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) q[k] = p[k];
-            } else {
+            for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) q[k] = p[k];
+        } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (i + k >= 0 && i + k < a.V) x[g][k] = in[i + k];
-            }
+            for (int k = 0; k < 8; ++k)
+                if (i + k >= 0 && i + k < a.V) x[g][k] = in[i + k];
         }
-    };
-    load(false);
+    }
 
     if (lists) {
         uint4* z = reinterpret_cast<uint4*>(dyn);
@@ -207,50 +202,54 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         each(a.e.bias_ids, b0, b1, ARC_EDIT_ERR_BIAS, false, [&](int at, uint32_t e) { atomicMax(&tab.entry[at], e); });
         __syncthreads();
     }
-    if (lists && a.in_place) load(true);
     if (err && first && a.err) atomicOr(a.err, err);
 
-    auto edited = [&](float z, int64_t id) {
-        const int at = static_cast<int>(id - base);
-        const uint32_t c = tab.count[at], e = tab.entry[at];
-        if (c) {
-            z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-            z = __fsub_rn(z, __fmul_rn(static_cast<float>(c), freq));
-            z = __fsub_rn(z, pres);
-        }
-        if (e) z = __fadd_rn(z, __ldg(a.e.bias + b0 + (e - 1)));
-        return z;
-    };
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const int64_t i = base + (g * kThreads + tid) * 8;
-        const bool marked = lists && tab.marks[g * kThreads + tid];
-        if (i >= a.V || (a.in_place && bits[g] == 0xFFu && !marked)) continue;
-        O y[8];
+        if (i >= a.V) continue;
+        if (!(a.in_place && bits[g] == 0xFFu)) {
+            O y[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (bits[g] >> k & 1) {
+            for (int k = 0; k < 8; ++k) {
                 if constexpr (DT == OT)
                     y[k] = x[g][k];
                 else
                     y[k] = narrow<OT>(widen<DT>(x[g][k]));
-                if (marked && i + k >= 0 && i + k < a.V) {
-                    const int at = static_cast<int>(i + k - base);
-                    if (tab.count[at] | tab.entry[at]) y[k] = narrow<OT>(edited(widen<DT>(x[g][k]), i + k));
-                }
+                if (!(bits[g] >> k & 1)) y[k] = narrow<OT>(none);
+            }
+            if (i >= 0 && i + 8 <= a.V) {
+                const uint4* q = reinterpret_cast<const uint4*>(y);
+                uint4* p = reinterpret_cast<uint4*>(out + i);
+#pragma unroll
+                for (int k = 0; k < static_cast<int>(sizeof(O)) / 2; ++k) p[k] = q[k];
             } else {
-                y[k] = narrow<OT>(none);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i + k >= 0 && i + k < a.V) out[i + k] = y[k];
             }
         }
-        if (i >= 0 && i + 8 <= a.V) {
-            const uint4* q = reinterpret_cast<const uint4*>(y);
-            uint4* p = reinterpret_cast<uint4*>(out + i);
+        if (LISTS && lists && tab.marks[g * kThreads + tid]) {
+            // the ids of the eight that the lists have, one by one, over what has just been stored
+            const int at = (g * kThreads + tid) * 8;
+            uint32_t hit = 0;
 #pragma unroll
-            for (int k = 0; k < static_cast<int>(sizeof(O)) / 2; ++k) p[k] = q[k];
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (i + k >= 0 && i + k < a.V) out[i + k] = y[k];
+            for (int k = 0; k < 2; ++k) {
+                const uint4 c = reinterpret_cast<const uint4*>(tab.count + at)[k], e = reinterpret_cast<const uint4*>(tab.entry + at)[k];
+                hit |= ((c.x | e.x ? 1u : 0u) | (c.y | e.y ? 2u : 0u) | (c.z | e.z ? 4u : 0u) | (c.w | e.w ? 8u : 0u)) << (4 * k);
+            }
+            for (hit &= bits[g]; hit; hit &= hit - 1) {
+                const int k = __ffs(hit) - 1;
+                const uint32_t c = tab.count[at + k], e = tab.entry[at + k];
+                float z = widen<DT>(in[i + k]);
+                if (c) {
+                    z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+                    z = __fsub_rn(z, __fmul_rn(static_cast<float>(c), freq));
+                    z = __fsub_rn(z, pres);
+                }
+                if (e) z = __fadd_rn(z, __ldg(a.e.bias + b0 + (e - 1)));
+                out[i + k] = narrow<OT>(z);
+            }
         }
     }
 }
@@ -270,9 +269,9 @@ int launch(const EditArgs& a, int dev, cudaStream_t st) {
 
 template <int DT, int OT>
 int launch(const EditArgs& a, int dev, cudaStream_t st) {
-    // Two groups a thread where there are lists: 256 rows x 129,280 55.9 us, 68.1 with one, 76.8 with four; 32 rows 11.7,
-    // 13.1, 15.4; 512 rows 96, 115, 137.  Few rows want more blocks: one row 5.8 us with one, 7.5 with two; 8 rows 7.8 and
-    // 9.5; 16 rows 7.5 and 7.8.  Without lists the numbers lie within 4%.
+    // Two groups a thread where there are lists (before the marks' loop: 256 rows x 129,280 55.9 us, 68.1 with one, 76.8
+    // with four; 32 rows 11.7, 13.1, 15.4; 512 rows 96, 115, 137).  Few rows want more blocks: one row 5.8 us with one,
+    // 7.5 with two; 8 rows 7.8 and 9.5; 16 rows 7.5 and 7.8.  Without lists the numbers lie within 4%.
     if (a.e.hist_offsets || a.e.bias_offsets)
         return a.B * a.V <= (5 << 19) ? launch<DT, OT, true, 1>(a, dev, st) : launch<DT, OT, true, 2>(a, dev, st);
     return launch<DT, OT, false, 1>(a, dev, st);
