@@ -47,6 +47,7 @@
 #pragma once
 
 #include <atomic>
+#include <cstring>
 
 #include "kv_device.cuh"
 #include "kv_host.cuh"
@@ -325,6 +326,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
     constexpr int LB = D / 8;    // values of a head that a lane holds of the output
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ S sm;
+    // kBehind runs beside the kernel of the prefix, which is launched before it and needs nothing of it; what comes after
+    // this kernel comes after that one, too.
+    struct End {
+        __device__ __forceinline__ ~End() {
+            if constexpr (MODE == kBehind) asm volatile("griddepcontrol.wait;" ::: "memory");
+        }
+    } const end_of_both;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
@@ -1044,6 +1052,22 @@ int launch(const AttendArgs& a, int dev, int sms, cudaStream_t st) {
     static_assert(S::kBytes + sizeof(S) <= arc::kSmemPerBlock, "shared memory");
     if (arc::prepare(attend_kernel<D, NT, MODE>, dev, done, 100) != cudaSuccess) return ARC_E_CUDA;
     const int grid = sms < kMaxBlocks ? sms : kMaxBlocks;
+    if constexpr (MODE == kBehind) {
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+        cfg.blockDim = dim3(S::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = S::kBytes;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaLaunchKernelEx(&cfg, attend_kernel<D, NT, MODE>, a) == cudaSuccess) return ARC_OK;
+        (void)cudaGetLastError();
+        return ARC_E_CUDA;
+    }
     attend_kernel<D, NT, MODE><<<grid, S::kThreads, S::kBytes, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ARC_OK : ARC_E_CUDA;
 }

@@ -1,6 +1,6 @@
 // arc_kv_attend_shared: attention of a step's new tokens behind a prefix that all sequences share.
 //
-// Three kernels.  The prefix: all rows of a cached head (new tokens times its query heads) against the prefix's pages,
+// Three kernels, the first two side by side where there are SMs for both.  The prefix: all rows of a cached head (new tokens times its query heads) against the prefix's pages,
 // which are read once for them.  The sequences' own tokens: kv_attend.cuh's kernel, with its results in fp32.  And the
 // join of a row's parts, each an output with the base-2 logarithm of its sum of weights:
 //     out = sum_i 2^(log_i - max) out_i / sum_i 2^(log_i - max).
@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
     using X = Prefix<D>;
     extern __shared__ uint8_t raw_smem[];
     __shared__ PrefixBars bars;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the own tokens' kernel needs nothing of this one
     uint8_t* const dyn = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
     uint8_t* const q_tiles = dyn;
     uint8_t* const ops = dyn + X::kTiles * X::kQ;
