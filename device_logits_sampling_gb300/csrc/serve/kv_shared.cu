@@ -600,9 +600,11 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                                 const uint64_t z = fma2(pack2(__uint_as_float(s[b][16 * h + 2 * i]),
                                                               __uint_as_float(s[b][16 * h + 2 * i + 1])), f2, add2);
                                 const float e0 = ex2(half_of(z, 0)), e1 = ex2(half_of(z, 1));
-                                part[0] += e0;
-                                part[1] += e1;
                                 p[8 * h + i] = Half<ARC_F16>::pack(e0, e1);
+                                // (the weights as they enter the product: their roundings cancel in the quotient)
+                                const float2 w2 = Half<ARC_F16>::unpack(p[8 * h + i]);
+                                part[0] += w2.x;
+                                part[1] += w2.y;
                             }
                             sum = fmaf(part[0] + part[1], unlifts[g], sum);
                         }
