@@ -28,11 +28,11 @@
 //
 // Every wait has a limit; a block whose wait runs out leaves NaN.
 //
-// Bounds and figures.  256 sequences behind 16,384 tokens, 64 + 8 heads of 128 (137 GFLOP): the prefix 142 us, 970
-// TFLOP/s, 51% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what is
+// Bounds and figures.  256 sequences behind 16,384 tokens, 64 + 8 heads of 128 (137 GFLOP): the prefix 145 us, 950
+// TFLOP/s, 50% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what is
 // left are the latencies of the softmax's steps (barrier, scores, maximum, exponentials, barrier), which two warps a
-// scheduler do not hide.  64 behind 32,768, 32 + 8 heads: 45 us of 78 in all.  Few rows: latency, 28 us for the three
-// kernels.  Measured and left, the prefix of the first case: output read back and added up in registers each tile 252 us;
+// scheduler do not hide.  64 behind 32,768, 32 + 8 heads: 45 us of 76 in all.  Few rows: latency, 19 us for the three
+// kernels, 28 one after another.  Measured and left, the prefix of the first case: output read back and added up in registers each tile 252 us;
 // steps of 128 tokens, one ahead 169; weights made before the maximum is known and again where the reference moves 186 to
 // 255; one thread for all products 161; loops over a step's scores unrolled further 10% to 30% slower each time.
 #include "kv_shared.cuh"
