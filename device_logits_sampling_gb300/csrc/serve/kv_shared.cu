@@ -15,16 +15,16 @@
 //
 // Softmax.  P holds the weights relative to a reference of the row and the value scales relative to a reference of the
 // tiles, 2^12 times, as fp16, and O is summed up in tensor memory in their units.  The references stay while the
-// largest score of a tile lies at most 3 above the row's (as a power of two) or 6 below, and its pages' value scales
-// within 1/16 of theirs; a tile is a chunk, or the part of one whose pages agree.  Else the row takes the tile's own
-// largest score, and the sums so far are multiplied by what that changes, in fp32: a weight keeps its bits beside those
-// of its own tile, whatever scores and scales came before.  (A reference lies at most 2^60 below the largest weight
+// largest score of a step's 64 tokens lies at most 3 above the row's (as a power of two) or 10 below, and its pages'
+// value scales within 1/16 of theirs; a tile is a chunk, or the part of one whose pages agree.  Else the row's becomes the
+// step's own largest score and 4, room for larger ones, and the sums so far are multiplied by what that changes, in fp32:
+// a weight keeps its bits beside those of its own step, whatever scores and scales came before.  (A reference lies at most 2^60 below the largest weight
 // times scale so far, so that the sums stay in fp32's range.)  The sum of the weights is kept apart, relative to the
 // largest score.
 //
 // Roles of a block: two groups of four warps take the softmax, a thread a row (two groups of 128 rows, or for heads of
-// 256 one, half of the output each), a group makes fp16 of codes, a warp issues the products and a warp looks up pages
-// and scales.  While one group of rows is at its softmax the products of the other run.
+// 256 one, half of the output each), a group makes fp16 of codes, a thread for each group of rows issues its products
+// and a warp looks up pages and scales.  While one group of rows is at its softmax the products of the other run.
 //
 // Every wait has a limit; a block whose wait runs out leaves NaN.
 //
@@ -50,7 +50,7 @@ namespace {
 
 constexpr float kSpread = 16.0f;  // of the value scales that share a reference
 constexpr int kInfos = 8;         // ring of tiles' descriptions
-// A new reference lies kRoom above the tile's largest score; it stays while that is at most kAbove above it (2^(12 + 3)
+// A new reference lies kRoom above the step's largest score; it stays while that is at most kAbove above it (2^(12 + 3)
 // is the largest weight as fp16) and kBelow below.
 constexpr float kLift = 12.0f, kRoom = 4.0f, kAbove = 3.0f, kBelow = 10.0f;
 constexpr float kSpan = 60.0f;

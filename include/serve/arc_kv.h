@@ -189,10 +189,10 @@ int arc_kv_attend_sinks(const arc_kv_cache* cache, const arc_kv_step* step, cons
  * prefix: one whose position lies before the prefix's end sets
  * ARC_KV_ERR_POSITION and its rows are NaN.  A page outside [0, pages) in the
  * prefix makes every row NaN.
- * Weights enter the products with the prefix as fp16, relative to the largest
- * of the 128 tokens (64 for heads of 256) they are multiplied with, all of
- * pages whose value scales lie within a factor of 64: off by 2^-11 of
- * themselves at most above 2^-22 of that one, 0 below 2^-33.
+ * Weights enter the products with the prefix as fp16, 64 tokens at a time, all
+ * of pages whose value scales lie within a factor of 16: off by 2^-11 of
+ * themselves at most above 2^-12 of the largest of the 64, by 2^-23 of that one
+ * below (as a rule 2^-22 and 2^-33); they are summed up as rounded.
  *   workspace  arc_kv_attend_shared_workspace_bytes(cache, T, q_heads) bytes,
  *              as for arc_kv_attend
  */
