@@ -1,26 +1,27 @@
 // arc_kv_attend_shared: attention of a step's new tokens behind a prefix that all sequences share.
 //
-// Three kernels, the first two side by side where there are SMs for both.  The prefix: all rows of a cached head (new tokens times its query heads) against the prefix's pages,
-// which are read once for them.  The sequences' own tokens: kv_attend.cuh's kernel, with its results in fp32.  And the
-// join of a row's parts, each an output with the base-2 logarithm of its sum of weights:
+// Three kernels, the first two side by side where there are SMs for both.  The prefix: all rows of a cached head (new
+// tokens times its query heads) against the prefix's pages, which are read once for them.  The sequences' own tokens:
+// kv_attend.cuh's kernel, with its results in fp32.  And the join of a row's parts, each an output with the base-2
+// logarithm of its sum of weights:
 //     out = sum_i 2^(log_i - max) out_i / sum_i 2^(log_i - max).
 //
 // The prefix.  A unit is a cached head and up to 256 rows (128 for heads of 256).  A chunk is 128 tokens (64 for heads
 // of 256) of the prefix; all units' chunks lie on a line that is cut into one piece a block.  A block runs through its
 // piece tile by tile, and leaves a partial for each unit that it has met.
 //
-// Products.  Codes are loaded a tile ahead into registers and become fp16 in shared memory, exactly.  S = Q K^T and
-// O += P V run on the 5th-generation tensor cores, M = 128 rows: Q and K from shared memory, P from tensor memory, where
+// Products.  Codes are loaded a tile ahead into registers and become fp16 in shared memory, exactly.  S = Q K^T and O
+// += P V run on the 5th-generation tensor cores, M = 128 rows: Q and K from shared memory, P from tensor memory, where
 // the softmax has put it over S, V as it lies, tokens as rows, read across.
 //
 // Softmax.  P holds the weights relative to a reference of the row and the value scales relative to a reference of the
 // tiles, 2^12 times, as fp16, and O is summed up in tensor memory in their units.  The references stay while the
 // largest score of a step's 64 tokens lies at most 3 above the row's (as a power of two) or 10 below, and its pages'
-// value scales within 1/16 of theirs; a tile is a chunk, or the part of one whose pages agree.  Else the row's becomes the
-// step's own largest score and 4, room for larger ones, and the sums so far are multiplied by what that changes, in fp32:
-// a weight keeps its bits beside those of its own step, whatever scores and scales came before.  (A reference lies at most 2^60 below the largest weight
-// times scale so far, so that the sums stay in fp32's range.)  The sum of the weights is kept apart, relative to the
-// largest score.
+// value scales within 1/16 of theirs; a tile is a chunk, or the part of one whose pages agree.  Else the row's becomes
+// the step's own largest score and 4, room for larger ones, and the sums so far are multiplied by what that changes, in
+// fp32: a weight keeps its bits beside those of its own step, whatever scores and scales came before.  (A reference
+// lies at most 2^60 below the largest weight times scale so far, so that the sums stay in fp32's range.)  The sum of
+// the weights is kept apart, relative to the largest score.
 //
 // Roles of a block: two groups of four warps take the softmax, a thread a row (two groups of 128 rows, or for heads of
 // 256 one, half of the output each), a group makes fp16 of codes, a thread for each group of rows issues its products
@@ -29,12 +30,13 @@
 // Every wait has a limit; a block whose wait runs out leaves NaN.
 //
 // Bounds and figures.  256 sequences behind 16,384 tokens, 64 + 8 heads of 128 (137 GFLOP): the prefix 145 us, 950
-// TFLOP/s, 50% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what is
-// left are the latencies of the softmax's steps (barrier, scores, maximum, exponentials, barrier), which two warps a
+// TFLOP/s, 50% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what
+// is left are the latencies of the softmax's steps (barrier, scores, maximum, exponentials, barrier), which two warps a
 // scheduler do not hide.  64 behind 32,768, 32 + 8 heads: 45 us of 76 in all.  Few rows: latency, 19 us for the three
-// kernels, 28 one after another.  Measured and left, the prefix of the first case: output read back and added up in registers each tile 252 us;
-// steps of 128 tokens, one ahead 169; weights made before the maximum is known and again where the reference moves 186 to
-// 255; one thread for all products 161; loops over a step's scores unrolled further 10% to 30% slower each time.
+// kernels, 28 one after another.  Measured and left, the prefix of the first case: output read back and added up in
+// registers each tile 252 us; steps of 128 tokens, one ahead 169; weights made before the maximum is known and again
+// where the reference moves 186 to 255; one thread for all products 161; loops over a step's scores unrolled further
+// 10% to 30% slower each time.
 #include "kv_shared.cuh"
 
 #include <atomic>
