@@ -687,11 +687,14 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
     for (int i = warp; i <= n; i += 8)
         weight[i][lane] = i < n ? __ldg(a.slot_logs + (slot0 + i) * X::kRows + in) : __ldg(a.logs + own);
     __syncthreads();
+    // (a row that nothing is joined to: what the prefix gave it, NaN included, counts nothing)
+    const bool alone = weight[n][lane] == kAlone;
     float top = kNothing, total = 0.0f;
     for (int i = 0; i <= n; ++i) top = fmaxf(top, weight[i][lane]);
     for (int i = 0; i <= n; ++i) total += ex2(weight[i][lane] - top);
     __syncthreads();
-    for (int i = warp; i <= n; i += 8) weight[i][lane] = ex2(weight[i][lane] - top) / total;
+    for (int i = warp; i <= n; i += 8)
+        weight[i][lane] = alone ? (i == n ? 1.0f : 0.0f) : ex2(weight[i][lane] - top) / total;
     __syncthreads();
     const int quad = blockIdx.z * 8 + warp;  // the warp's four values
     const float f0 = weight[n][lane];

@@ -188,7 +188,8 @@ int arc_kv_attend_sinks(const arc_kv_cache* cache, const arc_kv_step* step, cons
  * prefix_pages entries are not read here.  Every sequence holds the whole
  * prefix: one whose position lies before the prefix's end sets
  * ARC_KV_ERR_POSITION and its rows are NaN.  A page outside [0, pages) in the
- * prefix makes every row NaN.
+ * prefix makes every row NaN but those of parked sequences, which are 0 whatever
+ * their queries and the prefix hold.
  * Weights enter the products with the prefix as fp16, 64 tokens at a time, all
  * of pages whose value scales lie within a factor of 16: off by 2^-11 of
  * themselves at most above 2^-12 of the largest of the 64, by 2^-23 of that one
