@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
 
         // ---- copies
         int issued = 0;                 // stage of the next copy
-        int step = 0, step_end = 0;     // of the item that is being copied
+        int step = 0, step_end = 0;     // of the item that is being copied; of its sequence, or for kSinks of the item
         int first = 0, last = 0;        // tokens that its rows see; the others are filled with zeros
         const int32_t* table = nullptr;
         const char *k_head = nullptr, *v_head = nullptr;  // its head, this lane's 16 bytes
@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 if (ahead.unit == ahead.q.cost) ahead.next_item(a);
                 if (ahead.left <= 0) return;
                 const int n = ahead.q.cost - ahead.unit < ahead.left ? ahead.q.cost - ahead.unit : static_cast<int>(ahead.left);
-                step = ahead.unit > kItemCost ? ahead.unit - kItemCost : 0;
+                const int base = MODE == kSinks ? 0 : ahead.q.step0;
+                step = base + (ahead.unit > kItemCost ? ahead.unit - kItemCost : 0);
                 ahead.unit += n;
                 ahead.left -= n;
-                step_end = ahead.unit > kItemCost ? ahead.unit - kItemCost : 0;
+                step_end = base + (ahead.unit > kItemCost ? ahead.unit - kItemCost : 0);
             }
             const int row0 = ahead.tile * R, rows = ahead.q.n * a.group;
             const bool one = ahead.q.n == 1;
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
             if (step < step_end) {
 #pragma unroll
                 for (int hv = 0; hv < HV; ++hv) {
-                    const int tok0 = token_of_step<TS, MODE>(ahead.q, step) + 16 * hv, pi = tok0 >> ps_shift;
+                    const int tok0 = (MODE == kSinks ? token_of_step<TS, MODE>(ahead.q, step) : step << TS) + 16 * hv, pi = tok0 >> ps_shift;
                     // (a half that no row sees takes no page)
                     const bool none = HV > 1 && (tok0 > last || (tok0 + 15 < first && !(MODE == kSinks && tok0 < a.front)));
                     if (!none && pi != page_of) {
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                         page_of = pi;
                         page_ahead = -1;
                         if (((pi + 1) << ps_shift) <= last &&
-                            (MODE == kSinks || (((pi + 1) << ps_shift) >> TS) - ahead.q.step0 < step_end)) {
+                            (MODE == kSinks || ((pi + 1) << ps_shift) >> TS < step_end)) {
                             page_next = __ldg(table + pi + 1);
                             page_ahead = pi + 1;
                         }
