@@ -52,6 +52,9 @@ namespace {
 
 constexpr float kSpread = 16.0f;  // of the value scales that share a reference
 constexpr int kInfos = 8;         // ring of tiles' descriptions
+// Scales are at most kMost.  Value scales below kLeast count as 0: references of pages that lie further apart than that
+// would take each other's weights to 0 as fp16, and with them the sum of the weights.
+constexpr float kMost = 4294967296.0f, kLeast = 1.0f / (1ull << 60);
 // A new reference lies kRoom above the step's largest score; it stays while that is at most kAbove above it (2^(12 + 3)
 // is the largest weight as fp16) and kBelow below.
 constexpr float kLift = 12.0f, kRoom = 4.0f, kAbove = 3.0f, kBelow = 10.0f;
@@ -102,7 +105,8 @@ __host__ __device__ inline int64_t cut_of(int64_t total, int64_t i, int64_t of) 
 
 struct __align__(16) Info {  // a tile
     int32_t tokens;
-    int32_t flags;    // 1: the last of its unit's, 2: the last of all, 4: another reference than the tile before's
+    int32_t flags;    // 1: the last of its unit's, 2: the last of all, 4: another reference than the tile before's;
+                      // from bit 8 on the pages whose values count as zeros
     float value;      // the reference of the value scales,
     float value_log;  // its logarithm
     float key[8];     // of each 16 tokens: key scale,
@@ -318,17 +322,26 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                 const int offset = ((now.chunk & 3) * X::kTokens) & (ps - 1);  // where pages are larger than a tile (at most four)
                 const bool good = lane < n && static_cast<uint32_t>(id) < static_cast<uint32_t>(a.c.pages);
                 if (lane < n && !good && a.err) atomicOr(a.err, ARC_KV_ERR_PAGE);
+                if (good && !(key >= 0.0f && key <= kMost && val >= 0.0f && val <= kMost)) {
+                    if (a.err) atomicOr(a.err, ARC_KV_ERR_SCALE);
+                    key = __int_as_float(0x7FC00000);
+                    val = 1.0f;
+                }
+                // a page of zeros goes with any reference
+                const bool none = val < kLeast;
+                const uint32_t nones = __ballot_sync(0xFFFFFFFFu, none);
                 const int64_t at = (good ? id : 0) * a.c.page_stride + now.head * a.c.head_stride + int64_t{offset} * D;
                 const bool ends_all = next.c == to, unit_ends = next.chunk == 0 || ends_all;
                 for (int start = 0; ok && start < n; ++t) {
                     // the pages from `start` on whose scales go with the reference, or with one another
-                    bool apart = lane > start && lane < n;
+                    bool apart = lane > start && lane < n && !none;
                     const float v0 = __shfl_sync(0xFFFFFFFFu, val, start);
-                    const bool stays = v0 <= value && v0 * kSpread >= value;
+                    const bool stays = v0 < kLeast ? value > 0.0f : v0 <= value && v0 * kSpread >= value;
                     if (stays) {
                         apart = apart && !(val <= value && val * kSpread >= value);
                     } else {
-                        float hi = lane >= start && lane < n ? val : 0.0f, lo = hi;
+                        const bool counts = lane >= start && lane < n && !none;
+                        float hi = counts ? val : 0.0f, lo = counts ? val : kMost;
 #pragma unroll
                         for (int m = 1; m < 8; m <<= 1) {
                             const float h = __shfl_up_sync(0xFFFFFFFFu, hi, m), l = __shfl_up_sync(0xFFFFFFFFu, lo, m);
@@ -340,6 +353,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                         apart = apart && hi > kSpread * lo;
                         const uint32_t ends = __ballot_sync(0xFFFFFFFFu, apart);
                         value = __shfl_sync(0xFFFFFFFFu, hi, ends ? __ffs(ends) - 2 : n - 1);
+                        if (value == 0.0f) value = 1.0f;  // zeros alone
                     }
                     const uint32_t ends = __ballot_sync(0xFFFFFFFFu, apart);
                     const int end = ends ? __ffs(ends) - 1 : n;
@@ -350,14 +364,15 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                     const float k16 = __shfl_sync(0xFFFFFFFFu, key, page & 31), v16 = __shfl_sync(0xFFFFFFFFu, val, page & 31);
                     if (lane < X::kGranules) {
                         const bool there = page < end;
-                        const float lift = kLift + (v16 == value ? 0.0f : __log2f(v16 / value));
+                        const float lift = kLift + (v16 == value || v16 < kLeast ? 0.0f : __log2f(v16 / value));
                         info.key[lane] = there ? k16 : 0.0f;
                         info.lift[lane] = there ? lift : -kAlone;
                         info.back[lane] = there ? ex2(-lift) : 0.0f;
                     }
                     if (lane == 0) {
                         info.tokens = (end - start) << span_shift;
-                        info.flags = (end == n && unit_ends ? (ends_all ? 3 : 1) : 0) | (stays ? 0 : 4);
+                        info.flags = (end == n && unit_ends ? (ends_all ? 3 : 1) : 0) | (stays ? 0 : 4) |
+                                     (nones >> start & ((1u << (end - start)) - 1)) << 8;
                         info.value = value;
                         info.value_log = __log2f(value);
                     }
@@ -388,15 +403,21 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         auto chunk_of = [&](int j) { return (j / kTurns) * 4 + (me & 3); };
         const int ps = a.c.page_size, span = ps < X::kTokens ? ps : X::kTokens, shift = 31 - __clz(span);
         uint4 k[N], v[N];
-        auto load = [&](uint32_t t, const void* from, uint4 (&x)[N]) {
+        auto load = [&](uint32_t t, const void* from, bool values, uint4 (&x)[N]) {
             const Info& info = bars.info[t % kInfos];
             const int tokens = info.tokens;
+            const uint32_t zeros = values ? static_cast<uint32_t>(info.flags) >> 8 : 0;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int token = token_of(j), chunk = chunk_of(j);
                 const int64_t at = token < tokens ? info.at[token >> shift] : -1;
                 x[j] = at < 0 ? make_uint4(0, 0, 0, 0)
                               : load_past_l1(static_cast<const char*>(from) + at + (token & (span - 1)) * D + chunk * 16);
+            }
+            if (zeros) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (zeros >> (token_of(j) >> shift) & 1) x[j] = make_uint4(0, 0, 0, 0);
             }
         };
         uint32_t os = 0, phase = 1;
@@ -427,8 +448,8 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         };
         bool ok = warp_wait(&bars.info_full[0], 0, &bars.failed), last = !ok;
         if (ok) {
-            load(0, a.c.k, k);
-            load(0, a.c.v, v);
+            load(0, a.c.k, false, k);
+            load(0, a.c.v, true, v);
             last = bars.info[0].flags & 2;
         }
 #pragma unroll 1
@@ -440,10 +461,10 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                 last = bars.info[t % kInfos].flags & 2;
             }
             ok = convert(k);
-            if (ok && more) load(t, a.c.k, k);
+            if (ok && more) load(t, a.c.k, false, k);
             if (ok) ok = convert(v);
             if (!more) break;
-            if (ok) load(t, a.c.v, v);
+            if (ok) load(t, a.c.v, true, v);
         }
     } else {
         // ---- softmax and sums: a thread a row

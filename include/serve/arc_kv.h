@@ -49,7 +49,8 @@ extern "C" {
                                     those after it, are left out; their tokens are not stored, and the rows that
                                     no sequence before them has are NaN in q_out and in the attention */
 #define ARC_KV_ERR_SCALE 0x10u   /* a page that holds older tokens has a scale outside [2^-32, 2^32]: the new ones
-                                    are not stored under that head, and the page stays as it is */
+                                    are not stored under that head, and the page stays as it is; a scale of a shared
+                                    prefix is negative, NaN or above 2^32: the rows of that head are NaN */
 
 /* Host struct.  k and v have the same layout. */
 typedef struct arc_kv_cache {
@@ -189,7 +190,10 @@ int arc_kv_attend_sinks(const arc_kv_cache* cache, const arc_kv_step* step, cons
  * prefix: one whose position lies before the prefix's end sets
  * ARC_KV_ERR_POSITION and its rows are NaN.  A page outside [0, pages) in the
  * prefix makes every row NaN but those of parked sequences, which are 0 whatever
- * their queries and the prefix hold.
+ * their queries and the prefix hold.  The prefix's value scales lie in
+ * [2^-32, 2^32], or are 0: its values then count as zeros, and so they do under
+ * one below 2^-60.  Scales that are negative, NaN or above 2^32 set
+ * ARC_KV_ERR_SCALE and make the rows of their head NaN.
  * Weights enter the products with the prefix as fp16, 64 tokens at a time, all
  * of pages whose value scales lie within a factor of 16: off by 2^-11 of
  * themselves at most above 2^-12 of the largest of the 64, by 2^-23 of that one
