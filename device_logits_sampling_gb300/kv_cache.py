@@ -80,6 +80,7 @@ class PagedCache:
     def shared_workspace(self, tokens: int, q_heads: int, stream=None):
         """Zero-filled workspace for `attend_shared` of up to so many new tokens over caches of this shape (one per
         stream that uses it), made on the stream given, else on the current one."""
+        want(0 < q_heads < 1 << 31, "the heads must be positive and fit 32 bits")
         n = int(serve.load().arc_kv_attend_shared_workspace_bytes(self._ref, tokens, q_heads))
         want(n > 0, "arc_kv_attend_shared_workspace_bytes rejected the cache, the tokens or the heads")
         return serve.new_workspace(self.k, n, True, stream)
@@ -223,6 +224,7 @@ def attend(cache: PagedCache, q, positions, page_table, out=None, row_offsets=No
 
     stream: where the call runs, the current stream where None.  What the call makes for itself (out,
     workspace) is made there; tensors given have to be ready there."""
+    want(-1 << 31 <= sinks < 1 << 31, "sinks must fit 32 bits")
     T, dim, dev = q.shape[0], cache.head_dim, cache.index
     qt, qh, heads = _heads(q, T, None, dim, "q")
     code = serve.dtype_code(q)
