@@ -69,9 +69,8 @@ def edit_logits(logits, out=None, out_dtype=None, params=None, hist_offsets=None
         want(params.is_contiguous() and params.numel() * params.element_size() >= B * ROW_PARAMS_DTYPE.itemsize,
              "params must hold a record for each row")
         want(params.get_device() == dev, "every tensor must be on the logits' device")
-        hp, hi, hn, pp = hist_offsets.data_ptr(), hist_ids.data_ptr(), hist_ids.numel(), params.data_ptr()
-        if hn == 0:  # nothing to point at: no id is in any history
-            hp = hi = pp = 0
+        hp, hn, pp = hist_offsets.data_ptr(), hist_ids.numel(), params.data_ptr()
+        hi = hist_ids.data_ptr() if hn else hp  # (a list without an entry has no address, and is not read)
     if bias_offsets is not None or bias_ids is not None or bias is not None:
         want(bias_offsets is not None and bias_ids is not None and bias is not None,
              "biases are bias_offsets, bias_ids and bias")
@@ -80,9 +79,8 @@ def edit_logits(logits, out=None, out_dtype=None, params=None, hist_offsets=None
         if bias.dtype != torch.float32:
             raise TypeError(f"bias must be float32, not {bias.dtype}")
         want(bias.get_device() == dev, "every tensor must be on the logits' device")
-        bp, bi, bv, bn = bias_offsets.data_ptr(), bias_ids.data_ptr(), bias.data_ptr(), bias.numel()
-        if bn == 0:
-            bp = bi = bv = 0
+        bp, bn = bias_offsets.data_ptr(), bias.numel()
+        bi, bv = (bias_ids.data_ptr(), bias.data_ptr()) if bn else (bp, bp)
     if allowed is not None:
         want(allowed.dim() == 2 and allowed.shape[1] >= -(-V // 32), "allowed must be [masks, ceil(V / 32)]")
         want(allowed.stride(1) == 1 or allowed.shape[1] == 1, "rows of allowed must be contiguous")
