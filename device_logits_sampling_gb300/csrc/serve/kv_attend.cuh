@@ -51,6 +51,7 @@
 
 #include "kv_device.cuh"
 #include "kv_host.cuh"
+#include "kv_walk.cuh"
 #include "launch_util.cuh"
 #include "serve_util.cuh"
 
@@ -248,7 +249,7 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs& a, int64_t b) {
 // First token of the item's step s.
 template <int TS, Mode MODE>
 __device__ __forceinline__ int token_of_step(const Seq& q, int s) {
-    if constexpr (MODE == kSinks) return (s < q.sinks ? s : q.step0 + (s - q.sinks)) << TS;
+    if constexpr (MODE == kSinks) return sinks_token(s, q.sinks, q.step0, TS);
     return (q.step0 + s) << TS;
 }
 
@@ -475,13 +476,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) attend_kernel(co
                 for (int hv = 0; hv < HV; ++hv) {
                     const int tok0 = (MODE == kSinks ? token_of_step<TS, MODE>(ahead.q, step) : step << TS) + 16 * hv, pi = tok0 >> ps_shift;
                     // (a half that no row sees takes no page)
-                    const bool none = HV > 1 && (tok0 > last || (tok0 + 15 < first && !(MODE == kSinks && tok0 < a.front)));
+                    const bool none = HV > 1 && (MODE == kSinks ? sinks_unseen(tok0, first, last, a.front)
+                                                                : tok0 > last || tok0 + 15 < first);
                     if (!none && pi != page_of) {
                         page = pi == page_ahead ? page_next : __ldg(table + pi);
                         page_of = pi;
                         page_ahead = -1;
-                        if (((pi + 1) << ps_shift) <= last &&
-                            (MODE == kSinks || ((pi + 1) << ps_shift) >> TS < step_end)) {
+                        const int next = (pi + 1) << ps_shift;
+                        if (MODE == kSinks ? sinks_ahead(tok0, next, last, a.front)
+                                           : next <= last && next >> TS < step_end) {
                             page_next = __ldg(table + pi + 1);
                             page_ahead = pi + 1;
                         }
