@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         const int64_t i = base + (g * kThreads + tid) * 8;
         bits[g] = i < a.V ? bits_of(i) : 0;
     }
-    T x[G][8];
+    alignas(16) T x[G][8];  // moved 16 bytes at a time
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const int64_t i = base + (g * kThreads + tid) * 8;
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) edit_kernel(const __grid_constant__ 
         const int64_t i = base + (g * kThreads + tid) * 8;
         if (i >= a.V) continue;
         if (!(a.in_place && bits[g] == 0xFFu)) {
-            O y[8];
+            alignas(16) O y[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 if constexpr (DT == OT)
