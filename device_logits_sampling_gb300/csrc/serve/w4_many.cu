@@ -228,9 +228,9 @@ __global__ void __launch_bounds__(256) many_x_kernel(const __grid_constant__ Man
         if (real && u < units) load8<DT>(x + u * 16, a.x_vec, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= up;
-        const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
-                              __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f),
-                              __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f)};
+        alignas(16) const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
+                                          __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f),
+                                          __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f)};
         // 64 values of all rows, 128 bytes a row, its 16-byte chunks swizzled by the row
         const size_t at = (static_cast<size_t>(u >> 3) * block_rows + in) * 128 + (((u & 7) ^ (in & 7)) * 16);
         *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(h);

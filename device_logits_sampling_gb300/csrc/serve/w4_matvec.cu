@@ -196,9 +196,9 @@ __device__ __forceinline__ void stage_x(const FewArgs& f, uint8_t* dyn, int k0, 
             sum += v[e];
         }
         const int gi = k / G, in = k % G, t = in / (G / 4), w = (in % (G / 4)) >> 3;
-        const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
-                              __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f),
-                              __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f)};
+        alignas(16) const __half2 h[4] = {__floats2half2_rn(v[0], v[4]), __floats2half2_rn(v[2], v[6]),
+                                          __floats2half2_rn(v[1] * 0.0625f, v[5] * 0.0625f),
+                                          __floats2half2_rn(v[3] * 0.0625f, v[7] * 0.0625f)};
         if (on)
             *reinterpret_cast<uint4*>(dyn + f.x_off + (((gi * (G / 32) + w) * rows + m) * 4 + t) * 16) =
                 *reinterpret_cast<const uint4*>(h);
