@@ -56,8 +56,10 @@ typedef struct arc_logit_edits {
  *   logits    device [B][ld], ARC_F32, ARC_BF16 or ARC_F16
  *   B, V, ld  rows, vocabulary (at most 2^31 - 1), row stride in elements (ld >= V)
  *   out       device [B][out_ld], dtype or ARC_F32; may be logits with its stride
- *             and type (then what no edit touches is neither read nor written),
- *             otherwise it must not overlap
+ *             and type, otherwise it must not overlap.  In place, ids are taken in
+ *             groups of eight that begin on the 16-byte boundaries of each row: a
+ *             group that the mask allows whole and no list names is neither read nor
+ *             written, of the others any value may be written back as it was
  */
 int arc_edit_logits(const void* logits, int64_t B, int64_t V, int64_t ld, int32_t dtype, void* out, int64_t out_ld,
                     int32_t out_dtype, const arc_logit_edits* edits, uint32_t* err_word, void* stream);

@@ -10,7 +10,9 @@
  *
  * Library: libarcserve.so.  Conventions are those of arc_sample.h: plain
  * device pointers, sizes and a stream; the host arguments are checked before
- * any CUDA call and a negative ARC_E_* code means that nothing was enqueued;
+ * any CUDA call and a negative ARC_E_* code means that nothing was enqueued (but
+ * for ARC_E_CUDA of a call of several kernels, append, attend_shared or a 4-bit
+ * product: those before the one that could not be launched are);
  * nothing is allocated and nothing synchronises; what is found wrong on the
  * device becomes sticky bits in *err_word and leaves the other sequences alone
  * (but for offsets: where one is wrong, those after it say nothing either).
