@@ -59,6 +59,10 @@ constexpr float kMost = 4294967296.0f, kLeast = 1.0f / (1ull << 60);
 // is the largest weight as fp16) and kBelow below.
 constexpr float kLift = 12.0f, kRoom = 4.0f, kAbove = 3.0f, kBelow = 10.0f;
 constexpr float kSpan = 60.0f;
+// References up to here: a score's and a reference's half steps of fp32 are then 1/4, so that the largest weight stays below
+// 2^15.75.  Past it a weight as fp16 may be infinite or lost: the row becomes NaN.  Measured and left: scores rounded before
+// the reference is taken away, as the largest is, which would hold for any; 1 to 4% of each call.
+constexpr float kFar = 4194304.0f;
 
 template <int D>
 struct Prefix {
@@ -604,6 +608,7 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                                 tmem_store16(o_at + 16 * b, y);
                             }
                         }
+                        if (fabsf(ref) > kFar) l = __int_as_float(0x7FC00000);
                     }
                     fresh = false;
                     if (left > 0) peak = fmaxf(peak, top + value_log);

@@ -195,7 +195,9 @@ int arc_kv_attend_sinks(const arc_kv_cache* cache, const arc_kv_step* step, cons
  * their queries and the prefix hold.  The prefix's value scales lie in
  * [2^-32, 2^32], or are 0: its values then count as zeros, and so they do under
  * one below 2^-60.  Scales that are negative, NaN or above 2^32 set
- * ARC_KV_ERR_SCALE and make the rows of their head NaN.
+ * ARC_KV_ERR_SCALE and make the rows of their head NaN.  A row whose scores with
+ * the prefix, scale * q . k * log2(e), reach 2^22 in magnitude may be NaN, and is
+ * where its largest one does; arc_kv_attend takes any.
  * Weights enter the products with the prefix as fp16, 64 tokens at a time, all
  * of pages whose value scales lie within a factor of 16: off by 2^-11 of
  * themselves at most above 2^-12 of the largest of the 64, by 2^-23 of that one
