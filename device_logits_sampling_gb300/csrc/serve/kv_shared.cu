@@ -109,8 +109,8 @@ __host__ __device__ inline int64_t cut_of(int64_t total, int64_t i, int64_t of) 
 
 struct __align__(16) Info {  // a tile
     int32_t tokens;
-    int32_t flags;    // 1: the last of its unit's, 2: the last of all, 4: another reference than the tile before's;
-                      // from bit 8 on the pages whose values count as zeros
+    int32_t flags;    // 1: the last of its unit's, 2: the last of all, 4: another reference than the tile before's, 8: its
+                      // values count as zeros
     float value;      // the reference of the value scales,
     float value_log;  // its logarithm
     float key[8];     // of each 16 tokens: key scale,
@@ -331,21 +331,20 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                     key = __int_as_float(0x7FC00000);
                     val = 1.0f;
                 }
-                // a page of zeros goes with any reference
-                const bool none = val < kLeast;
+                const bool none = val < kLeast;  // pages of zeros, a tile of their own, go with any reference
                 const uint32_t nones = __ballot_sync(0xFFFFFFFFu, none);
                 const int64_t at = (good ? id : 0) * a.c.page_stride + now.head * a.c.head_stride + int64_t{offset} * D;
                 const bool ends_all = next.c == to, unit_ends = next.chunk == 0 || ends_all;
                 for (int start = 0; ok && start < n; ++t) {
                     // the pages from `start` on whose scales go with the reference, or with one another
-                    bool apart = lane > start && lane < n && !none;
+                    bool apart = lane > start && lane < n;
+                    const bool none0 = nones >> start & 1;
                     const float v0 = __shfl_sync(0xFFFFFFFFu, val, start);
-                    const bool stays = v0 < kLeast ? value > 0.0f : v0 <= value && v0 * kSpread >= value;
+                    const bool stays = none0 ? value > 0.0f : v0 <= value && v0 * kSpread >= value;
                     if (stays) {
-                        apart = apart && !(val <= value && val * kSpread >= value);
+                        apart = apart && (none != none0 || (!none0 && !(val <= value && val * kSpread >= value)));
                     } else {
-                        const bool counts = lane >= start && lane < n && !none;
-                        float hi = counts ? val : 0.0f, lo = counts ? val : kMost;
+                        float hi = lane >= start && lane < n ? val : 0.0f, lo = hi;
 #pragma unroll
                         for (int m = 1; m < 8; m <<= 1) {
                             const float h = __shfl_up_sync(0xFFFFFFFFu, hi, m), l = __shfl_up_sync(0xFFFFFFFFu, lo, m);
@@ -354,10 +353,10 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                                 lo = fminf(lo, l);
                             }
                         }
-                        apart = apart && hi > kSpread * lo;
+                        apart = apart && (none != none0 || (!none0 && hi > kSpread * lo));
                         const uint32_t ends = __ballot_sync(0xFFFFFFFFu, apart);
                         value = __shfl_sync(0xFFFFFFFFu, hi, ends ? __ffs(ends) - 2 : n - 1);
-                        if (value == 0.0f) value = 1.0f;  // zeros alone
+                        if (none0) value = 1.0f;
                     }
                     const uint32_t ends = __ballot_sync(0xFFFFFFFFu, apart);
                     const int end = ends ? __ffs(ends) - 1 : n;
@@ -368,15 +367,14 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
                     const float k16 = __shfl_sync(0xFFFFFFFFu, key, page & 31), v16 = __shfl_sync(0xFFFFFFFFu, val, page & 31);
                     if (lane < X::kGranules) {
                         const bool there = page < end;
-                        const float lift = kLift + (v16 == value || v16 < kLeast ? 0.0f : __log2f(v16 / value));
+                        const float lift = kLift + (v16 == value || none0 ? 0.0f : __log2f(v16 / value));
                         info.key[lane] = there ? k16 : 0.0f;
                         info.lift[lane] = there ? lift : -kAlone;
                         info.back[lane] = there ? ex2(-lift) : 0.0f;
                     }
                     if (lane == 0) {
                         info.tokens = (end - start) << span_shift;
-                        info.flags = (end == n && unit_ends ? (ends_all ? 3 : 1) : 0) | (stays ? 0 : 4) |
-                                     (nones >> start & ((1u << (end - start)) - 1)) << 8;
+                        info.flags = (end == n && unit_ends ? (ends_all ? 3 : 1) : 0) | (stays ? 0 : 4) | (none0 ? 8 : 0);
                         info.value = value;
                         info.value_log = __log2f(value);
                     }
@@ -409,19 +407,13 @@ __global__ void __launch_bounds__(512, 1) prefix_kernel(const __grid_constant__ 
         uint4 k[N], v[N];
         auto load = [&](uint32_t t, const void* from, bool values, uint4 (&x)[N]) {
             const Info& info = bars.info[t % kInfos];
-            const int tokens = info.tokens;
-            const uint32_t zeros = values ? static_cast<uint32_t>(info.flags) >> 8 : 0;
+            const int tokens = values && (info.flags & 8) ? 0 : info.tokens;
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const int token = token_of(j), chunk = chunk_of(j);
                 const int64_t at = token < tokens ? info.at[token >> shift] : -1;
                 x[j] = at < 0 ? make_uint4(0, 0, 0, 0)
                               : load_past_l1(static_cast<const char*>(from) + at + (token & (span - 1)) * D + chunk * 16);
-            }
-            if (zeros) {
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (zeros >> (token_of(j) >> shift) & 1) x[j] = make_uint4(0, 0, 0, 0);
             }
         };
         uint32_t os = 0, phase = 1;
