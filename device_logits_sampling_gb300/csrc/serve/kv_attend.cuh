@@ -34,13 +34,12 @@
 // 1 and summed up across steps by the matrix instruction, lost what lay below
 // 2^-25 of the largest, which a page of a far larger scale made of all others.
 //
-// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 282 us,
-// 6.6 TB/s, 97% of the measured copy rate (278 us with the products summed up by
-// the matrix instruction): the 12 warps of an SM need some 2,000 clocks a step,
-// which is what memory gives them 4 KB in.  One sequence of 200,003: 74 us (81%);
-// 256 of 1 to 4,096: 65 us (67%): the line's ends, about 12,000 clocks to the first
-// step and as many for the joins.  Short calls are those: 14 us.  48 sequences of 1
-// to 5 drafted tokens, heads of 64, a window: 36 us.  Measured and left: a block for
+// Bounds and figures.  64 sequences of 4,096 to 32,768 tokens (1.85 GB): 278 us,
+// 6.6 TB/s, 98% of the measured copy rate: the 12 warps of an SM need some 2,000
+// clocks a step, which is what memory gives them 4 KB in.  One sequence of 200,003: 73 us (83%);
+// 256 of 1 to 4,096: 64 us (68%): the line's ends, about 12,000 clocks to the first
+// step and as many for the joins.  Short calls are those: 13 us.  48 sequences of 1
+// to 5 drafted tokens, heads of 64, a window: 34 us.  Measured and left: a block for
 // each (sequence, head) and one token at a time a warp (157 ms for the 200,003),
 // more warps with fewer registers and stages (95 us for it), joins row by row in
 // every thread (84 us).

@@ -1,9 +1,9 @@
 // arc_kv_attend_shared: attention of a step's new tokens behind a prefix that all sequences share.
 //
-// Three kernels, the first two side by side where there are SMs for both.  The prefix: all rows of a cached head (new
-// tokens times its query heads) against the prefix's pages, which are read once for them.  The sequences' own tokens:
-// kv_attend.cuh's kernel, with its results in fp32.  And the join of a row's parts, each an output with the base-2
-// logarithm of its sum of weights:
+// Three kernels, the first two side by side where the first leaves SMs free, else one after the other.  The prefix: all
+// rows of a cached head (new tokens times its query heads) against the prefix's pages, which are read once for them.  The
+// sequences' own tokens: kv_attend.cuh's kernel, with its results in fp32.  And the join of a row's parts, each an output
+// with the base-2 logarithm of its sum of weights:
 //     out = sum_i 2^(log_i - max) out_i / sum_i 2^(log_i - max).
 //
 // The prefix.  A unit is a cached head and up to 256 rows (128 for heads of 256).  A chunk is 128 tokens (64 for heads
@@ -29,14 +29,15 @@
 //
 // Every wait has a limit; a block whose wait runs out leaves NaN.
 //
-// Bounds and figures.  256 sequences behind 16,384 tokens, 64 + 8 heads of 128 (137 GFLOP): the prefix 145 us, 950
-// TFLOP/s, 50% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what
+// Bounds and figures.  256 sequences behind 16,384 tokens, 64 + 8 heads of 128 (137 GFLOP): the prefix about 147 us, 930
+// TFLOP/s, 49% of the measured bf16 rate; a step of 64 tokens takes some 2,500 clocks, the products alone 1,262: what
 // is left are the latencies of the softmax's steps (barrier, scores, maximum, exponentials, barrier), which two warps a
-// scheduler do not hide.  64 behind 32,768, 32 + 8 heads: 45 us of 76 in all.  Few rows: latency, 19 us for the three
-// kernels, 28 one after another.  Measured and left, the prefix of the first case: output read back and added up in
-// registers each tile 252 us; steps of 128 tokens, one ahead 169; weights made before the maximum is known and again
-// where the reference moves 186 to 255; one thread for all products 161; loops over a step's scores unrolled further
-// 10% to 30% slower each time.
+// scheduler do not hide.  64 behind 32,768, 32 + 8 heads: 45 us of 76 in all.  Few rows: latency, 20 us for the three
+// kernels, 28 one after another.  Value scales between 2^-12 and 2^-4 on pages of 32, where references move and chunks
+// are split: 360 us for the first case's 196 in all.  Measured and left, the prefix of the first case: output read back
+// and added up in registers each tile 252 us; steps of 128 tokens, one ahead 169; weights made before the maximum is known
+// and again where the reference moves 186 to 255; one thread for all products 161; loops over a step's scores unrolled
+// further 10% to 30% slower each time.
 #include "kv_shared.cuh"
 
 #include <atomic>

@@ -6,10 +6,10 @@
 // are one byte of the mask, one byte of marks and 16 bytes of 16-bit logits.  Eight disallowed ids are written without
 // being read; in place, eight that are allowed and unmarked are not touched at all.
 //
-// Bounds and figures.  A mask alone, in place, 100 x 100,003 fp32: 10.0 us, faster than its 81 MB at the measured copy
+// Bounds and figures.  A mask alone, in place, 100 x 100,003 fp32: 9.2 us, faster than its 81 MB at the measured copy
 // rate (12.1), since what it takes out is not read.  256 rows x 129,280 with histories of up to 4,096 ids, up to 300
 // biases and masks: 47 us (20.5 of traffic): instructions, 70% of the issue slots; every block of a row goes through the
-// row's lists.  One row 5.0 us: four loads that wait for one another.  Measured and left: all eight ids of a marked group
+// row's lists.  One row 4.4 us: four loads that wait for one another.  Measured and left: all eight ids of a marked group
 // looked up with its store (56 us), a second kernel with a hash table a row that edits behind the stream (54, and 12 for
 // one row), edits by whoever takes an id's word out of the table (66 to 80), counts and entries in one word (73).
 //
@@ -269,9 +269,9 @@ int launch(const EditArgs& a, int dev, cudaStream_t st) {
 
 template <int DT, int OT>
 int launch(const EditArgs& a, int dev, cudaStream_t st) {
-    // Two groups a thread where there are lists (before the marks' loop: 256 rows x 129,280 55.9 us, 68.1 with one, 76.8
-    // with four; 32 rows 11.7, 13.1, 15.4; 512 rows 96, 115, 137).  Few rows want more blocks: one row 5.8 us with one,
-    // 7.5 with two; 8 rows 7.8 and 9.5; 16 rows 7.5 and 7.8.  Without lists the numbers lie within 4%.
+    // Two groups a thread where there are lists (256 rows x 129,280 46.6 us, 57.2 with one; 512 rows 90 and 111; 32 rows 9.5
+    // and 10.5; 64 x 50,003 9.3 and 10.1).  Few rows want more blocks: one row 5.4 us with one, 6.0 with two; 8 rows 6.0 and
+    // 7.0; 16 rows 7.0 and 7.6; 20 rows 8.3 and 7.6, 24 rows 7.8 and 8.3.  Without lists the numbers lie within 4%.
     if (a.e.hist_offsets || a.e.bias_offsets)
         return a.B * a.V <= (5 << 19) ? launch<DT, OT, true, 1>(a, dev, st) : launch<DT, OT, true, 2>(a, dev, st);
     return launch<DT, OT, false, 1>(a, dev, st);

@@ -6,7 +6,7 @@
 // Many long rows go through rings in shared memory (join_rows_kernel).
 //
 // Bounds and figures.  HBM: 8,191 rows of 5,120 with a 32-bit stream, gates and a post norm, 587 MB: 105 us, 84% of the
-// measured copy rate; 16 bits without gates 55 us, 90%; 60,000 x 512 56 us, 98%.  One row 4.1 us: two sums that wait for
+// measured copy rate; 16 bits without gates 55 us, 90%; 60,000 x 512 56 us, 98%.  One row 2.9 us: two sums that wait for
 // loads.  Odd rows: 4,000 x 5,003 61 us, 39%, 236 value by value: the weights do not begin as the rows do.
 #pragma once
 
