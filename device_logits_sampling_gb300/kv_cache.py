@@ -76,7 +76,6 @@ class PagedCache:
         want(n > 0, "arc_kv_attend_workspace_bytes rejected the cache")
         return serve.new_workspace(self.k, n, True, stream)
 
-
     def shared_workspace(self, tokens: int, q_heads: int, stream=None):
         """Zero-filled workspace for `attend_shared` of up to so many new tokens over caches of this shape (one per
         stream that uses it), made on the stream given, else on the current one."""
@@ -255,7 +254,9 @@ def attend_shared(cache: PagedCache, q, positions, page_table, prefix, out=None,
                   scale: float | None = None, err_word=None, workspace=None, stream=None, check: bool = True):
     """arc_kv_attend_shared: `attend` for sequences that all begin with the same tokens, whose whole pages `prefix`
     int32 [pages] names: they are read once for the batch.  page_table keeps a sequence's pages in their places; the
-    entries under the prefix are not read.  Every sequence's position lies at or past the prefix's end.  workspace:
+    entries under the prefix are not read.  Every sequence's position lies at or past the prefix's end.  The prefix's scales
+    lie in [2^-32, 2^32], value scales may be 0 too (others set ARC_KV_ERR_SCALE), and scale * q . k * log2(e) below 2^22
+    (rows beyond may be NaN).  workspace:
     cache.shared_workspace(tokens, q_heads), made for the call where None.  Returns out.  stream: as in `attend`."""
     T, dim, dev = q.shape[0], cache.head_dim, cache.index
     qt, qh, heads = _heads(q, T, None, dim, "q")

@@ -1,7 +1,7 @@
 """Binding of libarcserve.so (include/serve/): loading, error codes, structs.
 
-The operators of a decode step before the sampler live in kv_cache.py and
-w4.py; every step of them runs in the library's CUDA kernels.  There is no
+The operators of a decode step before the sampler live in kv_cache.py, w4.py,
+norm.py and edit.py; every step of them runs in the library's CUDA kernels.  There is no
 fallback: if the library is not built, `load()` raises.
 """
 from __future__ import annotations
