@@ -255,9 +255,9 @@ def attend_shared(cache: PagedCache, q, positions, page_table, prefix, out=None,
     """arc_kv_attend_shared: `attend` for sequences that all begin with the same tokens, whose whole pages `prefix`
     int32 [pages] names: they are read once for the batch.  page_table keeps a sequence's pages in their places; the
     entries under the prefix are not read.  Every sequence's position lies at or past the prefix's end.  The prefix's scales
-    lie in [2^-32, 2^32], value scales may be 0 too (others set ARC_KV_ERR_SCALE), and scale * q . k * log2(e) below 2^22
-    (rows beyond may be NaN).  workspace:
-    cache.shared_workspace(tokens, q_heads), made for the call where None.  Returns out.  stream: as in `attend`."""
+    lie in [2^-32, 2^32] (negative, NaN and larger ones set ARC_KV_ERR_SCALE) or, those of values, are 0; scale * q . k *
+    log2(e) lies below 2^22 (rows beyond may be NaN).  workspace: cache.shared_workspace(tokens, q_heads), made for the call
+    where None.  Returns out.  stream: as in `attend`."""
     T, dim, dev = q.shape[0], cache.head_dim, cache.index
     qt, qh, heads = _heads(q, T, None, dim, "q")
     code = serve.dtype_code(q)

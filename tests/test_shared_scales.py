@@ -1,5 +1,5 @@
-"""Value scales of a shared prefix's pages that append does not write: 0 and less than 2^-60 count as zeros, as they do to
-the last bit of what attend gives; negative, NaN and too large ones, of keys or values, are reported and spoil the rows."""
+"""Scales of a shared prefix's pages that append does not write: under value scales of 0 and below 2^-60 the values count as
+zeros; negative, NaN and too large scales, of keys or values, are reported and spoil their head's rows."""
 import numpy as np
 import pytest
 
